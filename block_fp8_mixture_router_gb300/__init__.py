@@ -43,7 +43,13 @@ EXPORTED = ("moe_create", "moe_load_weights", "moe_forward", "moe_forward_host",
             "moe_last_device_status", "moe_destroy", "moe_status_string",
             "moe_profile_forward", "moe_route_static", "moe_add_rmsnorm_quantize",
             "moe_forward_codes", "moe_forward_addnorm", "moe_chain_create",
-            "moe_chain_forward", "moe_chain_destroy", "moe_debug_poison_workspace")
+            "moe_chain_forward", "moe_chain_destroy", "moe_debug_poison_workspace",
+            "moe_attn_required_bytes", "moe_attn_create", "moe_rope", "moe_kv_append",
+            "moe_attn_forward", "moe_attn_step", "moe_attn_last_device_status",
+            "moe_attn_destroy")
+
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BY_PARTS = 0, 1, 2
 
 MOE_ROUTE_STATIC_MAX_LOGITS = 262144
 
@@ -58,6 +64,30 @@ class moe_config(ctypes.Structure):
 class moe_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("w13", "s13", "w2", "s2", "router", "ws13", "ws2", "shared_gate")]
+
+
+class moe_attn_config(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in
+                 ("q_heads", "kv_heads", "head_dim", "page_tokens", "rotary_dim", "rope_layout",
+                  "rope_scaling", "rope_trained_positions")] +
+                [(n, ctypes.c_double) for n in
+                 ("rope_base", "rope_factor", "rope_turns_low", "rope_turns_high",
+                  "rope_amplitude", "softmax_scale")] +
+                [(n, ctypes.c_int) for n in ("window", "max_rows", "max_seqs")] +
+                [("workspace_cap_bytes", ctypes.c_size_t)])
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int)]
+
+
+class moe_attn_batch(ctypes.Structure):
+    _fields_ = [("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p)] + [
+                    (n, ctypes.c_int) for n in
+                    ("n_seqs", "pages_stride", "rows", "max_seq_rows", "max_kv_len")]
 
 
 class MoEError(RuntimeError):
@@ -104,8 +134,21 @@ def load_library(path: str = LIB_PATH):
     L.moe_destroy.restype = None
     L.moe_status_string.argtypes = [i]
     L.moe_status_string.restype = ctypes.c_char_p
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    kvp, bp = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_attn_batch)
+    L.moe_attn_required_bytes.argtypes = [ctypes.POINTER(moe_attn_config),
+                                          ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_attn_create.argtypes = [ctypes.POINTER(moe_attn_config), i, ip]
+    L.moe_rope.argtypes = [vp, vp, i64, i, vp, vp, f32, i, vp, i64, vp]
+    L.moe_kv_append.argtypes = [vp, kvp, vp, i64, vp, i64, bp, vp]
+    L.moe_attn_forward.argtypes = [vp, kvp, vp, i64, bp, vp, i64, vp]
+    L.moe_attn_step.argtypes = [vp, kvp, vp, i64, vp, vp, f32, bp, vp, i64, vp]
+    L.moe_attn_last_device_status.argtypes = [vp]
+    L.moe_attn_destroy.argtypes = [vp]
+    L.moe_attn_destroy.restype = None
     for n in EXPORTED:
-        if n not in ("moe_destroy", "moe_status_string", "moe_chain_destroy"):
+        if n not in ("moe_destroy", "moe_status_string", "moe_chain_destroy",
+                     "moe_attn_destroy"):
             getattr(L, n).restype = ctypes.c_int
     _lib = L
     return L
@@ -223,6 +266,51 @@ def moe_profile_forward(ctx, x, y, rows: int, stream=None, capacity: int = 16):
                                             ctypes.cast(names, ctypes.c_void_p), capacity,
                                             ctypes.byref(n), _stream(stream))
     return rc, [(names[i].decode(), float(ms[i])) for i in range(n.value)]
+
+
+def moe_attn_required_bytes(cfg: moe_attn_config):
+    n = ctypes.c_size_t()
+    rc = load_library().moe_attn_required_bytes(ctypes.byref(cfg), ctypes.byref(n))
+    return rc, n.value
+
+
+def moe_attn_create(cfg: moe_attn_config, device: int = 0):
+    h = ctypes.c_void_p()
+    rc = load_library().moe_attn_create(ctypes.byref(cfg), device, ctypes.byref(h))
+    return rc, h
+
+
+def moe_rope(ctx, x, x_stride: int, heads: int, positions, gamma, eps: float, rows: int, y,
+             y_stride: int, stream=None) -> int:
+    return load_library().moe_rope(ctx, _ptr(x), x_stride, heads, _ptr(positions), _ptr(gamma),
+                                   eps, rows, _ptr(y), y_stride, _stream(stream))
+
+
+def moe_kv_append(ctx, cache, k, k_stride: int, v, v_stride: int, batch, stream=None) -> int:
+    """cache: a moe_kv_cache, batch: a moe_attn_batch (each may be None)."""
+    return load_library().moe_kv_append(ctx, cache, _ptr(k), k_stride, _ptr(v), v_stride, batch,
+                                        _stream(stream))
+
+
+def moe_attn_forward(ctx, cache, q, q_stride: int, batch, out, out_stride: int,
+                     stream=None) -> int:
+    return load_library().moe_attn_forward(ctx, cache, _ptr(q), q_stride, batch, _ptr(out),
+                                           out_stride, _stream(stream))
+
+
+def moe_attn_step(ctx, cache, qkv, qkv_stride: int, q_gamma, k_gamma, eps: float, batch, out,
+                  out_stride: int, stream=None) -> int:
+    return load_library().moe_attn_step(ctx, cache, _ptr(qkv), qkv_stride, _ptr(q_gamma),
+                                        _ptr(k_gamma), eps, batch, _ptr(out), out_stride,
+                                        _stream(stream))
+
+
+def moe_attn_last_device_status(ctx) -> int:
+    return load_library().moe_attn_last_device_status(ctx)
+
+
+def moe_attn_destroy(ctx) -> None:
+    load_library().moe_attn_destroy(ctx)
 
 
 def moe_set_option(ctx, option: int, value: int) -> int:
@@ -429,3 +517,210 @@ class MoEChain:
                                 device=x.device)
         _check(moe_chain_forward(self.chain, x, y_all, x.shape[0], stream), "moe_chain_forward")
         return y_all
+
+
+# ---- attention over an 8-bit paged cache -----------------------------------
+
+_ROPE_LAYOUTS = {"half": MOE_ROPE_HALF, "interleaved": MOE_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"plain": MOE_ROPE_PLAIN, "linear": MOE_ROPE_LINEAR,
+                  "by_parts": MOE_ROPE_BY_PARTS}
+
+
+@dataclass
+class AttnShape:
+    """An attention layer's shape (moe_attn_config in include/moe.h)."""
+    q_heads: int = 16
+    kv_heads: int = 2
+    head_dim: int = 128
+    page_tokens: int = 64
+    rotary_dim: int = 128
+    rope_layout: str = "half"        # half | interleaved
+    rope_base: float = 10000.0
+    rope_scaling: str = "plain"      # plain | linear | by_parts
+    rope_factor: float = 1.0
+    rope_trained_positions: int = 0
+    rope_turns_low: float = 0.0
+    rope_turns_high: float = 0.0
+    rope_amplitude: float = 1.0
+    softmax_scale: float = 0.0       # 0: 1 / sqrt(head_dim)
+    window: int = 0                  # 0: all earlier positions
+
+    def config(self, max_rows: int, max_seqs: int, workspace_cap_bytes: int = 0):
+        if self.rope_layout not in _ROPE_LAYOUTS or self.rope_scaling not in _ROPE_SCALINGS:
+            raise ValueError("unknown rope_layout or rope_scaling")
+        return moe_attn_config(
+            self.q_heads, self.kv_heads, self.head_dim, self.page_tokens, self.rotary_dim,
+            _ROPE_LAYOUTS[self.rope_layout], _ROPE_SCALINGS[self.rope_scaling],
+            self.rope_trained_positions, self.rope_base, self.rope_factor, self.rope_turns_low,
+            self.rope_turns_high, self.rope_amplitude, self.softmax_scale, self.window, max_rows,
+            max_seqs, workspace_cap_bytes)
+
+
+class KVCache:
+    """One layer's paged cache: e4m3 codes [pages][kv_heads][page_tokens][head_dim]
+    (uint8) and fp32 scales [pages][kv_heads], for keys and for values."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        for t, kind, dims in ((k_codes, torch.uint8, 4), (v_codes, torch.uint8, 4),
+                              (k_scales, torch.float32, 2), (v_scales, torch.float32, 2)):
+            if t.dtype != kind or not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
+                raise ValueError("codes must be contiguous 4-D uint8 and scales contiguous 2-D "
+                                 "fp32 CUDA tensors")
+        if k_codes.shape != v_codes.shape or k_scales.shape != v_scales.shape or \
+                k_scales.shape != k_codes.shape[:2]:
+            raise ValueError("keys and values, codes and scales must agree in shape")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = \
+            k_codes, v_codes, k_scales, v_scales
+        self._c = moe_kv_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                               v_scales.data_ptr(), k_codes.shape[0])
+
+    @classmethod
+    def empty(cls, shape: AttnShape, n_pages: int, device="cuda"):
+        """A cache of unwritten pages."""
+        def codes():
+            return torch.empty((n_pages, shape.kv_heads, shape.page_tokens, shape.head_dim),
+                               dtype=torch.uint8, device=device)
+
+        def scales():
+            return torch.empty((n_pages, shape.kv_heads), dtype=torch.float32, device=device)
+        return cls(codes(), codes(), scales(), scales())
+
+
+class AttnBatch:
+    """The rows of one call (moe_attn_batch): int32 CUDA tensors row_start
+    [n_seqs + 1], kv_len [n_seqs] (with this call's rows) and pages [n_seqs][most pages].
+    Their contents may change from call to call (a captured graph replays with new
+    lengths); max_seq_rows and max_kv_len bound them for the launch's sake."""
+
+    def __init__(self, row_start, kv_len, pages, rows: int, max_seq_rows: int = 0,
+                 max_kv_len: int = 0):
+        for t, dims in ((row_start, 1), (kv_len, 1), (pages, 2)):
+            if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims or \
+                    not t.is_contiguous():
+                raise ValueError("row_start, kv_len and pages must be contiguous int32 CUDA "
+                                 "tensors of 1, 1 and 2 dimensions")
+        n = kv_len.shape[0]
+        if row_start.shape[0] != n + 1 or pages.shape[0] != n:
+            raise ValueError("row_start has one entry more than kv_len, pages one row for each")
+        self.row_start, self.kv_len, self.pages, self.rows = row_start, kv_len, pages, rows
+        self._c = moe_attn_batch(row_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), n,
+                                 pages.shape[1], rows, max_seq_rows, max_kv_len)
+
+
+def _rows3(t: torch.Tensor, heads: int, dim: int, what: str) -> int:
+    """Row stride of a [rows, heads, dim] bf16 CUDA tensor whose heads lie side by side."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{what} must be a 3-D bf16 CUDA tensor")
+    rows, h, d = t.shape
+    if h != heads or d != dim:
+        raise ValueError(f"{what} must be [rows, {heads}, {dim}], not {tuple(t.shape)}")
+    sr, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != dim):
+        raise ValueError(f"{what}: the heads of a row must lie side by side")
+    return sr if rows > 1 else heads * dim
+
+
+class Attention:
+    """The attention of one layer shape on one GPU: owns a context and its workspace."""
+
+    def __init__(self, shape: AttnShape, max_rows: int = 1024, max_seqs: int = 1,
+                 device: int = 0, workspace_cap_bytes: int = 0):
+        self.shape = shape
+        self.device = device
+        rc, h = moe_attn_create(shape.config(max_rows, max_seqs, workspace_cap_bytes), device)
+        _check(rc, "moe_attn_create")
+        self.ctx = h
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            moe_attn_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _cache_ok(self, cache: KVCache):
+        s = self.shape
+        if tuple(cache.k_codes.shape[1:]) != (s.kv_heads, s.page_tokens, s.head_dim):
+            raise ValueError("the cache's pages are not of this shape")
+
+    def _gamma_ok(self, *gammas):
+        for g in gammas:
+            if g is not None and (g.dtype != torch.bfloat16 or not g.is_cuda or
+                                  not g.is_contiguous() or g.shape != (self.shape.head_dim,)):
+                raise ValueError("a gamma must be a contiguous bf16 CUDA tensor [head_dim]")
+
+    def _out(self, out, like, rows):
+        s = self.shape
+        if out is None:
+            out = torch.empty((rows, s.q_heads, s.head_dim), dtype=torch.bfloat16,
+                              device=like.device)
+        return out, _rows3(out, s.q_heads, s.head_dim, "out")
+
+    def rope(self, x: torch.Tensor, positions: torch.Tensor, gamma: torch.Tensor | None = None,
+             eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Rotary positions of x [rows, heads, head_dim] (queries or keys, any number of
+        heads), after an RMS norm of each head where gamma is given; out may be x."""
+        heads = x.shape[1] if x.dim() == 3 else 0
+        xs = _rows3(x, heads, self.shape.head_dim, "x")
+        rows = x.shape[0]
+        if positions.dtype != torch.int32 or not positions.is_cuda or \
+                positions.shape != (rows,) or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 CUDA tensor [rows]")
+        self._gamma_ok(gamma)
+        if out is None:
+            out = torch.empty((rows, heads, self.shape.head_dim), dtype=x.dtype, device=x.device)
+        ys = _rows3(out, heads, self.shape.head_dim, "out")
+        if out.shape[0] != rows:
+            raise ValueError("out must have x's rows")
+        _check(moe_rope(self.ctx, x, xs, heads, positions, gamma, eps, rows, out, ys, stream),
+               "moe_rope")
+        return out
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: AttnBatch,
+               stream=None):
+        """Rows of keys and values [rows, kv_heads, head_dim] into the cache."""
+        s = self.shape
+        ks = _rows3(k, s.kv_heads, s.head_dim, "k")
+        vs = _rows3(v, s.kv_heads, s.head_dim, "v")
+        if k.shape[0] != batch.rows or v.shape[0] != batch.rows:
+            raise ValueError("k and v must have the batch's rows")
+        self._cache_ok(cache)
+        _check(moe_kv_append(self.ctx, cache._c, k, ks, v, vs, batch._c, stream),
+               "moe_kv_append")
+
+    def forward(self, q: torch.Tensor, cache: KVCache, batch: AttnBatch,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of q [rows, q_heads, head_dim] over the cache, which already
+        holds the batch's rows."""
+        s = self.shape
+        qs = _rows3(q, s.q_heads, s.head_dim, "q")
+        out, os_ = self._out(out, q, batch.rows)
+        if q.shape[0] != batch.rows or out.shape[0] != batch.rows:
+            raise ValueError("q and out must have the batch's rows")
+        self._cache_ok(cache)
+        _check(moe_attn_forward(self.ctx, cache._c, q, qs, batch._c, out, os_, stream),
+               "moe_attn_forward")
+        return out
+
+    def step(self, qkv: torch.Tensor, cache: KVCache, batch: AttnBatch,
+             q_gamma: torch.Tensor | None = None, k_gamma: torch.Tensor | None = None,
+             eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The whole attention step from a projection's rows [rows, q_heads + 2 kv_heads,
+        head_dim]: norms and rotates, appends, attends."""
+        s = self.shape
+        xs = _rows3(qkv, s.q_heads + 2 * s.kv_heads, s.head_dim, "qkv")
+        out, os_ = self._out(out, qkv, batch.rows)
+        if qkv.shape[0] != batch.rows or out.shape[0] != batch.rows:
+            raise ValueError("qkv and out must have the batch's rows")
+        self._cache_ok(cache)
+        self._gamma_ok(q_gamma, k_gamma)
+        _check(moe_attn_step(self.ctx, cache._c, qkv, xs, q_gamma, k_gamma, eps, batch._c, out,
+                             os_, stream), "moe_attn_step")
+        return out
+
+    def device_status(self) -> int:
+        return moe_attn_last_device_status(self.ctx)

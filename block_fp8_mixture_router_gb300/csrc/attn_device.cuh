@@ -1,0 +1,98 @@
+// Device helpers of the attention kernels.
+#pragma once
+
+#include "attn_internal.cuh"
+#include "moe_device.cuh"
+
+namespace moe {
+
+// Rows and lengths of one sequence, clamped so that no address taken from them
+// leaves the caller's buffers.
+struct SeqView {
+  int row0;   // first row
+  int n;      // rows
+  int len;    // tokens in the cache
+  int first;  // position of the first row (negative: rows in front of the cache)
+  bool ok;
+};
+
+__device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s) {
+  SeqView v;
+  const int r0 = a.row_start[s], r1 = a.row_start[s + 1], len = a.kv_len[s];
+  const int cap = (int)min((long long)a.pages_stride << a.page_shift, (long long)kAttnMaxTokens);
+  v.row0 = min(max(r0, 0), a.rows);
+  v.n = min(max(r1, v.row0), a.rows) - v.row0;
+  v.len = min(max(len, 0), cap);
+  v.first = v.len - v.n;
+  v.ok = v.row0 == r0 && v.row0 + v.n == r1 && v.len == len;
+  return v;
+}
+
+// The page that holds tokens j << page_shift and on, or -1 where the table
+// names none of the cache's (the caller reports it).
+__device__ __forceinline__ int page_at(const AttnArgs& a, int s, int j) {
+  const int p = a.pages[(size_t)s * a.pages_stride + j];
+  return (unsigned)p < (unsigned)a.n_pages ? p : -1;
+}
+
+// Work units are numbered without a table of prefix sums: sequence s's units
+// begin at row_start[s] / per + extra * s, which leaves room for the
+// rows / per + extra it can need.  Returns the sequence of unit u (all
+// threads of the block call; u is block-uniform) and its first unit.
+__device__ __forceinline__ int unit_seq(const AttnArgs& a, int per, int extra, int u, int* first) {
+  int below = 0;  // sequences s >= 1 whose units begin at or before u
+  for (int b = 1; b < a.n_seqs; b += blockDim.x) {
+    const int s = b + (int)threadIdx.x;
+    const bool in = s < a.n_seqs && min(max(a.row_start[s], 0), a.rows) / per + extra * s <= u;
+    below += __syncthreads_count(in);
+  }
+  *first = min(max(a.row_start[below], 0), a.rows) / per + extra * below;
+  return below;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Cosine and sine (times the amplitude) of pair i at a position.  The angle in
+// turns is the top 32 bits of position x turns[i] modulo 2^64, read as a signed
+// fraction: off by at most 2^-33 of a turn, and its float by 2^-25.
+__device__ __forceinline__ float2 rope_cs(const RopeArgs& r, int i, int pos) {
+  const unsigned long long t = (unsigned long long)(long long)pos * r.turns[i];
+  const float half_turns = (float)(int)(t >> 32) * 0x1p-31f;
+  float sn, cs;
+  sincospif(half_turns, &sn, &cs);
+  return make_float2(cs * r.amp, sn * r.amp);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool is_finite(float x) {
+  return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
+}
+
+// 0x80 in every byte of w that is an e4m3 NaN code (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t e4m3_nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+}  // namespace moe

@@ -1,0 +1,82 @@
+// Declarations shared by the attention kernels and their host code.
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+constexpr int kAttnMaxGroup = 16;     // query heads of one key head
+constexpr int kAttnMaxSeqs = 4096;
+constexpr int kAttnMaxTokens = 0x7FFF0000;  // positions and a tile behind them fit an int
+constexpr int kAttnKeys = 64;         // keys of one step of the decode kernel
+constexpr int kScaleMinExp = -100;    // the smallest block scale is 2^-100
+
+// Device status word bits.
+constexpr int kAttnTimeout = 1;
+constexpr int kAttnBadBatch = 2;
+
+// What every attention kernel knows of the layer, the cache and the batch.
+struct AttnArgs {
+  int Hq, Hkv, g;        // query heads, key heads, query heads of a key head
+  int page_shift;        // page_tokens = 1 << page_shift
+  int window;            // 0 = none
+  float scale;           // softmax scale x log2(e)
+  // cache
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;
+  float* vs;
+  int n_pages;
+  // batch
+  const int* row_start;
+  const int* kv_len;
+  const int* pages;
+  int n_seqs, pages_stride, rows;
+  int* status;
+};
+
+// The rotation of a head: turns per position of each pair as 64-bit fractions
+// of a turn, so that position x entry, taken modulo 2^64, is the exact angle
+// modulo one turn to 2^-65 per position.
+struct RopeArgs {
+  const unsigned long long* turns;  // [rot / 2]
+  int rot;
+  int interleaved;
+  float amp;
+};
+
+// Partial results of a key range that one CTA worked through, merged by the
+// last CTA of a unit to arrive.
+struct AttnSplit {
+  float* o;        // [slots][rows of a tile][D]
+  float2* ml;      // [slots][rows of a tile]: running maximum (log2) and sum
+  int* arrived;    // counters, zero between launches
+};
+
+cudaError_t launch_rope(int D, const bf16* x, int64_t x_stride, int heads, const int* positions,
+                        const bf16* gamma, float eps, int rows, bf16* y, int64_t y_stride,
+                        const RopeArgs& r, int sm_count, cudaStream_t s);
+
+// Append of k and v rows; with `q` the prologue of a step: queries and keys
+// normed and rotated at the batch's positions, the queries written to q_out.
+struct AppendArgs {
+  const bf16* k;
+  const bf16* v;
+  int64_t k_stride, v_stride;
+  const bf16* q;          // nullptr: append only, keys as they are
+  int64_t q_stride;
+  bf16* q_out;            // [rows][Hq][D]
+  const bf16* q_gamma;
+  const bf16* k_gamma;
+  float eps;
+  RopeArgs rope;
+};
+cudaError_t launch_append(int D, const AttnArgs& a, const AppendArgs& p, cudaStream_t s);
+
+cudaError_t setup_attn_decode(int D);
+int attn_decode_slots(int D, int sm_count);  // CTAs of a full grid
+cudaError_t launch_attn_decode(int D, const AttnArgs& a, const bf16* q, int64_t q_stride,
+                               bf16* out, int64_t out_stride, const AttnSplit& sp, int grid,
+                               bool split, bool pdl, cudaStream_t s);
+
+}  // namespace moe

@@ -419,6 +419,182 @@ void moe_chain_destroy(moe_chain* chain);
  * thread owns the context, stream and modules and releases them). */
 void moe_destroy(moe_ctx* ctx);
 
+/* ---- attention over an 8-bit paged cache ------------------------------------
+ *
+ * The other half of a backbone block: the attention whose output the MoE layer's
+ * add-norm takes.  Rotary positions (moe_rope), the append of new keys and
+ * values to a paged e4m3 cache (moe_kv_append), attention over that cache for
+ * prompt chunks, frames and single tokens alike (moe_attn_forward), and the
+ * three from a projection's packed rows (moe_attn_step).
+ *
+ * Shape of an attention layer.  Supported: head_dim 64, 128 or 256;
+ * kv_heads 1..64; q_heads a multiple of kv_heads, at most 16 query heads to a
+ * key head; page_tokens 16, 32, 64 or 128; rotary_dim even, 0..head_dim;
+ * 1 <= max_rows <= 65536; 1 <= max_seqs <= 4096; window >= 0; every double
+ * finite.  Query head j reads key head j / (q_heads / kv_heads).
+ *
+ * Rotation: pair i of a head's first rotary_dim values turns by position x f_i
+ * radians, f_i = rope_base^(-2i/rotary_dim); MOE_ROPE_LINEAR divides every f_i by
+ * rope_factor; MOE_ROPE_BY_PARTS divides only the slow ones: with
+ * t_i = rope_trained_positions x f_i / 2 pi turns over the trained length and
+ * g_i = clamp((t_i - rope_turns_low) / (rope_turns_high - rope_turns_low), 0, 1),
+ * f_i becomes f_i (g_i + (1 - g_i) / rope_factor).  Cosine and sine are
+ * multiplied by rope_amplitude.  The pairs are (i, i + rotary_dim/2)
+ * (MOE_ROPE_HALF) or (2i, 2i + 1) (MOE_ROPE_INTERLEAVED).
+ *
+ * softmax_scale 0 stands for 1/sqrt(head_dim).  window w > 0: a row at position
+ * p sees keys p-w+1..p; 0: all keys up to p. */
+enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 };
+enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_BY_PARTS = 2 };
+typedef struct {
+  int q_heads;
+  int kv_heads;
+  int head_dim;
+  int page_tokens;            /* tokens of a cache page, which share one scale per head */
+  int rotary_dim;
+  int rope_layout;            /* MOE_ROPE_HALF or MOE_ROPE_INTERLEAVED */
+  int rope_scaling;           /* MOE_ROPE_PLAIN, _LINEAR or _BY_PARTS */
+  int rope_trained_positions; /* BY_PARTS */
+  double rope_base;
+  double rope_factor;         /* LINEAR, BY_PARTS: > 0 */
+  double rope_turns_low;      /* BY_PARTS: 0 <= low < high */
+  double rope_turns_high;
+  double rope_amplitude;      /* > 0 */
+  double softmax_scale;       /* >= 0 */
+  int window;
+  int max_rows;               /* most rows of one batch */
+  int max_seqs;               /* most sequences of one batch */
+  size_t workspace_cap_bytes; /* 0 = no cap */
+} moe_attn_config;
+
+/* The cache of one layer, device memory of the caller: n_pages pages, each
+ * [kv_heads][page_tokens][head_dim] e4m3 codes (16-byte aligned), and one fp32
+ * scale per page and head, [n_pages][kv_heads]; a value is code x scale.
+ * moe_kv_append writes powers of two; a cache that other code filled may hold
+ * any finite positive scales. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int n_pages;
+} moe_kv_cache;
+
+/* The rows of one call, device arrays of the caller.  Sequence s has rows
+ * row_start[s] .. row_start[s+1]-1 (ascending, row_start[0] = 0,
+ * row_start[n_seqs] = rows; a sequence may have none) and kv_len[s] tokens in the
+ * cache once this call's rows are in it: its i-th row of n stands at position
+ * kv_len[s] - n + i.  pages[s * pages_stride + j] is the page that holds tokens
+ * j * page_tokens and on; entries behind the last token are not read.
+ * max_seq_rows and max_kv_len: no sequence has more rows or tokens.  They size
+ * the launch only: larger values in the arrays are handled, more slowly.
+ * A page number outside the cache, a length outside 0..pages_stride *
+ * page_tokens or a descending row_start touches no memory outside the buffers;
+ * results of that sequence are then undefined, and
+ * moe_attn_last_device_status returns MOE_ERR_INVALID_ARG. */
+typedef struct {
+  const int32_t* row_start;
+  const int32_t* kv_len;
+  const int32_t* pages;
+  int n_seqs;
+  int pages_stride;
+  int rows;
+  int max_seq_rows;
+  int max_kv_len;
+} moe_attn_batch;
+
+/* Bytes moe_attn_create would allocate for `cfg`.
+ * Defined by: PR #925 "drama: load the checkpoint with direct I/O in file
+ * order and build the codec on its own thread", conversation, the
+ * allocation-cap commit (an engine admits a model against a memory budget). */
+int moe_attn_required_bytes(const moe_attn_config* cfg, size_t* bytes);
+
+/* Validate `cfg`, tabulate the rotation, allocate the workspace.  Refusals and
+ * ownership as in moe_create.  Synchronous.  A context is used by one stream at a
+ * time; it holds no cache and no weights, so layers of one shape that run one
+ * after the other can share it.
+ * Defined by: commit "the Drama 3 text backbone on CUDA" (gated full attention
+ * with Q/K norm and partial rotary positions beside each MoE layer). */
+typedef struct moe_attn moe_attn;
+int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out);
+
+/* Rotary positions of query or key heads, after an optional RMS norm of each
+ * head: y[r][h] = R(positions[r]) (x[r][h] * gamma / sqrt(mean(x^2) + eps)),
+ * fp32 math, one rounding to bf16; values behind rotary_dim pass unrotated.
+ * x, y bf16 [rows][heads][head_dim] with row strides of x_stride and y_stride
+ * values (multiples of 8, at least heads * head_dim); positions int32 [rows],
+ * any value; gamma bf16 [head_dim] or NULL for no norm; all device pointers,
+ * x, y and gamma 16-byte aligned.  y may be x with the same stride (in place);
+ * no other overlap (MOE_ERR_INVALID_ARG).  1 <= heads <= 1024; rows is not
+ * bounded by max_rows; rows == 0 does nothing.  Angles are exact fractions of a
+ * turn in 64-bit fixed point, so far positions lose nothing.  Asynchronous.
+ * Defined by: commit "the Drama 3 text backbone on CUDA" (Q/K norm, partial
+ * rotary positions in the half layout); the interleaved layout and the scaled
+ * frequencies are this library's. */
+int moe_rope(moe_attn* ctx, const void* x, int64_t x_stride, int heads, const int32_t* positions,
+             const void* gamma, float eps, int rows, void* y, int64_t y_stride, void* stream);
+
+/* Append rows of keys and values (already rotated) to the cache: k and v bf16
+ * [rows][kv_heads][head_dim] with a row stride of k_stride and v_stride values
+ * (multiples of 8), 16-byte aligned.  For each page and head that the rows
+ * reach, separately for K and V:
+ *   scale = the smallest 2^j >= amax / 448 (j >= -100), amax over the call's
+ *           finite rows in the page, but not below the old scale where tokens of
+ *           earlier calls stand in the page;
+ *   codes = e4m3(x / scale), nearest even.  Where a scale grows, the page's
+ *           older codes are rounded to it again: exact for powers of two but at
+ *           the subnormal end of e4m3 (below scale / 64).
+ * A (token, head) row that holds an infinity or NaN is stored as NaN codes.  What
+ * an unwritten or a reused page held before is never read.  Asynchronous.
+ * Sequences of one call must not share the pages that the call writes to.
+ * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA
+ * GPU", section "Precision" (e4m3 rounding); the cache held in 8 bits is this
+ * library's. */
+int moe_kv_append(moe_attn* ctx, const moe_kv_cache* cache, const void* k, int64_t k_stride,
+                  const void* v, int64_t v_stride, const moe_attn_batch* batch, void* stream);
+
+/* Attention of the batch's rows over the cache, which already holds them:
+ * out[r][h] = sum_j softmax_j(softmax_scale q[r][h] . k_j) v_j over the keys j
+ * that the row sees (see moe_attn_batch and window); a row at a negative
+ * position sees none and gets zeros.  q and out bf16 [rows][q_heads][head_dim]
+ * with row strides in values (multiples of 8), 16-byte aligned, not overlapping.
+ * A row that sees a NaN key or value, or holds one itself, is NaN; unseen tokens
+ * reach no row, whatever they hold.  The softmax and every sum run in fp32; the
+ * queries are taken to 2^-17 of the head's largest value, the weights to 11 bits.  Results are bitwise identical from run to run.  Asynchronous.
+ * Defined by: commit "the Drama 3 text backbone on CUDA" (full attention with
+ * shared key heads, for prompts and single tokens); the cache held in 8 bits is
+ * this library's. */
+int moe_attn_forward(moe_attn* ctx, const moe_kv_cache* cache, const void* q, int64_t q_stride,
+                     const moe_attn_batch* batch, void* out, int64_t out_stride, void* stream);
+
+/* The whole attention step from the projection's rows: qkv bf16 [rows][q_heads +
+ * 2 kv_heads][head_dim] (queries, keys, values; row stride in values).  Queries
+ * and keys are normed (q_gamma, k_gamma bf16 [head_dim], each NULL for no norm),
+ * rotated at the batch's positions and rounded to bf16; keys and values go to the
+ * cache; out as in moe_attn_forward.  Bit for bit moe_rope on the queries and on
+ * the keys, moe_kv_append and moe_attn_forward, with the first three in one
+ * launch.  Asynchronous.
+ * Defined by: commit "the Drama 3 text backbone on CUDA" and PR #925 "drama: load
+ * the checkpoint with direct I/O in file order and build the codec on its own
+ * thread", commit list (one prologue launch norms, rotates and caches a row). */
+int moe_attn_step(moe_attn* ctx, const moe_kv_cache* cache, const void* qkv, int64_t qkv_stride,
+                  const void* q_gamma, const void* k_gamma, float eps,
+                  const moe_attn_batch* batch, void* out, int64_t out_stride, void* stream);
+
+/* Device-side status of the context: MOE_OK; MOE_ERR_INVALID_ARG if a batch held
+ * a page, length or row start out of range; MOE_ERR_DEVICE_TIMEOUT if a bounded
+ * wait gave up.  Synchronises the context's last stream and clears the flag.
+ * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA
+ * GPU", conversation, the follow-up fixes (a bad value is refused by name with
+ * an error, not trapped on). */
+int moe_attn_last_device_status(moe_attn* ctx);
+
+/* Release everything the context owns.  NULL is accepted.
+ * Defined by: PR #925 "drama: load the checkpoint with direct I/O in file
+ * order and build the codec on its own thread", conversation (the worker
+ * thread that owns the modules releases them). */
+void moe_attn_destroy(moe_attn* ctx);
+
 /* Static text for a status code.
  * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA
  * GPU", conversation, the follow-up fixes (errors refused by name). */
