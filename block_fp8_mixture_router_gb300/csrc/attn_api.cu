@@ -3,9 +3,12 @@
 // Conventions as in moe_api.cu: unsupported shapes are refused when the context
 // is created, sizes are checked against the cap before anything is allocated,
 // and every refusal is a status code.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -181,6 +184,37 @@ AttnArgs attn_args(const moe_attn* c, const moe_kv_cache* k, const moe_attn_batc
   return a;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    cudaGetLastError();
+  });
+  return fn;
+}
+
+bool encode_pool(CUtensorMap* m, const void* pool, const AttnArgs& a, int D) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
+  if (!encode) return false;
+  const cuuint64_t tokens = (cuuint64_t)a.Hkv << a.page_shift;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, tokens, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, tokens * D};
+  const cuuint32_t box[3] = {(cuuint32_t)std::min(D, 128),
+                             (cuuint32_t)std::min(1 << a.page_shift, kAttnKeys), 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
+                unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const bf16* q,
                   int64_t q_stride, bf16* out, int64_t out_stride, bool pdl, cudaStream_t s) {
   const int D = c->cfg.head_dim;
@@ -199,13 +233,21 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
     const long long tiles = units * a.Hkv * ((span + kAttnKeys - 1) / kAttnKeys);
     grid = std::max<long long>(1, std::min<long long>((tiles + 3) / 4, c->dec_slots));
   }
-  return launch_attn_decode(D, a, q, q_stride, out, out_stride, c->split, (int)grid, split, pdl,
+  AttnMaps maps;
+  if (!make_attn_maps(&maps, a, D)) return MOE_ERR_CUDA;
+  return launch_attn_decode(D, a, maps, q, q_stride, out, out_stride, c->split, (int)grid, split, pdl,
                             s) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
 
 }  // namespace
+
+namespace moe {
+bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D) {
+  return encode_pool(&m->k, a.kc, a, D) && encode_pool(&m->v, a.vc, a, D);
+}
+}  // namespace moe
 
 extern "C" {
 

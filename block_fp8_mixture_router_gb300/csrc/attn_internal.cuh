@@ -73,10 +73,19 @@ struct AppendArgs {
 };
 cudaError_t launch_append(int D, const AttnArgs& a, const AppendArgs& p, cudaStream_t s);
 
+// The cache's codes as the TMA sees them: [page][kv_heads x page_tokens][head_dim],
+// a box of min(page_tokens, 64) tokens of a head, 128 bytes of each (64 at
+// head_dim 64), stored with the swizzle of that width.
+struct AttnMaps {
+  CUtensorMap k, v;
+};
+bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D);
+
 cudaError_t setup_attn_decode(int D);
 int attn_decode_slots(int D, int sm_count);  // CTAs of a full grid
-cudaError_t launch_attn_decode(int D, const AttnArgs& a, const bf16* q, int64_t q_stride,
-                               bf16* out, int64_t out_stride, const AttnSplit& sp, int grid,
-                               bool split, bool pdl, cudaStream_t s);
+cudaError_t launch_attn_decode(int D, const AttnArgs& a, const AttnMaps& m, const bf16* q,
+                               int64_t q_stride, bf16* out, int64_t out_stride,
+                               const AttnSplit& sp, int grid, bool split, bool pdl,
+                               cudaStream_t s);
 
 }  // namespace moe

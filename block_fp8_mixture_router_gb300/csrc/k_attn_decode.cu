@@ -6,23 +6,53 @@
 //
 // in one pass over the keys with a running maximum m and sum.  A row tile is 16
 // rows: the g query heads of a key head times 16/g tokens.
+//
+// Bound by the cache's bytes: a CTA has a producer warp that keeps a ring of
+// kStages key tiles (64 keys and their values, 16 KB at head_dim 128) filled by
+// TMA, and four consumer warps that take 16 keys of a tile each; at head_dim 256
+// a second set of four takes the other half of the output.  The tiles lie in
+// shared memory with the TMA's swizzle, and a lane's keys are chosen (key_row) so
+// that the eight lanes of a shared-memory phase read eight different 16-byte
+// columns, of keys and of values alike.
 #include "attn_device.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kDecThreads = 128;
-constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kTileRows = 16;
 constexpr float kPShift = 1024.0f;  // weights are held as p x 2^10 in fp16
 
 template <int D>
 struct Dec {
-  static constexpr int kSlices = D / 64;           // 64-byte slices of a key row
-  static constexpr int kOut = D / 8;               // n8 output tiles
-  static constexpr int kVBytes = D / 8;            // a lane's bytes of a value row
+  static constexpr int kHalves = D == 256 ? 2 : 1;     // consumer sets, each with its output half
+  static constexpr int kConsumers = 128 * kHalves;     // threads
+  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kDO = D / kHalves;              // output values of a consumer set
+  static constexpr int kSlices = D / 64;               // 64-byte slices of a key row
+  static constexpr int kOut = kDO / 8;                 // n8 output tiles of a warp
+  static constexpr int kVBytes = kDO / 8;              // a lane's bytes of a value row
+  static constexpr int kRowBytes = D < 128 ? D : 128;  // a stored row (of a half) and its swizzle
+  static constexpr int kHalfBytes = kAttnKeys * kRowBytes;
+  static constexpr int kTileBytes = kAttnKeys * D;     // keys or values of a stage
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kQStride = D + 64;              // staged query rows, offset by half a phase
+  static constexpr bool kQInRegs = D == 64;
 };
+
+// Key of the n8 score tile n that lane group jj's column stands for: columns 2c,
+// 2c+1 of tiles 0, 1 are keys 2c, (2c^4)+8, 2c+1, (2c^4)+9 of a warp's sixteen.
+__device__ __forceinline__ int key_row(int n, int jj) {
+  return ((2 * (jj >> 1)) ^ ((jj & 1) * 4)) + (jj & 1) * 8 + n;
+}
+
+// Byte of 16-byte column `col` of row `row` under the TMA's swizzle.
+template <int D>
+__device__ __forceinline__ int swz(int row, int col) {
+  return D == 64 ? row * 64 + ((col ^ ((row >> 1) & 3)) << 4)
+                 : row * 128 + ((col ^ (row & 7)) << 4);
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -75,14 +105,14 @@ __device__ __forceinline__ void unit_range(const AttnArgs& a, Unit& u) {
 // it exactly down to 1/4 (2^-9 of the row's largest), and to 2^-10, e4m3's half
 // step (2^-17 of the largest), below.  The tensor cores then take the keys' codes
 // as they are stored.
-// Layout: [hi | lo][16 rows][D bytes]; factor[row] = the score's factor but for
-// the key's scale.
+// Layout: [hi | lo][16 rows][kQStride bytes]; factor[row] = the score's factor but
+// for the key's scale.
 template <int D>
 __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Unit& u, const bf16* q,
                                               int64_t q_stride, uint8_t* sq, float* factor) {
   constexpr int kPer = D / 8;
   const int c = threadIdx.x % kPer, sub = threadIdx.x / kPer;
-  for (int r = sub; r < kTileRows; r += kDecThreads / kPer) {
+  for (int r = sub; r < kTileRows; r += Dec<D>::kConsumers / kPer) {
     const bool on = r < u.rows;
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (on) {
@@ -125,22 +155,30 @@ __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Unit& u, 
       hi = make_uint2(w[0], w[1]);
       lo = make_uint2(z[0], z[1]);
     }
-    *reinterpret_cast<uint2*>(sq + r * D + 8 * c) = hi;
-    *reinterpret_cast<uint2*>(sq + (kTileRows + r) * D + 8 * c) = lo;
+    *reinterpret_cast<uint2*>(sq + r * Dec<D>::kQStride + 8 * c) = hi;
+    *reinterpret_cast<uint2*>(sq + (kTileRows + r) * Dec<D>::kQStride + 8 * c) = lo;
     if (c == 0) factor[r] = f;
   }
 }
 
-// One CTA's shared memory.
+// One CTA's shared memory behind the ring.
 template <int D>
 struct DecSmem {
-  uint8_t q[2 * kTileRows * D];
+  uint8_t q[2 * kTileRows * Dec<D>::kQStride];
+  float o[kTileRows][D];
   float factor[kTileRows];
-  float m[kDecWarps][kTileRows], l[kDecWarps][kTileRows];
-  float o[kDecWarps][kTileRows][D];
-  int last;
-  long long scan[kDecWarps];
+  float m[4][kTileRows], l[4][kTileRows];
+  float2 meta[Dec<D>::kStages][4];  // scales of the keys and values of 16 keys of a stage
+  uint64_t full[Dec<D>::kStages], empty[Dec<D>::kStages];
+  int last, abort, seq, tile;
+  long long front;
+  long long scan[Dec<D>::kThreads / 32];
 };
+
+template <int D>
+constexpr size_t dec_smem_bytes() {
+  return 1024 + (size_t)Dec<D>::kStages * 2 * Dec<D>::kTileBytes + sizeof(DecSmem<D>);
+}
 
 // A warp's running state over its keys: rows j and j + 8 (j = lane / 4).
 template <int D>
@@ -150,26 +188,34 @@ struct Acc {
   float vref;  // values are held as multiples of it
 };
 
+// The first operand of the score product: rows j and j + 8, hi and lo parts.
+struct QFrag {
+  uint4 h0, h1, l0, l1;
+};
+
+template <int D>
+__device__ __forceinline__ QFrag load_q(const uint8_t* sq, int j, int c, int t) {
+  const uint8_t* p = sq + j * Dec<D>::kQStride + 64 * t + 16 * c;
+  QFrag f;
+  f.h0 = *reinterpret_cast<const uint4*>(p);
+  f.h1 = *reinterpret_cast<const uint4*>(p + 8 * Dec<D>::kQStride);
+  f.l0 = *reinterpret_cast<const uint4*>(p + kTileRows * Dec<D>::kQStride);
+  f.l1 = *reinterpret_cast<const uint4*>(p + (kTileRows + 8) * Dec<D>::kQStride);
+  return f;
+}
+
 // 16 keys of one page, warp-wide: scores, weights, and the weighted values.
-// key0: position of the first; kp, vp: their code rows.  kEdge: some keys are
-// unseen by some rows (or lie behind the cache's last token).
+// key0: position of the first; kp, vp: the stage's key rows and the rows of the
+// warp's half of the values, row0 the first of the sixteen in the stage.  kEdge:
+// some keys are unseen by some rows (or lie behind the cache's last token).
 template <int D, bool kEdge>
 __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<D>& acc,
-                                          const uint8_t* sq, const float (&fac)[2], int key0,
-                                          const uint8_t* kp, const uint8_t* vp, float ksc,
-                                          float vsc) {
+                                          const QFrag* qf, const uint8_t* sq,
+                                          const float (&fac)[2], int key0, const uint8_t* kp,
+                                          const uint8_t* vp, float ksc, float vsc) {
   const int lane = threadIdx.x & 31, j = lane >> 2, c = lane & 3;
   constexpr int S = Dec<D>::kSlices;
-  // the lane's keys of the second product: 2c, 2c+1, 2c+8, 2c+9
   const int limit = u.v.len - key0;  // keys of this step that exist
-  uint4 kq[2][S];
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int t = 0; t < S; ++t)
-      kq[n][t] = (!kEdge || 8 * n + j < limit)
-                     ? *reinterpret_cast<const uint4*>(kp + (8 * n + j) * D + 64 * t + 16 * c)
-                     : make_uint4(0, 0, 0, 0);
   float s[2][4];
 #pragma unroll
   for (int n = 0; n < 2; ++n)
@@ -177,38 +223,32 @@ __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<
     for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
 #pragma unroll
   for (int t = 0; t < S; ++t) {
-    const uint8_t* p = sq + j * D + 64 * t + 16 * c;
-    const uint4 h0 = *reinterpret_cast<const uint4*>(p);
-    const uint4 h1 = *reinterpret_cast<const uint4*>(p + 8 * D);
-    const uint4 l0 = *reinterpret_cast<const uint4*>(p + kTileRows * D);
-    const uint4 l1 = *reinterpret_cast<const uint4*>(p + (kTileRows + 8) * D);
+    const QFrag f = Dec<D>::kQInRegs ? qf[t] : load_q<D>(sq, j, c, t);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      mma_e4m3_k64(s[n], h0, h1, kq[n][t]);
-      mma_e4m3_k64(s[n], l0, l1, kq[n][t]);
+      const uint4 k = *reinterpret_cast<const uint4*>(
+          kp + (t >> 1) * Dec<D>::kHalfBytes + swz<D>(key_row(n, j), 4 * (t & 1) + c));
+      mma_e4m3_k64(s[n], f.h0, f.h1, k);
+      mma_e4m3_k64(s[n], f.l0, f.l1, k);
     }
   }
-  // value rows of the lane's four keys
+  // value rows of the lane's four keys: key_row(0, 2c), (0, 2c+1), (1, 2c), (1, 2c+1)
   constexpr int W = Dec<D>::kVBytes / 4;
   uint32_t vw[4][W];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int key = 2 * c + (k & 1) + (k & 2) * 4;
-    const uint8_t* p = vp + key * D + j * Dec<D>::kVBytes;
+    const int key = key_row(k >> 1, 2 * c + (k & 1));
     const bool on = !kEdge || key < limit;
     if constexpr (W == 2) {
-      const uint2 x = on ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-      vw[k][0] = x.x;
-      vw[k][1] = x.y;
+      const uint2 x = *reinterpret_cast<const uint2*>(vp + swz<D>(key, j >> 1) + 8 * (j & 1));
+      vw[k][0] = on ? x.x : 0;
+      vw[k][1] = on ? x.y : 0;
     } else {
-#pragma unroll
-      for (int i = 0; i < W; i += 4) {
-        const uint4 x = on ? *reinterpret_cast<const uint4*>(p + 4 * i) : make_uint4(0, 0, 0, 0);
-        vw[k][i] = x.x;
-        vw[k][i + 1] = x.y;
-        vw[k][i + 2] = x.z;
-        vw[k][i + 3] = x.w;
-      }
+      const uint4 x = *reinterpret_cast<const uint4*>(vp + swz<D>(key, j));
+      vw[k][0] = on ? x.x : 0;
+      vw[k][1] = on ? x.y : 0;
+      vw[k][2] = on ? x.z : 0;
+      vw[k][3] = on ? x.w : 0;
     }
   }
   uint32_t poison = 0;  // bit k: the lane's k-th key has a NaN value
@@ -239,7 +279,7 @@ __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<
     for (int k = 0; k < 4; ++k) {
       float x = s[k >> 1][2 * r + (k & 1)] * f;
       if constexpr (kEdge) {
-        const int key = key0 + 2 * c + (k & 1) + (k & 2) * 4;
+        const int key = key0 + key_row(k >> 1, 2 * c + (k & 1));
         const bool seen = key <= pos && key < u.v.len && (!a.window || key > pos - a.window);
         if (poison & (1u << k)) x = __int_as_float(0x7FFFFFFF);
         x = seen ? x : -INFINITY;
@@ -314,125 +354,223 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, const Unit& u, bf16
   *reinterpret_cast<uint2*>(out + (int64_t)row * out_stride + (u.h * a.g + r % a.g) * D + d) = w;
 }
 
-// Key tiles [t0, t1) of a unit by one CTA.  whole: they are all of the unit's,
-// and the output is written; else the partial result goes to slot `slot`, and
-// the last of the `parts` CTAs to arrive at counter `c0` merges them all in
-// order (the first part lies in slot 2 c0 + 1, the others in 2 (c0 + i)).
+// Barrier of the consumer warps.
 template <int D>
-__device__ __forceinline__ void run_segment(const AttnArgs& a, const Unit& u, int t0, int t1,
-                                            bool whole, int slot, int c0, int first_slot,
-                                            int parts, const bf16* q, int64_t q_stride, bf16* out,
-                                            int64_t out_stride, const AttnSplit& sp,
-                                            DecSmem<D>& sm) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane >> 2, c = lane & 3;
-  __syncthreads();  // shared memory is free again
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;\n" ::"n"(Dec<D>::kConsumers) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// The ring's next stage and the parity of its barriers.
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// The producer warp's part of key tiles [t0, t1): a lane for each box (a page's
+// share of a tile) of up to 32 looks up page and scales, then each tile's lanes copy
+// their boxes once its stage is free.
+template <int D>
+__device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0, int t1,
+                                        const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                        uint8_t* ring, DecSmem<D>& sm, Ring& r) {
+  using C = Dec<D>;
+  const int lane = threadIdx.x & 31;
+  const int box_rows = min(1 << a.page_shift, kAttnKeys);
+  const int per_tile = kAttnKeys / box_rows;
+  const int batch = 32 / per_tile;  // tiles of a batch of boxes
+  for (int kt0 = t0; kt0 < t1; kt0 += batch) {
+    const int tiles = min(batch, t1 - kt0);
+    const int key = kt0 * kAttnKeys + lane * box_rows;
+    bool on = lane < tiles * per_tile && key < u.hi && key + box_rows > u.lo;
+    int page = 0;
+    float ks = 0.0f, vs = 0.0f;
+    if (on) {
+      page = page_at(a, u.s, key >> a.page_shift);
+      if (page < 0) {
+        atomicOr(a.status, kAttnBadBatch);
+        on = false;
+        ks = -1.0f;  // its keys count as absent
+      } else {
+        ks = a.ks[(size_t)page * a.Hkv + u.h];
+        vs = a.vs[(size_t)page * a.Hkv + u.h];
+      }
+    }
+    const int y = (u.h << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+    for (int i = 0; i < tiles; ++i) {
+      tc::wait_bounded(&sm.empty[r.stage], r.phase ^ 1, &sm.abort, a.status);
+      if (*(volatile int*)&sm.abort) return;
+      const int sub = lane - i * per_tile;  // this lane's box in the tile
+      const bool mine = sub >= 0 && sub < per_tile;
+      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine && on));
+      if (mine)
+        for (int g = sub * box_rows / 16; g < (sub + 1) * box_rows / 16; ++g)
+          sm.meta[r.stage][g] = make_float2(ks, vs);
+      __syncwarp();
+      if (lane == 0)
+        tc::mbar_arrive_expect_tx(&sm.full[r.stage], boxes * box_rows * D * 2);
+      __syncwarp();
+      if (mine && on) {
+        uint8_t* k = ring + (size_t)r.stage * 2 * C::kTileBytes + sub * box_rows * C::kRowBytes;
+#pragma unroll
+        for (int half = 0; half < D / C::kRowBytes; ++half) {
+          tma_load_3d(k + half * C::kHalfBytes, kmap, half * 128, y, page, &sm.full[r.stage]);
+          tma_load_3d(k + C::kTileBytes + half * C::kHalfBytes, vmap, half * 128, y, page,
+                      &sm.full[r.stage]);
+        }
+      }
+      r.next(C::kStages);
+    }
+  }
+}
+
+// The consumers' part of key tiles [t0, t1) of a unit.  whole: they are all of
+// the unit's, and the output is written; else the partial result goes to slot
+// `slot`, and the last of the `parts` CTAs to arrive at counter `c0` merges them all
+// in order (the first part lies in slot 2 c0 + 1, the others in 2 (c0 + i)).
+template <int D>
+__device__ __forceinline__ void consume(const AttnArgs& a, const Unit& u, int t0, int t1,
+                                        bool whole, int slot, int c0, int parts, const bf16* q,
+                                        int64_t q_stride, bf16* out, int64_t out_stride,
+                                        const AttnSplit& sp, const uint8_t* ring, DecSmem<D>& sm,
+                                        Ring& r) {
+  using C = Dec<D>;
+  const int tid = threadIdx.x, lane = tid & 31, j = lane >> 2, c = lane & 3;
+  const int grp = (tid >> 5) & 3, half = tid >> 7;  // keys of a tile, output half
+  consumer_sync<D>();  // shared memory is free again
   stage_queries<D>(a, u, q, q_stride, sm.q, sm.factor);
-  __syncthreads();
+  consumer_sync<D>();
   const float fac[2] = {sm.factor[j], sm.factor[j + 8]};
+  QFrag qf[C::kQInRegs ? C::kSlices : 1];
+  if constexpr (C::kQInRegs)
+#pragma unroll
+    for (int t = 0; t < C::kSlices; ++t) qf[t] = load_q<D>(sm.q, j, c, t);
   Acc<D> acc;
 #pragma unroll
-  for (int t = 0; t < Dec<D>::kOut; ++t)
+  for (int t = 0; t < C::kOut; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc.o[t][i] = 0.0f;
   acc.m[0] = acc.m[1] = -INFINITY;
   acc.l[0] = acc.l[1] = 0.0f;
   acc.vref = 0x1p-126f;
-  const int P = 1 << a.page_shift;
   const int pos0 = u.v.first + u.tok0;                      // earliest row
   const int pos1 = pos0 + (u.rows - 1) / a.g;               // latest row
   for (int kt = t0; kt < t1; ++kt) {
-    const int key0 = kt * kAttnKeys + warp * 16;
-    if (key0 >= u.hi || key0 + 16 <= u.lo) continue;
-    const int page = page_at(a, u.s, key0 >> a.page_shift);
-    if (page < 0) {
-      if (lane == 0) atomicOr(a.status, kAttnBadBatch);
-      continue;
+    tc::wait_bounded(&sm.full[r.stage], r.phase, &sm.abort, a.status);
+    const int key0 = kt * kAttnKeys + grp * 16;
+    const float2 sc = sm.meta[r.stage][grp];
+    if (key0 < u.hi && key0 + 16 > u.lo && sc.x >= 0.0f) {
+      const uint8_t* kp = ring + (size_t)r.stage * 2 * C::kTileBytes + grp * 16 * C::kRowBytes;
+      const uint8_t* vp = kp + C::kTileBytes + half * C::kHalfBytes;
+      const bool edge = key0 + 15 > pos0 || (a.window && key0 <= pos1 - a.window);
+      if (edge)
+        warp_keys<D, true>(a, u, acc, qf, sm.q, fac, key0, kp, vp, sc.x, sc.y);
+      else
+        warp_keys<D, false>(a, u, acc, qf, sm.q, fac, key0, kp, vp, sc.x, sc.y);
     }
-    const size_t block = (size_t)page * a.Hkv + u.h;
-    const size_t at = (block * P + (key0 & (P - 1))) * D;
-    const float ksc = a.ks[block], vsc = a.vs[block];
-    const bool edge = key0 + 15 > pos0 || (a.window && key0 <= pos1 - a.window);
-    if (edge)
-      warp_keys<D, true>(a, u, acc, sm.q, fac, key0, a.kc + at, a.vc + at, ksc, vsc);
-    else
-      warp_keys<D, false>(a, u, acc, sm.q, fac, key0, a.kc + at, a.vc + at, ksc, vsc);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.empty[r.stage]);
+    r.next(C::kStages);
   }
-  // join the warps: l over the lanes of a row, then rows scaled to one maximum
+  // join the warps: l over the lanes of a row, then rows scaled to one maximum and
+  // added in the order of the warps
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], o);
-    if (c == 0) {
-      sm.m[warp][j + 8 * r] = acc.m[r];
-      sm.l[warp][j + 8 * r] = acc.l[r];
+    for (int o = 1; o < 4; o <<= 1) acc.l[i] += __shfl_xor_sync(0xffffffffu, acc.l[i], o);
+    if (c == 0 && half == 0) {
+      sm.m[grp][j + 8 * i] = acc.m[i];
+      sm.l[grp][j + 8 * i] = acc.l[i];
     }
   }
-  __syncthreads();
+  consumer_sync<D>();
+  float g[2];
+  bool none[2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = j + 8 * r;
+  for (int i = 0; i < 2; ++i) {
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sm.m[w][row]);
-    const float f = acc.m[r] == -INFINITY ? 0.0f : exp2_approx(acc.m[r] - m);
-    const float g = f * (acc.vref * (1.0f / kPShift));
-    // lane's values of the row: 2c kVBytes + t and (2c + 1) kVBytes + t
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int t = 0; t < Dec<D>::kOut; t += 4) {
-        float4 x = make_float4(acc.o[t][2 * r + h] * g, acc.o[t + 1][2 * r + h] * g,
-                               acc.o[t + 2][2 * r + h] * g, acc.o[t + 3][2 * r + h] * g);
-        // a warp that saw no key of the row adds nothing, NaN or not
-        if (acc.m[r] == -INFINITY && !(acc.l[r] != acc.l[r])) x = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(&sm.o[warp][row][(2 * c + h) * Dec<D>::kVBytes + t]) = x;
-      }
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.m[w][j + 8 * i]);
+    const float f = acc.m[i] == -INFINITY ? 0.0f : exp2_approx(acc.m[i] - m);
+    g[i] = f * (acc.vref * (1.0f / kPShift));
+    // a warp that saw no key of the row adds nothing; one that only saw NaN, NaN
+    none[i] = acc.m[i] == -INFINITY && acc.l[i] == acc.l[i];
   }
-  __syncthreads();
+  for (int w = 0; w < 4; ++w) {
+    if (w == grp) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < C::kOut; t += 4) {
+            float4* at = reinterpret_cast<float4*>(
+                &sm.o[j + 8 * i][half * C::kDO + (2 * c + h) * C::kVBytes + t]);
+            float4 x = make_float4(acc.o[t][2 * i + h] * g[i], acc.o[t + 1][2 * i + h] * g[i],
+                                   acc.o[t + 2][2 * i + h] * g[i], acc.o[t + 3][2 * i + h] * g[i]);
+            if (none[i]) x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w > 0) {
+              const float4 y = *at;
+              x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+            }
+            *at = x;
+          }
+    }
+    consumer_sync<D>();
+  }
   const int rows = u.rows;
-  for (int i = tid; i < rows * (D / 4); i += kDecThreads) {
-    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+  for (int i = tid; i < rows * (D / 4); i += C::kConsumers) {
+    const int row = i / (D / 4), d = (i % (D / 4)) * 4;
     float m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sm.m[w][r]);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.m[w][row]);
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      const float mw = sm.m[w][r], lw = sm.l[w][r];
+    for (int w = 0; w < 4; ++w) {
+      const float mw = sm.m[w][row], lw = sm.l[w][row];
       l += mw == -INFINITY ? lw : lw * exp2_approx(mw - m);
-      const float4 y = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
     }
+    const float4 x = *reinterpret_cast<const float4*>(&sm.o[row][d]);
     if (whole) {
       const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-      store_out<D>(a, u, out, out_stride, r, d,
+      store_out<D>(a, u, out, out_stride, row, d,
                    make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
     } else {
-      const size_t at = (size_t)slot * kTileRows + r;
+      const size_t at = (size_t)slot * kTileRows + row;
       __stcg(reinterpret_cast<float4*>(sp.o + at * D + d), x);
       if (d == 0) __stcg(sp.ml + at, make_float2(m, l));
     }
   }
   if (whole) return;
   __threadfence();
-  __syncthreads();
+  consumer_sync<D>();
   if (tid == 0) {
     const int n = atomicAdd(sp.arrived + c0, 1);
     sm.last = n == parts - 1;
     if (sm.last) sp.arrived[c0] = 0;
   }
-  __syncthreads();
+  consumer_sync<D>();
   if (!sm.last) return;
   __threadfence();
-  for (int i = tid; i < rows * (D / 4); i += kDecThreads) {
-    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+  for (int i = tid; i < rows * (D / 4); i += C::kConsumers) {
+    const int row = i / (D / 4), d = (i % (D / 4)) * 4;
     float m = -INFINITY, l = 0.0f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p = 0; p < parts; ++p) {
-      const size_t at = (size_t)(p == 0 ? first_slot : 2 * (c0 + p)) * kTileRows + r;
+      const size_t at = (size_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kTileRows + row;
       const float2 ml = __ldcg(sp.ml + at);
       const float4 y = __ldcg(reinterpret_cast<const float4*>(sp.o + at * D + d));
       const float mn = fmaxf(m, ml.x);
@@ -444,25 +582,44 @@ __device__ __forceinline__ void run_segment(const AttnArgs& a, const Unit& u, in
                       x.w * fo + y.w * fn);
     }
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-    store_out<D>(a, u, out, out_stride, r, d,
+    store_out<D>(a, u, out, out_stride, row, d,
                  make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
   }
 }
 
 // kSplit: the key tiles of all units, in unit order, are dealt to the CTAs in
 // equal runs, whatever the sequences' lengths are; a unit that several CTAs share
-// is merged by the last of them.  Else a CTA per unit.
+// is merged by the last of them.  Else a CTA per unit.  The producer and the
+// consumers walk the same run.
 template <int D, bool kSplit>
-__global__ void __launch_bounds__(kDecThreads)
-    k_attn_decode(AttnArgs a, const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
-                  AttnSplit sp) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  DecSmem<D>& sm = *reinterpret_cast<DecSmem<D>*>(smem_raw);
+__global__ void __launch_bounds__(Dec<D>::kThreads, D == 256 ? 1 : 2)
+    k_attn_decode(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const AttnArgs a, const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
+                  const AttnSplit sp) {
+  using C = Dec<D>;
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* ring = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  DecSmem<D>& sm =
+      *reinterpret_cast<DecSmem<D>*>(ring + (size_t)C::kStages * 2 * C::kTileBytes);
   const int tid = threadIdx.x;
   const int tq = tile_tokens(a.g);
+  const bool producer = tid >= C::kConsumers;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], C::kConsumers / 32);
+    }
+    sm.abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (producer && (tid & 31) == 0) {
+    tc::tma_prefetch_map(&kmap);
+    tc::tma_prefetch_map(&vmap);
+  }
+  Ring r;
+  Unit u;
+  long long begin = 0, end = 0, per = 1, f = 0;
   if constexpr (!kSplit) {
-    pdl_wait();
-    Unit u;
     int u0;
     const int unit = blockIdx.x / a.Hkv;
     u.h = blockIdx.x % a.Hkv;
@@ -472,14 +629,17 @@ __global__ void __launch_bounds__(kDecThreads)
     u.t = unit - u0;
     if (u.t < 0 || u.t * tq >= u.v.n) return;
     unit_range(a, u);
-    run_segment<D>(a, u, u.kt0, u.kt1, true, 0, 0, 0, 1, q, q_stride, out, out_stride, sp, sm);
-    return;
+    // this unit alone: a run that is exactly its tiles
+    f = 0;
+    begin = (long long)u.h * (u.kt1 - u.kt0);
+    end = begin + (u.kt1 - u.kt0);
+    per = 0x7FFFFFFFFFFFll;
+    __syncthreads();
   } else {
     // each thread's run of sequences, their key tiles, and the tiles in front
-    const int per_thread = (a.n_seqs + kDecThreads - 1) / kDecThreads;
+    const int per_thread = (a.n_seqs + C::kThreads - 1) / C::kThreads;
     const int s0 = min(tid * per_thread, a.n_seqs), s1 = min(s0 + per_thread, a.n_seqs);
     long long mine = 0;
-    Unit u;
     for (int s = s0; s < s1; ++s) {
       u.v = seq_view(a, s);
       if (!u.v.ok) atomicOr(a.status, kAttnBadBatch);
@@ -499,29 +659,28 @@ __global__ void __launch_bounds__(kDecThreads)
     __syncthreads();
     long long total = 0, front = run - mine;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
+    for (int w = 0; w < C::kThreads / 32; ++w) {
       if (w < warp) front += sm.scan[w];
       total += sm.scan[w];
     }
     if (total == 0) return;
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
-    const long long begin = per * blockIdx.x, end = min(begin + per, total);
+    per = (total + gridDim.x - 1) / gridDim.x;
+    begin = per * blockIdx.x;
+    end = min(begin + per, total);
     if (begin >= end) return;
     // the thread whose run holds the first tile finds its unit
-    __shared__ int s_seq, s_t;
-    __shared__ long long s_front;
     if (mine > 0 && front <= begin && begin < front + mine) {
-      long long f = front;
       bool found = false;
+      f = front;
       for (int s = s0; s < s1 && !found; ++s) {
         u.v = seq_view(a, s);
         for (u.t = 0; u.t * tq < u.v.n && !found; ++u.t) {
           unit_range(a, u);
           const long long w = (long long)(u.kt1 - u.kt0) * a.Hkv;
           if (begin < f + w) {
-            s_seq = s;
-            s_t = u.t;
-            s_front = f;
+            sm.seq = s;
+            sm.tile = u.t;
+            sm.front = f;
             found = true;
           } else {
             f += w;
@@ -530,39 +689,49 @@ __global__ void __launch_bounds__(kDecThreads)
       }
     }
     __syncthreads();
-    u.s = s_seq;
-    u.t = s_t;
-    long long f = s_front;  // tiles in front of (sequence, row tile)
+    u.s = sm.seq;
+    u.t = sm.tile;
+    f = sm.front;  // tiles in front of (sequence, row tile)
     u.v = seq_view(a, u.s);
     unit_range(a, u);
     u.h = (int)((begin - f) / (u.kt1 - u.kt0));
-    pdl_wait();
-    long long at = begin;
-    while (at < end) {
-      const int w = u.kt1 - u.kt0;
-      const long long u_first = f + (long long)u.h * w;  // the unit's first tile
-      const long long stop = min(end, u_first + w);
+  }
+  pdl_wait();
+  long long at = begin;
+  while (at < end) {
+    const int w = u.kt1 - u.kt0;
+    const long long u_first = f + (long long)u.h * w;  // the unit's first tile
+    const long long stop = min(end, u_first + w);
+    const int t0 = u.kt0 + (int)(at - u_first), t1 = u.kt0 + (int)(stop - u_first);
+    if (producer) {
+      produce<D>(a, u, t0, t1, &kmap, &vmap, ring, sm, r);
+    } else {
       const bool whole = at == u_first && stop == u_first + w;
       const int c0 = (int)(u_first / per), c1 = (int)((u_first + w - 1) / per);
-      // a unit that begins with a CTA's run lies in the CTA's first slot when
-      // the CTA only works on it
-      const int first_slot = 2 * c0 + 1;
-      const int slot = at == u_first ? first_slot : 2 * (int)blockIdx.x;
-      run_segment<D>(a, u, u.kt0 + (int)(at - u_first), u.kt0 + (int)(stop - u_first), whole, slot, c0,
-                     first_slot, c1 - c0 + 1, q, q_stride, out, out_stride, sp, sm);
-      at = stop;
-      if (at >= end) break;
-      if (++u.h == a.Hkv) {
-        u.h = 0;
-        f += (long long)w * a.Hkv;
-        ++u.t;
-        while (u.t * tq >= u.v.n) {
-          u.t = 0;
-          u.v = seq_view(a, ++u.s);
-        }
-        unit_range(a, u);
-      }
+      const int slot = at == u_first ? 2 * c0 + 1 : 2 * (int)blockIdx.x;
+      consume<D>(a, u, t0, t1, whole, slot, c0, c1 - c0 + 1, q, q_stride, out, out_stride, sp, ring,
+                 sm, r);
     }
+    at = stop;
+    if (at >= end) break;
+    if (++u.h == a.Hkv) {
+      u.h = 0;
+      f += (long long)w * a.Hkv;
+      ++u.t;
+      while (u.t * tq >= u.v.n) {
+        u.t = 0;
+        u.v = seq_view(a, ++u.s);
+      }
+      unit_range(a, u);
+    }
+  }
+  if (producer && *(volatile int*)&sm.abort) {
+    // a wait gave up: let this CTA's copies land before its memory goes back
+    for (int i = 0; i < C::kStages; ++i)
+      for (int k = 0; k < 100000 && !tc::mbar_try_wait(&sm.full[i], 0) &&
+                      !tc::mbar_try_wait(&sm.full[i], 1);
+           ++k) {
+      }
   }
 }
 
@@ -570,18 +739,18 @@ template <int D>
 cudaError_t setup_d() {
   cudaError_t e = cudaFuncSetAttribute(k_attn_decode<D, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(DecSmem<D>));
+                                       (int)dec_smem_bytes<D>());
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_attn_decode<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(DecSmem<D>));
+                             (int)dec_smem_bytes<D>());
   return e;
 }
 
 template <int D>
 int slots_d(int sm_count) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attn_decode<D, true>, kDecThreads,
-                                                    sizeof(DecSmem<D>)) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attn_decode<D, true>, Dec<D>::kThreads,
+                                                    dec_smem_bytes<D>()) != cudaSuccess) {
     cudaGetLastError();
     n = 1;
   }
@@ -589,13 +758,12 @@ int slots_d(int sm_count) {
 }
 
 template <int D>
-cudaError_t launch_d(const AttnArgs& a, const bf16* q, int64_t q_stride, bf16* out,
-                     int64_t out_stride, const AttnSplit& sp, int grid, bool split, bool pdl,
-                     cudaStream_t s) {
-  return split ? launch_pdl(k_attn_decode<D, true>, dim3(grid), dim3(kDecThreads),
-                            sizeof(DecSmem<D>), s, pdl, a, q, q_stride, out, out_stride, sp)
-               : launch_pdl(k_attn_decode<D, false>, dim3(grid), dim3(kDecThreads),
-                            sizeof(DecSmem<D>), s, pdl, a, q, q_stride, out, out_stride, sp);
+cudaError_t launch_d(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64_t q_stride,
+                     bf16* out, int64_t out_stride, const AttnSplit& sp, int grid, bool split,
+                     bool pdl, cudaStream_t s) {
+  auto* kernel = split ? k_attn_decode<D, true> : k_attn_decode<D, false>;
+  return launch_pdl(kernel, dim3(grid), dim3(Dec<D>::kThreads), dec_smem_bytes<D>(), s, pdl, m.k,
+                    m.v, a, q, q_stride, out, out_stride, sp);
 }
 
 }  // namespace
@@ -609,11 +777,12 @@ int attn_decode_slots(int D, int sm_count) {
                                                     : slots_d<256>(sm_count);
 }
 
-cudaError_t launch_attn_decode(int D, const AttnArgs& a, const bf16* q, int64_t q_stride,
-                               bf16* out, int64_t out_stride, const AttnSplit& sp, int grid,
-                               bool split, bool pdl, cudaStream_t s) {
+cudaError_t launch_attn_decode(int D, const AttnArgs& a, const AttnMaps& m, const bf16* q,
+                               int64_t q_stride, bf16* out, int64_t out_stride,
+                               const AttnSplit& sp, int grid, bool split, bool pdl,
+                               cudaStream_t s) {
   auto* f = D == 64 ? launch_d<64> : D == 128 ? launch_d<128> : launch_d<256>;
-  return f(a, q, q_stride, out, out_stride, sp, grid, split, pdl, s);
+  return f(a, m, q, q_stride, out, out_stride, sp, grid, split, pdl, s);
 }
 
 }  // namespace moe
