@@ -573,6 +573,8 @@ class KVCache:
             k_codes, v_codes, k_scales, v_scales
         self._c = moe_kv_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                                v_scales.data_ptr(), k_codes.shape[0])
+        self._ref = ctypes.byref(self._c)
+        self._pages = tuple(k_codes.shape[1:])
 
     @classmethod
     def empty(cls, shape: AttnShape, n_pages: int, device="cuda"):
@@ -605,17 +607,15 @@ class AttnBatch:
         self.row_start, self.kv_len, self.pages, self.rows = row_start, kv_len, pages, rows
         self._c = moe_attn_batch(row_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), n,
                                  pages.shape[1], rows, max_seq_rows, max_kv_len)
+        self._ref = ctypes.byref(self._c)
 
 
-def _rows3(t: torch.Tensor, heads: int, dim: int, what: str) -> int:
+def _rows3(t: torch.Tensor, rows: int, heads: int, dim: int, what: str) -> int:
     """Row stride of a [rows, heads, dim] bf16 CUDA tensor whose heads lie side by side."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{what} must be a 3-D bf16 CUDA tensor")
-    rows, h, d = t.shape
-    if h != heads or d != dim:
-        raise ValueError(f"{what} must be [rows, {heads}, {dim}], not {tuple(t.shape)}")
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.shape != (rows, heads, dim):
+        raise ValueError(f"{what} must be a bf16 CUDA tensor [{rows}, {heads}, {dim}]")
     sr, sh, sd = t.stride()
-    if sd != 1 or (h > 1 and sh != dim):
+    if (sd != 1 and rows) or (sh != dim and heads > 1 and rows):
         raise ValueError(f"{what}: the heads of a row must lie side by side")
     return sr if rows > 1 else heads * dim
 
@@ -630,6 +630,9 @@ class Attention:
         rc, h = moe_attn_create(shape.config(max_rows, max_seqs, workspace_cap_bytes), device)
         _check(rc, "moe_attn_create")
         self.ctx = h
+        self._lib = load_library()
+        self._pages = (shape.kv_heads, shape.page_tokens, shape.head_dim)
+        self._gamma_shape = (shape.head_dim,)
 
     def close(self):
         if getattr(self, "ctx", None):
@@ -642,68 +645,75 @@ class Attention:
         except Exception:
             pass
 
+    def _at(self, stream) -> int:
+        """The stream's handle; None: PyTorch's current stream of the device."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
     def _cache_ok(self, cache: KVCache):
-        s = self.shape
-        if tuple(cache.k_codes.shape[1:]) != (s.kv_heads, s.page_tokens, s.head_dim):
+        if cache._pages != self._pages:
             raise ValueError("the cache's pages are not of this shape")
 
-    def _gamma_ok(self, *gammas):
-        for g in gammas:
-            if g is not None and (g.dtype != torch.bfloat16 or not g.is_cuda or
-                                  not g.is_contiguous() or g.shape != (self.shape.head_dim,)):
-                raise ValueError("a gamma must be a contiguous bf16 CUDA tensor [head_dim]")
+    def _gamma(self, g):
+        if g is None:
+            return None
+        if g.dtype is not torch.bfloat16 or not g.is_cuda or g.shape != self._gamma_shape or \
+                not g.is_contiguous():
+            raise ValueError("a gamma must be a contiguous bf16 CUDA tensor [head_dim]")
+        return g.data_ptr()
 
-    def _out(self, out, like, rows):
-        s = self.shape
-        if out is None:
-            out = torch.empty((rows, s.q_heads, s.head_dim), dtype=torch.bfloat16,
-                              device=like.device)
-        return out, _rows3(out, s.q_heads, s.head_dim, "out")
+    def _out(self, like, rows):
+        return torch.empty((rows, self.shape.q_heads, self.shape.head_dim), dtype=torch.bfloat16,
+                           device=like.device)
 
     def rope(self, x: torch.Tensor, positions: torch.Tensor, gamma: torch.Tensor | None = None,
              eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Rotary positions of x [rows, heads, head_dim] (queries or keys, any number of
         heads), after an RMS norm of each head where gamma is given; out may be x."""
-        heads = x.shape[1] if x.dim() == 3 else 0
-        xs = _rows3(x, heads, self.shape.head_dim, "x")
-        rows = x.shape[0]
-        if positions.dtype != torch.int32 or not positions.is_cuda or \
+        if x.dim() != 3:
+            raise ValueError("x must be [rows, heads, head_dim]")
+        rows, heads, dim = x.shape[0], x.shape[1], self.shape.head_dim
+        xs = _rows3(x, rows, heads, dim, "x")
+        if positions.dtype is not torch.int32 or not positions.is_cuda or \
                 positions.shape != (rows,) or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int32 CUDA tensor [rows]")
-        self._gamma_ok(gamma)
         if out is None:
-            out = torch.empty((rows, heads, self.shape.head_dim), dtype=x.dtype, device=x.device)
-        ys = _rows3(out, heads, self.shape.head_dim, "out")
-        if out.shape[0] != rows:
-            raise ValueError("out must have x's rows")
-        _check(moe_rope(self.ctx, x, xs, heads, positions, gamma, eps, rows, out, ys, stream),
-               "moe_rope")
+            out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=x.device)
+        rc = self._lib.moe_rope(self.ctx, x.data_ptr(), xs, heads, positions.data_ptr(),
+                                self._gamma(gamma), eps, rows, out.data_ptr(),
+                                _rows3(out, rows, heads, dim, "out"), self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_rope")
         return out
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cache: KVCache, batch: AttnBatch,
                stream=None):
         """Rows of keys and values [rows, kv_heads, head_dim] into the cache."""
-        s = self.shape
-        ks = _rows3(k, s.kv_heads, s.head_dim, "k")
-        vs = _rows3(v, s.kv_heads, s.head_dim, "v")
-        if k.shape[0] != batch.rows or v.shape[0] != batch.rows:
-            raise ValueError("k and v must have the batch's rows")
+        s, n = self.shape, batch.rows
+        ks = _rows3(k, n, s.kv_heads, s.head_dim, "k")
+        vs = _rows3(v, n, s.kv_heads, s.head_dim, "v")
         self._cache_ok(cache)
-        _check(moe_kv_append(self.ctx, cache._c, k, ks, v, vs, batch._c, stream),
-               "moe_kv_append")
+        rc = self._lib.moe_kv_append(self.ctx, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
+                                     batch._ref, self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_kv_append")
 
     def forward(self, q: torch.Tensor, cache: KVCache, batch: AttnBatch,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of q [rows, q_heads, head_dim] over the cache, which already
         holds the batch's rows."""
-        s = self.shape
-        qs = _rows3(q, s.q_heads, s.head_dim, "q")
-        out, os_ = self._out(out, q, batch.rows)
-        if q.shape[0] != batch.rows or out.shape[0] != batch.rows:
-            raise ValueError("q and out must have the batch's rows")
+        s, n = self.shape, batch.rows
+        qs = _rows3(q, n, s.q_heads, s.head_dim, "q")
+        if out is None:
+            out = self._out(q, n)
         self._cache_ok(cache)
-        _check(moe_attn_forward(self.ctx, cache._c, q, qs, batch._c, out, os_, stream),
-               "moe_attn_forward")
+        rc = self._lib.moe_attn_forward(self.ctx, cache._ref, q.data_ptr(), qs, batch._ref,
+                                        out.data_ptr(),
+                                        _rows3(out, n, s.q_heads, s.head_dim, "out"),
+                                        self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_attn_forward")
         return out
 
     def step(self, qkv: torch.Tensor, cache: KVCache, batch: AttnBatch,
@@ -711,15 +721,18 @@ class Attention:
              eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The whole attention step from a projection's rows [rows, q_heads + 2 kv_heads,
         head_dim]: norms and rotates, appends, attends."""
-        s = self.shape
-        xs = _rows3(qkv, s.q_heads + 2 * s.kv_heads, s.head_dim, "qkv")
-        out, os_ = self._out(out, qkv, batch.rows)
-        if qkv.shape[0] != batch.rows or out.shape[0] != batch.rows:
-            raise ValueError("qkv and out must have the batch's rows")
+        s, n = self.shape, batch.rows
+        xs = _rows3(qkv, n, s.q_heads + 2 * s.kv_heads, s.head_dim, "qkv")
+        if out is None:
+            out = self._out(qkv, n)
         self._cache_ok(cache)
-        self._gamma_ok(q_gamma, k_gamma)
-        _check(moe_attn_step(self.ctx, cache._c, qkv, xs, q_gamma, k_gamma, eps, batch._c, out,
-                             os_, stream), "moe_attn_step")
+        rc = self._lib.moe_attn_step(self.ctx, cache._ref, qkv.data_ptr(), xs,
+                                     self._gamma(q_gamma), self._gamma(k_gamma), eps, batch._ref,
+                                     out.data_ptr(),
+                                     _rows3(out, n, s.q_heads, s.head_dim, "out"),
+                                     self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_attn_step")
         return out
 
     def device_status(self) -> int:

@@ -22,7 +22,12 @@ namespace moe {
 namespace {
 
 constexpr int kTileRows = 16;
-constexpr float kPShift = 1024.0f;  // weights are held as p x 2^10 in fp16
+// Weights are held as p x 2^10 in fp16, and p is taken against a maximum that may
+// lag the true one by kLag powers of two: a row's sums are only scaled again where its
+// scores outgrow that, and 2^(10 + kLag) is still half of fp16's range.  fp16's
+// smallest step is then 2^-34 of a weight of one.
+constexpr float kPShift = 1024.0f;
+constexpr float kLag = 5.0f;
 
 template <int D>
 struct Dec {
@@ -186,6 +191,7 @@ struct Acc {
   float o[Dec<D>::kOut][4];
   float m[2], l[2];
   float vref;  // values are held as multiples of it
+  float up;    // kPShift / vref
 };
 
 // The first operand of the score product: rows j and j + 8, hi and lo parts.
@@ -268,55 +274,45 @@ __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) poison |= __shfl_xor_sync(0xffffffffu, poison, o);
   }
-  // scores in log2 units, masked
-  float mx[2] = {-INFINITY, -INFINITY};
+  // the rows' factors to log2 units; which keys they see; whether a score outgrew
+  // the row's reference
+  const float f[2] = {fac[0] * ksc, fac[1] * ksc};
+  bool seen[2][4];
+  float mx[2];
+  bool grow = vsc > acc.vref;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const float f = fac[r] * ksc;
-    const int row = j + 8 * r;
-    const int pos = u.v.first + u.tok0 + row / a.g;
+    mx[r] = -INFINITY;
+    if constexpr (kEdge) {
+      const int pos = u.v.first + u.tok0 + (j + 8 * r) / a.g;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float x = s[k >> 1][2 * r + (k & 1)] * f;
-      if constexpr (kEdge) {
+      for (int k = 0; k < 4; ++k) {
         const int key = key0 + key_row(k >> 1, 2 * c + (k & 1));
-        const bool seen = key <= pos && key < u.v.len && (!a.window || key > pos - a.window);
-        if (poison & (1u << k)) x = __int_as_float(0x7FFFFFFF);
-        x = seen ? x : -INFINITY;
+        seen[r][k] = key <= pos && key < u.v.len && (!a.window || key > pos - a.window);
+        if (seen[r][k]) mx[r] = fmaxf(mx[r], s[k >> 1][2 * r + (k & 1)]);
       }
-      s[k >> 1][2 * r + (k & 1)] = x;
-      mx[r] = fmaxf(mx[r], x);
+    } else {
+      mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+    mx[r] = mx[r] == -INFINITY ? mx[r] : mx[r] * f[r];
+    grow |= mx[r] > acc.m[r] + kLag;
   }
-  // values are held relative to the largest page scale so far
-  float vf = 1.0f;
-  if (vsc > acc.vref) {
-    vf = acc.vref / vsc;
-    acc.vref = vsc;
-  }
-  const float w = __fdividef(vsc, acc.vref) * kPShift;
-  float corr[2];
-  uint32_t p16[4];
+  if (__any_sync(0xffffffffu, grow)) {
+    // new references: the rows' running maxima, and the largest page scale so far
+    const float vf = vsc > acc.vref ? __fdiv_rn(acc.vref, vsc) : 1.0f;
+    acc.vref = fmaxf(acc.vref, vsc);
+    acc.up = __fdiv_rn(kPShift, acc.vref);
+    float corr[2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const float m_new = fmaxf(acc.m[r], mx[r]);
-    const float base = m_new == -INFINITY ? 0.0f : m_new;
-    const float alpha = exp2_approx(acc.m[r] - base);
-    acc.m[r] = m_new;
-    float p[4], sum = 0.0f;
+    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      p[k] = exp2_approx(s[k >> 1][2 * r + (k & 1)] - base);
-      sum += p[k];
+      for (int o = 1; o < 4; o <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+      const float m_new = fmaxf(acc.m[r], mx[r]);
+      const float alpha = m_new == -INFINITY ? 1.0f : exp2_approx(acc.m[r] - m_new);
+      acc.m[r] = m_new;
+      acc.l[r] *= alpha;
+      corr[r] = alpha * vf;
     }
-    acc.l[r] = acc.l[r] * alpha + sum;
-    corr[r] = alpha * vf;
-    p16[r] = f16x2(p[0] * w, p[1] * w);
-    p16[2 + r] = f16x2(p[2] * w, p[3] * w);
-  }
-  if (corr[0] != 1.0f || corr[1] != 1.0f) {
 #pragma unroll
     for (int t = 0; t < Dec<D>::kOut; ++t) {
       acc.o[t][0] *= corr[0];
@@ -324,6 +320,30 @@ __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<
       acc.o[t][2] *= corr[1];
       acc.o[t][3] *= corr[1];
     }
+  }
+  // the weights carry the page's scale in their exponent, and the sum of them is
+  // freed of it again; a page below 2^-70 of the largest adds no value that counts
+  const float w = fmaxf(vsc * acc.up, 0x1p-60f);
+  float lw, w_inv;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(lw) : "f"(w));
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(w_inv) : "f"(w));
+  uint32_t p16[4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float base = acc.m[r] == -INFINITY ? lw : lw - acc.m[r];
+    float p[4], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      p[k] = exp2_approx(fmaf(s[k >> 1][2 * r + (k & 1)], f[r], base));
+      if constexpr (kEdge) {
+        if (poison & (1u << k)) p[k] = __int_as_float(0x7FFFFFFF);
+        if (!seen[r][k]) p[k] = 0.0f;
+      }
+      sum += p[k];
+    }
+    acc.l[r] = fmaf(sum, w_inv, acc.l[r]);
+    p16[r] = f16x2(p[0], p[1]);
+    p16[2 + r] = f16x2(p[2], p[3]);
   }
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -406,7 +426,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
         on = false;
         ks = -1.0f;  // its keys count as absent
       } else {
-        ks = a.ks[(size_t)page * a.Hkv + u.h];
+        ks = a.ks[(size_t)page * a.Hkv + u.h];  // used after the first copies are out
         vs = a.vs[(size_t)page * a.Hkv + u.h];
       }
     }
@@ -417,13 +437,6 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
       const int sub = lane - i * per_tile;  // this lane's box in the tile
       const bool mine = sub >= 0 && sub < per_tile;
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine && on));
-      if (mine)
-        for (int g = sub * box_rows / 16; g < (sub + 1) * box_rows / 16; ++g)
-          sm.meta[r.stage][g] = make_float2(ks, vs);
-      __syncwarp();
-      if (lane == 0)
-        tc::mbar_arrive_expect_tx(&sm.full[r.stage], boxes * box_rows * D * 2);
-      __syncwarp();
       if (mine && on) {
         uint8_t* k = ring + (size_t)r.stage * 2 * C::kTileBytes + sub * box_rows * C::kRowBytes;
 #pragma unroll
@@ -433,6 +446,13 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
                       &sm.full[r.stage]);
         }
       }
+      // the stage's one arrival, with the bytes to expect, follows the scales
+      if (mine)
+        for (int g = sub * box_rows / 16; g < (sub + 1) * box_rows / 16; ++g)
+          sm.meta[r.stage][g] = make_float2(ks, vs);
+      __syncwarp();
+      if (lane == 0)
+        tc::mbar_arrive_expect_tx(&sm.full[r.stage], boxes * box_rows * D * 2);
       r.next(C::kStages);
     }
   }
@@ -466,7 +486,8 @@ __device__ __forceinline__ void consume(const AttnArgs& a, const Unit& u, int t0
     for (int i = 0; i < 4; ++i) acc.o[t][i] = 0.0f;
   acc.m[0] = acc.m[1] = -INFINITY;
   acc.l[0] = acc.l[1] = 0.0f;
-  acc.vref = 0x1p-126f;
+  acc.vref = 0x1p-126f;  // any page's scale replaces it
+  acc.up = 0.0f;
   const int pos0 = u.v.first + u.tok0;                      // earliest row
   const int pos1 = pos0 + (u.rows - 1) / a.g;               // latest row
   for (int kt = t0; kt < t1; ++kt) {
@@ -565,21 +586,23 @@ __device__ __forceinline__ void consume(const AttnArgs& a, const Unit& u, int t0
   consumer_sync<D>();
   if (!sm.last) return;
   __threadfence();
+  // the parts' loads are independent: the maximum first, then the weighted sum
   for (int i = tid; i < rows * (D / 4); i += C::kConsumers) {
     const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+    const auto at = [&](int p) {
+      return (size_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kTileRows + row;
+    };
     float m = -INFINITY, l = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, __ldcg(&sp.ml[at(p)].x));
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int p = 0; p < parts; ++p) {
-      const size_t at = (size_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kTileRows + row;
-      const float2 ml = __ldcg(sp.ml + at);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(sp.o + at * D + d));
-      const float mn = fmaxf(m, ml.x);
-      const float fo = m == -INFINITY ? 1.0f : exp2_approx(m - mn);
-      const float fn = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - mn);
-      m = mn;
-      l = l * fo + ml.y * fn;
-      x = make_float4(x.x * fo + y.x * fn, x.y * fo + y.y * fn, x.z * fo + y.z * fn,
-                      x.w * fo + y.w * fn);
+      const float2 ml = __ldcg(sp.ml + at(p));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(sp.o + at(p) * D + d));
+      const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
     }
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     store_out<D>(a, u, out, out_stride, row, d,

@@ -471,7 +471,7 @@ typedef struct {
  * [kv_heads][page_tokens][head_dim] e4m3 codes (16-byte aligned), and one fp32
  * scale per page and head, [n_pages][kv_heads]; a value is code x scale.
  * moe_kv_append writes powers of two; a cache that other code filled may hold
- * any finite positive scales. */
+ * any scales from 2^-100 to 2^100. */
 typedef struct {
   uint8_t* k_codes;
   uint8_t* v_codes;

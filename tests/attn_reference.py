@@ -134,7 +134,8 @@ def attention(shape, q, codes_k, scales_k, codes_v, scales_v, pages, row_start, 
     Tolerance, with A the weighted mean of |v|, per row:
     - the output's rounding to bf16;
     - the weights' rounding to fp16 (relative HALF_FP16 each, so A times that), and the
-      smallest of them lost: 2^-35 of the largest value for each key;
+      smallest of them lost: 2^-35 of the largest value for each key (half of fp16's
+      smallest step, the weights being held as 2^10 times theirs);
     - the scores: the queries are off by up to 2^-17 of their largest value, the products
       accumulate in fp32 (D + 8 half-steps of sum |q k|), the score in log2 units is
       rounded and subtracted in fp32 (4 half-steps of the largest), and the exponential
