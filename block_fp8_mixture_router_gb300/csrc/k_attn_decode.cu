@@ -42,7 +42,8 @@ struct Dec {
   static constexpr int kHalfBytes = kAttnKeys * kRowBytes;
   static constexpr int kTileBytes = kAttnKeys * D;     // keys or values of a stage
   static constexpr int kStages = D == 64 ? 8 : 5;
-  static constexpr int kQStride = D + 64;              // staged query rows, offset by half a phase
+  static constexpr int kQStride = 2 * D + 16;          // staged query rows: eight lanes' pieces
+                                                       // in eight 16-byte columns
   static constexpr bool kQInRegs = D == 64;
 };
 
@@ -104,14 +105,14 @@ __device__ __forceinline__ void unit_range(const AttnArgs& a, Unit& u) {
   u.kt1 = max((int)(((long long)u.hi + kAttnKeys - 1) / kAttnKeys), u.kt0 + 1);
 }
 
-// The queries of a tile as e4m3 operands.  A row's values are scaled by the power
-// of two that brings its largest into [128, 256) and split into a rounded part
-// and the rest, hi + lo: a bf16 value has 8 bits and each part 4, so the two hold
-// it exactly down to 1/4 (2^-9 of the row's largest), and to 2^-10, e4m3's half
-// step (2^-17 of the largest), below.  The tensor cores then take the keys' codes
-// as they are stored.
-// Layout: [hi | lo][16 rows][kQStride bytes]; factor[row] = the score's factor but
-// for the key's scale.
+// The queries of a tile as fp16 operands.  A row's values are scaled by the power
+// of two that brings its largest into [2^14, 2^15): a bf16 value's 8 bits then fit
+// fp16's 11 down to 2^-29 of the row's largest.  (Warp MMAs on e4m3 codes as stored,
+// with the queries split into two e4m3 parts, take longer: sm_103a runs them as fp16
+// MMAs behind conversions of both operands, 440 instructions a step of 16 keys
+// against 300.)
+// Layout: [16 rows][kQStride bytes]; factor[row] = the score's factor but for the
+// key's scale.
 template <int D>
 __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Unit& u, const bf16* q,
                                               int64_t q_stride, uint8_t* sq, float* factor) {
@@ -137,31 +138,16 @@ __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Unit& u, 
     if (odd) mx = __int_as_float(0x7F800000);
 #pragma unroll
     for (int o = kPer / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    uint2 hi, lo;
+    uint4 w = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);  // NaN scores
     float f = 0.0f;
-    if (!is_finite(mx)) {
-      hi = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // NaN scores
-      lo = hi;
-    } else {
+    if (is_finite(mx)) {
       const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-      f = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * a.scale;
-      uint32_t w[2], z[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float x0 = x[4 * i] * up, x1 = x[4 * i + 1] * up, x2 = x[4 * i + 2] * up,
-                    x3 = x[4 * i + 3] * up;
-        w[i] = e4m3x4(x0, x1, x2, x3);
-        const uint32_t h01 = e4m3x2_to_f16x2(w[i]), h23 = e4m3x2_to_f16x2(w[i] >> 16);
-        const float2 b01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-        const float2 b23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-        z[i] = e4m3x4(x0 - b01.x, x1 - b01.y, x2 - b23.x, x3 - b23.y);
-      }
-      hi = make_uint2(w[0], w[1]);
-      lo = make_uint2(z[0], z[1]);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      f = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * a.scale;
+      w = make_uint4(f16x2(x[0] * up, x[1] * up), f16x2(x[2] * up, x[3] * up),
+                     f16x2(x[4] * up, x[5] * up), f16x2(x[6] * up, x[7] * up));
     }
-    *reinterpret_cast<uint2*>(sq + r * Dec<D>::kQStride + 8 * c) = hi;
-    *reinterpret_cast<uint2*>(sq + (kTileRows + r) * Dec<D>::kQStride + 8 * c) = lo;
+    *reinterpret_cast<uint4*>(sq + r * Dec<D>::kQStride + 16 * c) = w;
     if (c == 0) factor[r] = f;
   }
 }
@@ -169,7 +155,7 @@ __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Unit& u, 
 // One CTA's shared memory behind the ring.
 template <int D>
 struct DecSmem {
-  uint8_t q[2 * kTileRows * Dec<D>::kQStride];
+  uint8_t q[kTileRows * Dec<D>::kQStride];
   float o[kTileRows][D];
   float factor[kTileRows];
   float m[4][kTileRows], l[4][kTileRows];
@@ -194,20 +180,35 @@ struct Acc {
   float up;    // kPShift / vref
 };
 
-// The first operand of the score product: rows j and j + 8, hi and lo parts.
+// The first operand of the score product over 64 values: the lane's 16 values of
+// rows j and j + 8.
 struct QFrag {
-  uint4 h0, h1, l0, l1;
+  uint4 lo[2], hi[2];  // rows j, j + 8; first and second eight
 };
 
 template <int D>
 __device__ __forceinline__ QFrag load_q(const uint8_t* sq, int j, int c, int t) {
-  const uint8_t* p = sq + j * Dec<D>::kQStride + 64 * t + 16 * c;
+  const uint8_t* p = sq + j * Dec<D>::kQStride + 128 * t + 32 * c;
   QFrag f;
-  f.h0 = *reinterpret_cast<const uint4*>(p);
-  f.h1 = *reinterpret_cast<const uint4*>(p + 8 * Dec<D>::kQStride);
-  f.l0 = *reinterpret_cast<const uint4*>(p + kTileRows * Dec<D>::kQStride);
-  f.l1 = *reinterpret_cast<const uint4*>(p + (kTileRows + 8) * Dec<D>::kQStride);
+  f.lo[0] = *reinterpret_cast<const uint4*>(p);
+  f.hi[0] = *reinterpret_cast<const uint4*>(p + 16);
+  f.lo[1] = *reinterpret_cast<const uint4*>(p + 8 * Dec<D>::kQStride);
+  f.hi[1] = *reinterpret_cast<const uint4*>(p + 8 * Dec<D>::kQStride + 16);
   return f;
+}
+
+// Scores of 64 values: the order of a dot product is free, so the lane's 16 key
+// bytes serve as four MMAs' labels 2c, 2c+1, 2c+8, 2c+9 in turn, and the queries'
+// values alike.
+__device__ __forceinline__ void mma_q_k64(float (&d)[4], const QFrag& f, const uint4& k) {
+  mma_f16(d, f.lo[0].x, f.lo[1].x, f.lo[0].y, f.lo[1].y, e4m3x2_to_f16x2(k.x),
+          e4m3x2_to_f16x2(k.x >> 16));
+  mma_f16(d, f.lo[0].z, f.lo[1].z, f.lo[0].w, f.lo[1].w, e4m3x2_to_f16x2(k.y),
+          e4m3x2_to_f16x2(k.y >> 16));
+  mma_f16(d, f.hi[0].x, f.hi[1].x, f.hi[0].y, f.hi[1].y, e4m3x2_to_f16x2(k.z),
+          e4m3x2_to_f16x2(k.z >> 16));
+  mma_f16(d, f.hi[0].z, f.hi[1].z, f.hi[0].w, f.hi[1].w, e4m3x2_to_f16x2(k.w),
+          e4m3x2_to_f16x2(k.w >> 16));
 }
 
 // 16 keys of one page, warp-wide: scores, weights, and the weighted values.
@@ -234,8 +235,7 @@ __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<
     for (int n = 0; n < 2; ++n) {
       const uint4 k = *reinterpret_cast<const uint4*>(
           kp + (t >> 1) * Dec<D>::kHalfBytes + swz<D>(key_row(n, j), 4 * (t & 1) + c));
-      mma_e4m3_k64(s[n], f.h0, f.h1, k);
-      mma_e4m3_k64(s[n], f.l0, f.l1, k);
+      mma_q_k64(s[n], f, k);
     }
   }
   // value rows of the lane's four keys: key_row(0, 2c), (0, 2c+1), (1, 2c), (1, 2c+1)
