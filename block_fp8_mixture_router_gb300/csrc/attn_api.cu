@@ -223,7 +223,7 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const int seq_rows = b->max_seq_rows > 0 ? std::min(b->max_seq_rows, b->rows) : b->rows;
   const int tq = kDecTileRows / a.g;
   const long long units = (long long)b->rows / tq + b->n_seqs;  // per key head, at most
-  // Few row tiles: the key tiles of all of them in equal runs, at least four
+  // Few row tiles: the key tiles of all of them in equal runs, at least two
   // (256 keys) to a CTA.  Many: a CTA per row tile.
   const bool split = units <= 2048 && (seq_rows + tq - 1) / tq <= 64;
   long long grid = units * a.Hkv;
@@ -231,7 +231,7 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
     long long span = keys;
     if (a.window) span = std::min<long long>(span, (long long)a.window + tq + kAttnKeys);
     const long long tiles = units * a.Hkv * ((span + kAttnKeys - 1) / kAttnKeys);
-    grid = std::max<long long>(1, std::min<long long>((tiles + 3) / 4, c->dec_slots));
+    grid = std::max<long long>(1, std::min<long long>((tiles + 1) / 2, c->dec_slots));
   }
   AttnMaps maps;
   if (!make_attn_maps(&maps, a, D)) return MOE_ERR_CUDA;

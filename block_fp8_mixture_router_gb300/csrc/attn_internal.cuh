@@ -8,7 +8,7 @@ namespace moe {
 constexpr int kAttnMaxGroup = 16;     // query heads of one key head
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxTokens = 0x7FFF0000;  // positions and a tile behind them fit an int
-constexpr int kAttnKeys = 64;         // keys of one step of the decode kernel
+constexpr int kAttnKeys = 128;        // keys of a tile of the decode kernel
 constexpr int kScaleMinExp = -100;    // the smallest block scale is 2^-100
 
 // Device status word bits.
@@ -74,7 +74,7 @@ struct AppendArgs {
 cudaError_t launch_append(int D, const AttnArgs& a, const AppendArgs& p, cudaStream_t s);
 
 // The cache's codes as the TMA sees them: [page][kv_heads x page_tokens][head_dim],
-// a box of min(page_tokens, 64) tokens of a head, 128 bytes of each (64 at
+// a box of a page's tokens of a head, 128 bytes of each (64 at
 // head_dim 64), stored with the swizzle of that width.
 struct AttnMaps {
   CUtensorMap k, v;

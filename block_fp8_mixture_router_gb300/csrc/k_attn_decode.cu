@@ -8,8 +8,8 @@
 // rows: the g query heads of a key head times 16/g tokens.
 //
 // Bound by the cache's bytes: a CTA has a producer warp that keeps a ring of
-// kStages key tiles (64 keys and their values, 16 KB at head_dim 128) filled by
-// TMA, and four consumer warps that take 16 keys of a tile each; at head_dim 256
+// kStages key tiles (128 keys and their values, 32 KB at head_dim 128) filled by
+// TMA, and four consumer warps that take 32 keys of a tile each; at head_dim 256
 // a second set of four takes the other half of the output.  The tiles lie in
 // shared memory with the TMA's swizzle, and a lane's keys are chosen (key_row) so
 // that the eight lanes of a shared-memory phase read eight different 16-byte
@@ -22,6 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kTileRows = 16;
+constexpr int kPair = 2;            // groups of 16 keys that a warp takes of a tile
 // Weights are held as p x 2^10 in fp16, and p is taken against a maximum that may
 // lag the true one by kLag powers of two: a row's sums are only scaled again where its
 // scores outgrow that, and 2^(10 + kLag) is still half of fp16's range.  fp16's
@@ -41,7 +42,7 @@ struct Dec {
   static constexpr int kRowBytes = D < 128 ? D : 128;  // a stored row (of a half) and its swizzle
   static constexpr int kHalfBytes = kAttnKeys * kRowBytes;
   static constexpr int kTileBytes = kAttnKeys * D;     // keys or values of a stage
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kStages = D == 64 ? 5 : 3;
   static constexpr int kQStride = 2 * D + 16;          // staged query rows: eight lanes' pieces
                                                        // in eight 16-byte columns
   static constexpr bool kQInRegs = D == 64;
@@ -159,7 +160,7 @@ struct DecSmem {
   float o[kTileRows][D];
   float factor[kTileRows];
   float m[4][kTileRows], l[4][kTileRows];
-  float2 meta[Dec<D>::kStages][4];  // scales of the keys and values of 16 keys of a stage
+  float2 meta[Dec<D>::kStages][kAttnKeys / 16];  // scales of 16 keys and their values
   uint64_t full[Dec<D>::kStages], empty[Dec<D>::kStages];
   int last, abort, seq, tile;
   long long front;
@@ -211,96 +212,93 @@ __device__ __forceinline__ void mma_q_k64(float (&d)[4], const QFrag& f, const u
           e4m3x2_to_f16x2(k.w >> 16));
 }
 
-// 16 keys of one page, warp-wide: scores, weights, and the weighted values.
-// key0: position of the first; kp, vp: the stage's key rows and the rows of the
-// warp's half of the values, row0 the first of the sixteen in the stage.  kEdge:
-// some keys are unseen by some rows (or lie behind the cache's last token).
+// Weighted values of 16 keys: V's fragments straight from its rows, a pair of keys'
+// bytes interleaved and widened for each MMA.
+template <int D>
+__device__ __forceinline__ void add_values(Acc<D>& acc, const uint32_t (&p16)[4],
+                                           const uint32_t (&vw)[4][Dec<D>::kVBytes / 4]) {
+#pragma unroll
+  for (int i = 0; i < Dec<D>::kVBytes / 4; ++i) {
+    const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140);
+    const uint32_t a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
+    const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140);
+    const uint32_t b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+    mma_f16(acc.o[4 * i], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a01),
+            e4m3x2_to_f16x2(b01));
+    mma_f16(acc.o[4 * i + 1], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a01 >> 16),
+            e4m3x2_to_f16x2(b01 >> 16));
+    mma_f16(acc.o[4 * i + 2], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a23),
+            e4m3x2_to_f16x2(b23));
+    mma_f16(acc.o[4 * i + 3], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a23 >> 16),
+            e4m3x2_to_f16x2(b23 >> 16));
+  }
+}
+
+// kPair groups of 16 keys (each of one page), warp-wide: scores, weights, and the
+// weighted values.  key0: position of the first; kp, vp: the stage's key rows and the
+// rows of the warp's half of the values; sc: the groups' scales.  kEdge: some keys
+// are unseen by some rows, lie behind the cache's last token, or belong to a page that
+// does not exist (there: bit g of `there` clear).
 template <int D, bool kEdge>
 __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<D>& acc,
                                           const QFrag* qf, const uint8_t* sq,
                                           const float (&fac)[2], int key0, const uint8_t* kp,
-                                          const uint8_t* vp, float ksc, float vsc) {
+                                          const uint8_t* vp, const float2 (&sc)[kPair],
+                                          uint32_t there) {
   const int lane = threadIdx.x & 31, j = lane >> 2, c = lane & 3;
   constexpr int S = Dec<D>::kSlices;
-  const int limit = u.v.len - key0;  // keys of this step that exist
-  float s[2][4];
+  float s[kPair][2][4];
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
+  for (int g = 0; g < kPair; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[g][n][i] = 0.0f;
 #pragma unroll
   for (int t = 0; t < S; ++t) {
     const QFrag f = Dec<D>::kQInRegs ? qf[t] : load_q<D>(sq, j, c, t);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint4 k = *reinterpret_cast<const uint4*>(
-          kp + (t >> 1) * Dec<D>::kHalfBytes + swz<D>(key_row(n, j), 4 * (t & 1) + c));
-      mma_q_k64(s[n], f, k);
-    }
-  }
-  // value rows of the lane's four keys: key_row(0, 2c), (0, 2c+1), (1, 2c), (1, 2c+1)
-  constexpr int W = Dec<D>::kVBytes / 4;
-  uint32_t vw[4][W];
+    for (int g = 0; g < kPair; ++g)
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int key = key_row(k >> 1, 2 * c + (k & 1));
-    const bool on = !kEdge || key < limit;
-    if constexpr (W == 2) {
-      const uint2 x = *reinterpret_cast<const uint2*>(vp + swz<D>(key, j >> 1) + 8 * (j & 1));
-      vw[k][0] = on ? x.x : 0;
-      vw[k][1] = on ? x.y : 0;
-    } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(vp + swz<D>(key, j));
-      vw[k][0] = on ? x.x : 0;
-      vw[k][1] = on ? x.y : 0;
-      vw[k][2] = on ? x.z : 0;
-      vw[k][3] = on ? x.w : 0;
-    }
-  }
-  uint32_t poison = 0;  // bit k: the lane's k-th key has a NaN value
-  if constexpr (kEdge) {
-    // an unseen key's weight is 0, but 0 x NaN is not: NaN codes become zeros here,
-    // and the rows that do see the key get a NaN score instead
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const uint32_t bad = e4m3_nan_bytes(vw[k][i]);
-        if (bad) {
-          poison |= 1u << k;
-          vw[k][i] &= ~((bad >> 7) * 0xFFu);
-        }
-      }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) poison |= __shfl_xor_sync(0xffffffffu, poison, o);
+      for (int n = 0; n < 2; ++n)
+        mma_q_k64(s[g][n], f,
+                  *reinterpret_cast<const uint4*>(kp + (t >> 1) * Dec<D>::kHalfBytes +
+                                                  g * 16 * Dec<D>::kRowBytes +
+                                                  swz<D>(key_row(n, j), 4 * (t & 1) + c)));
   }
   // the rows' factors to log2 units; which keys they see; whether a score outgrew
-  // the row's reference
-  const float f[2] = {fac[0] * ksc, fac[1] * ksc};
-  bool seen[2][4];
-  float mx[2];
-  bool grow = vsc > acc.vref;
+  // the row's reference, or a page's scale the largest so far
+  uint32_t seen[2] = {~0u, ~0u};  // bits 4 g + k of rows j, j + 8
+  float f[kPair][2], mx[2] = {-INFINITY, -INFINITY}, top = 0.0f;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    mx[r] = -INFINITY;
-    if constexpr (kEdge) {
-      const int pos = u.v.first + u.tok0 + (j + 8 * r) / a.g;
+  for (int g = 0; g < kPair; ++g) {
+    if (!kEdge || ((there >> g) & 1)) top = fmaxf(top, sc[g].y);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = key0 + key_row(k >> 1, 2 * c + (k & 1));
-        seen[r][k] = key <= pos && key < u.v.len && (!a.window || key > pos - a.window);
-        if (seen[r][k]) mx[r] = fmaxf(mx[r], s[k >> 1][2 * r + (k & 1)]);
+    for (int r = 0; r < 2; ++r) {
+      f[g][r] = fac[r] * sc[g].x;
+      float m = -INFINITY;
+      if constexpr (kEdge) {
+        const int pos = u.v.first + u.tok0 + (j + 8 * r) / a.g;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + 16 * g + key_row(k >> 1, 2 * c + (k & 1));
+          const bool on = ((there >> g) & 1) && key <= pos && key < u.v.len &&
+                          (!a.window || key > pos - a.window);
+          if (on) m = fmaxf(m, s[g][k >> 1][2 * r + (k & 1)]);
+          else seen[r] &= ~(1u << (4 * g + k));
+        }
+      } else {
+        m = fmaxf(fmaxf(s[g][0][2 * r], s[g][0][2 * r + 1]),
+                  fmaxf(s[g][1][2 * r], s[g][1][2 * r + 1]));
       }
-    } else {
-      mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      if (m != -INFINITY) mx[r] = fmaxf(mx[r], m * f[g][r]);
     }
-    mx[r] = mx[r] == -INFINITY ? mx[r] : mx[r] * f[r];
-    grow |= mx[r] > acc.m[r] + kLag;
   }
+  const bool grow = top > acc.vref || mx[0] > acc.m[0] + kLag || mx[1] > acc.m[1] + kLag;
   if (__any_sync(0xffffffffu, grow)) {
     // new references: the rows' running maxima, and the largest page scale so far
-    const float vf = vsc > acc.vref ? __fdiv_rn(acc.vref, vsc) : 1.0f;
-    acc.vref = fmaxf(acc.vref, vsc);
+    const float vf = top > acc.vref ? __fdiv_rn(acc.vref, top) : 1.0f;
+    acc.vref = fmaxf(acc.vref, top);
     acc.up = __fdiv_rn(kPShift, acc.vref);
     float corr[2];
 #pragma unroll
@@ -321,44 +319,71 @@ __device__ __forceinline__ void warp_keys(const AttnArgs& a, const Unit& u, Acc<
       acc.o[t][3] *= corr[1];
     }
   }
-  // the weights carry the page's scale in their exponent, and the sum of them is
-  // freed of it again; a page below 2^-70 of the largest adds no value that counts
-  const float w = fmaxf(vsc * acc.up, 0x1p-60f);
-  float lw, w_inv;
-  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(lw) : "f"(w));
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(w_inv) : "f"(w));
-  uint32_t p16[4];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const float base = acc.m[r] == -INFINITY ? lw : lw - acc.m[r];
-    float p[4], sum = 0.0f;
+  for (int g = 0; g < kPair; ++g) {
+    // value rows of the lane's four keys: key_row(0, 2c), (0, 2c+1), (1, 2c), (1, 2c+1)
+    constexpr int W = Dec<D>::kVBytes / 4;
+    const int limit = !kEdge ? 16 : ((there >> g) & 1) ? u.v.len - key0 - 16 * g : 0;
+    uint32_t vw[4][W];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      p[k] = exp2_approx(fmaf(s[k >> 1][2 * r + (k & 1)], f[r], base));
-      if constexpr (kEdge) {
-        if (poison & (1u << k)) p[k] = __int_as_float(0x7FFFFFFF);
-        if (!seen[r][k]) p[k] = 0.0f;
+      const int key = key_row(k >> 1, 2 * c + (k & 1));
+      const bool on = !kEdge || key < limit;
+      const uint8_t* p = vp + g * 16 * Dec<D>::kRowBytes;
+      if constexpr (W == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + swz<D>(key, j >> 1) + 8 * (j & 1));
+        vw[k][0] = on ? x.x : 0;
+        vw[k][1] = on ? x.y : 0;
+      } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(p + swz<D>(key, j));
+        vw[k][0] = on ? x.x : 0;
+        vw[k][1] = on ? x.y : 0;
+        vw[k][2] = on ? x.z : 0;
+        vw[k][3] = on ? x.w : 0;
       }
-      sum += p[k];
     }
-    acc.l[r] = fmaf(sum, w_inv, acc.l[r]);
-    p16[r] = f16x2(p[0], p[1]);
-    p16[2 + r] = f16x2(p[2], p[3]);
-  }
+    uint32_t poison = 0;  // bit k: the lane's k-th key has a NaN value
+    if constexpr (kEdge) {
+      // an unseen key's weight is 0, but 0 x NaN is not: NaN codes become zeros here,
+      // and the rows that do see the key get a NaN weight instead
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140);
-    const uint32_t a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
-    const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140);
-    const uint32_t b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
-    mma_f16(acc.o[4 * i], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a01),
-            e4m3x2_to_f16x2(b01));
-    mma_f16(acc.o[4 * i + 1], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a01 >> 16),
-            e4m3x2_to_f16x2(b01 >> 16));
-    mma_f16(acc.o[4 * i + 2], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a23),
-            e4m3x2_to_f16x2(b23));
-    mma_f16(acc.o[4 * i + 3], p16[0], p16[1], p16[2], p16[3], e4m3x2_to_f16x2(a23 >> 16),
-            e4m3x2_to_f16x2(b23 >> 16));
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const uint32_t bad = e4m3_nan_bytes(vw[k][i]);
+          if (bad) {
+            poison |= 1u << k;
+            vw[k][i] &= ~((bad >> 7) * 0xFFu);
+          }
+        }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) poison |= __shfl_xor_sync(0xffffffffu, poison, o);
+    }
+    // the weights carry the page's scale in their exponent, and the sum of them is
+    // freed of it again; a page below 2^-70 of the largest adds no value that counts
+    const float w = fmaxf(sc[g].y * acc.up, 0x1p-60f);
+    float lw, w_inv;
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(lw) : "f"(w));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(w_inv) : "f"(w));
+    uint32_t p16[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float base = acc.m[r] == -INFINITY ? lw : lw - acc.m[r];
+      float p[4], sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        p[k] = exp2_approx(fmaf(s[g][k >> 1][2 * r + (k & 1)], f[g][r], base));
+        if constexpr (kEdge) {
+          if (poison & (1u << k)) p[k] = __int_as_float(0x7FFFFFFF);
+          if (!(seen[r] & (1u << (4 * g + k)))) p[k] = 0.0f;
+        }
+        sum += p[k];
+      }
+      acc.l[r] = kEdge && !((there >> g) & 1) ? acc.l[r] : fmaf(sum, w_inv, acc.l[r]);
+      p16[r] = f16x2(p[0], p[1]);
+      p16[2 + r] = f16x2(p[2], p[3]);
+    }
+    add_values<D>(acc, p16, vw);
   }
 }
 
@@ -372,6 +397,11 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, const Unit& u, bf16
   w.x = *reinterpret_cast<const uint32_t*>(&p0);
   w.y = *reinterpret_cast<const uint32_t*>(&p1);
   *reinterpret_cast<uint2*>(out + (int64_t)row * out_stride + (u.h * a.g + r % a.g) * D + d) = w;
+}
+
+// a / b for a, b >= 0: a 32-bit division wherever both fit.
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Barrier of the consumer warps.
@@ -492,16 +522,25 @@ __device__ __forceinline__ void consume(const AttnArgs& a, const Unit& u, int t0
   const int pos1 = pos0 + (u.rows - 1) / a.g;               // latest row
   for (int kt = t0; kt < t1; ++kt) {
     tc::wait_bounded(&sm.full[r.stage], r.phase, &sm.abort, a.status);
-    const int key0 = kt * kAttnKeys + grp * 16;
-    const float2 sc = sm.meta[r.stage][grp];
-    if (key0 < u.hi && key0 + 16 > u.lo && sc.x >= 0.0f) {
-      const uint8_t* kp = ring + (size_t)r.stage * 2 * C::kTileBytes + grp * 16 * C::kRowBytes;
+    const int key0 = kt * kAttnKeys + grp * 16 * kPair;
+    if (key0 < u.hi && key0 + 16 * kPair > u.lo) {
+      float2 sc[kPair];
+      uint32_t there = 0;
+#pragma unroll
+      for (int g = 0; g < kPair; ++g) {
+        sc[g] = sm.meta[r.stage][kPair * grp + g];
+        const int k = key0 + 16 * g;
+        if (k < u.hi && k + 16 > u.lo && sc[g].x >= 0.0f) there |= 1u << g;
+      }
+      const uint8_t* kp =
+          ring + (size_t)r.stage * 2 * C::kTileBytes + grp * 16 * kPair * C::kRowBytes;
       const uint8_t* vp = kp + C::kTileBytes + half * C::kHalfBytes;
-      const bool edge = key0 + 15 > pos0 || (a.window && key0 <= pos1 - a.window);
+      const bool edge = key0 + 16 * kPair - 1 > pos0 ||
+                        (a.window && key0 <= pos1 - a.window) || there != (1u << kPair) - 1;
       if (edge)
-        warp_keys<D, true>(a, u, acc, qf, sm.q, fac, key0, kp, vp, sc.x, sc.y);
+        warp_keys<D, true>(a, u, acc, qf, sm.q, fac, key0, kp, vp, sc, there);
       else
-        warp_keys<D, false>(a, u, acc, qf, sm.q, fac, key0, kp, vp, sc.x, sc.y);
+        warp_keys<D, false>(a, u, acc, qf, sm.q, fac, key0, kp, vp, sc, there);
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.empty[r.stage]);
@@ -687,7 +726,7 @@ __global__ void __launch_bounds__(Dec<D>::kThreads, D == 256 ? 1 : 2)
       total += sm.scan[w];
     }
     if (total == 0) return;
-    per = (total + gridDim.x - 1) / gridDim.x;
+    per = div_ll(total + gridDim.x - 1, gridDim.x);
     begin = per * blockIdx.x;
     end = min(begin + per, total);
     if (begin >= end) return;
@@ -717,7 +756,7 @@ __global__ void __launch_bounds__(Dec<D>::kThreads, D == 256 ? 1 : 2)
     f = sm.front;  // tiles in front of (sequence, row tile)
     u.v = seq_view(a, u.s);
     unit_range(a, u);
-    u.h = (int)((begin - f) / (u.kt1 - u.kt0));
+    u.h = (int)div_ll(begin - f, u.kt1 - u.kt0);
   }
   pdl_wait();
   long long at = begin;
@@ -730,7 +769,7 @@ __global__ void __launch_bounds__(Dec<D>::kThreads, D == 256 ? 1 : 2)
       produce<D>(a, u, t0, t1, &kmap, &vmap, ring, sm, r);
     } else {
       const bool whole = at == u_first && stop == u_first + w;
-      const int c0 = (int)(u_first / per), c1 = (int)((u_first + w - 1) / per);
+      const int c0 = (int)div_ll(u_first, per), c1 = (int)div_ll(u_first + w - 1, per);
       const int slot = at == u_first ? 2 * c0 + 1 : 2 * (int)blockIdx.x;
       consume<D>(a, u, t0, t1, whole, slot, c0, c1 - c0 + 1, q, q_stride, out, out_stride, sp, ring,
                  sm, r);
