@@ -221,7 +221,9 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const long long cap = (long long)b->pages_stride << c->page_shift;
   const long long keys = b->max_kv_len > 0 ? std::min<long long>(b->max_kv_len, cap) : cap;
   const int seq_rows = b->max_seq_rows > 0 ? std::min(b->max_seq_rows, b->rows) : b->rows;
-  const int tq = kDecTileRows / a.g;
+  // eight rows to a tile where one holds a sequence's: less work per key
+  const int tile_rows = (long long)seq_rows * a.g <= 8 ? 8 : kDecTileRows;
+  const int tq = tile_rows / a.g;
   const long long units = (long long)b->rows / tq + b->n_seqs;  // per key head, at most
   // Few row tiles: the key tiles of all of them in equal runs, at least two
   // (256 keys) to a CTA.  Many: a CTA per row tile.
@@ -235,7 +237,7 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   }
   AttnMaps maps;
   if (!make_attn_maps(&maps, a, D)) return MOE_ERR_CUDA;
-  return launch_attn_decode(D, a, maps, q, q_stride, out, out_stride, c->split, (int)grid, split, pdl,
+  return launch_attn_decode(D, tile_rows, a, maps, q, q_stride, out, out_stride, c->split, (int)grid, split, pdl,
                             s) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;

@@ -83,8 +83,9 @@ bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D);
 
 cudaError_t setup_attn_decode(int D);
 int attn_decode_slots(int D, int sm_count);  // CTAs of a full grid
-cudaError_t launch_attn_decode(int D, const AttnArgs& a, const AttnMaps& m, const bf16* q,
-                               int64_t q_stride, bf16* out, int64_t out_stride,
+// tile_rows: 8 (at most eight query heads of a key head) or 16.
+cudaError_t launch_attn_decode(int D, int tile_rows, const AttnArgs& a, const AttnMaps& m,
+                               const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
                                const AttnSplit& sp, int grid, bool split, bool pdl,
                                cudaStream_t s);
 

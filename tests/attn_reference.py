@@ -133,9 +133,8 @@ def attention(shape, q, codes_k, scales_k, codes_v, scales_v, pages, row_start, 
 
     Tolerance, with A the weighted mean of |v|, per row:
     - the output's rounding to bf16;
-    - the weights' rounding to fp16 (relative HALF_FP16 each, so A times that), and the
-      smallest of them lost: 2^-35 of the largest value for each key (half of fp16's
-      smallest step, the weights being held as 2^10 times theirs);
+    - the weights' rounding to 11 bits (relative HALF_FP16 each, so A times that), and
+      the smallest of them lost: 2^-30 of the largest value for each key;
     - the scores: the queries are off by up to 2^-17 of their largest value, the products
       accumulate in fp32 (D + 8 half-steps of sum |q k|), the score in log2 units is
       rounded and subtracted in fp32 (4 half-steps of the largest), and the exponential
@@ -178,5 +177,5 @@ def attention(shape, q, codes_k, scales_k, codes_v, scales_v, pages, row_start, 
                      4 * HALF_FP32 * sc.abs().amax(-1) * 1.4427 + 2.0 ** -22)
                 tol[r0 + i, h * g:(h + 1) * g] = (
                     HALF_BF16 * o.abs() + A * (HALF_FP16 + 2 * d[:, None]) +
-                    int(m.sum()) * 2.0 ** -35 * v[m].abs().max())
+                    int(m.sum()) * 2.0 ** -30 * v[m].abs().max())
     return out, tol
