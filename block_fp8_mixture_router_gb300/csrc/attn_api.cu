@@ -32,10 +32,7 @@ struct moe_attn {
 
 namespace {
 
-// CTAs that a decode grid can hold: the split buffers are sized for this many,
-// whatever the device's occupancy turns out to be.
-constexpr int kMaxDecSlots = 1024;
-constexpr int kDecTileRows = 16;
+constexpr int kDecTileRows = kAttnSlotRows;
 
 struct Device {
   int prev = -1;
@@ -80,20 +77,20 @@ bool supported(const moe_attn_config* c) {
 
 // Byte sizes of everything a context allocates, in order.
 struct Sizes {
-  size_t turns, q, part_o, part_ml, arrived, status;
-  size_t total() const { return turns + q + part_o + part_ml + arrived + status; }
+  size_t turns, q, part_o, part_ml, shared, status;
+  size_t total() const { return turns + q + part_o + part_ml + shared + status; }
 };
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 Sizes sizes_of(const moe_attn_config* c) {
   Sizes s;
-  const size_t slots = 2 * (size_t)kMaxDecSlots;
+  const size_t slots = 2 * (size_t)kAttnMaxCtas;
   s.turns = up256((size_t)std::max(c->rotary_dim / 2, 1) * 8);
   s.q = up256((size_t)c->max_rows * c->q_heads * c->head_dim * 2);
   s.part_o = up256(slots * kDecTileRows * c->head_dim * 4);
   s.part_ml = up256(slots * kDecTileRows * 8);
-  s.arrived = up256(slots * 4);
+  s.shared = up256((size_t)kAttnMaxCtas * 16);
   s.status = 256;
   return s;
 }
@@ -282,7 +279,7 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out) {
   while ((1 << c->page_shift) < cfg->page_tokens) ++c->page_shift;
   bool ok = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, device) ==
             cudaSuccess;
-  const size_t bytes[6] = {z.turns, z.q, z.part_o, z.part_ml, z.arrived, z.status};
+  const size_t bytes[6] = {z.turns, z.q, z.part_o, z.part_ml, z.shared, z.status};
   void* p[6] = {};
   try {
     c->allocs.reserve(6);
@@ -295,16 +292,15 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out) {
       c->q = static_cast<bf16*>(p[1]);
       c->split.o = static_cast<float*>(p[2]);
       c->split.ml = static_cast<float2*>(p[3]);
-      c->split.arrived = static_cast<int*>(p[4]);
+      c->split.shared = static_cast<int4*>(p[4]);
       c->status = static_cast<int*>(p[5]);
       const std::vector<unsigned long long> t = turn_table(*cfg);
       ok = cudaMemcpy(p[0], t.data(), t.size() * 8, cudaMemcpyHostToDevice) == cudaSuccess &&
-           cudaMemset(p[4], 0, z.arrived) == cudaSuccess &&
            cudaMemset(p[5], 0, z.status) == cudaSuccess &&
            cudaDeviceSynchronize() == cudaSuccess &&
            setup_attn_decode(cfg->head_dim) == cudaSuccess;
     }
-    if (ok) c->dec_slots = std::min(attn_decode_slots(cfg->head_dim, c->sm_count), kMaxDecSlots);
+    if (ok) c->dec_slots = std::min(attn_decode_slots(cfg->head_dim, c->sm_count), kAttnMaxCtas);
   } catch (const std::bad_alloc&) {
     ok = false;
   }

@@ -45,13 +45,16 @@ struct RopeArgs {
   float amp;
 };
 
-// Partial results of a key range that one CTA worked through, merged by the
-// last CTA of a unit to arrive.
+// Partial results of key ranges that CTAs of one launch worked through: CTA c has
+// slots 2c and 2c + 1 of kAttnSlotRows rows.
 struct AttnSplit {
-  float* o;        // [slots][rows of a tile][D]
-  float2* ml;      // [slots][rows of a tile]: running maximum (log2) and sum
-  int* arrived;    // counters, zero between launches
+  float* o;        // [slots][kAttnSlotRows][D]: weighted sums of the values
+  float2* ml;      // [slots][kAttnSlotRows]: the rows' references (log2) and sums
+  int4* shared;    // [CTAs]: the unit that begins in this CTA and goes on in others:
+                   // its parts (0: none), rows, first row, key head
 };
+constexpr int kAttnSlotRows = 16;
+constexpr int kAttnMaxCtas = 512;  // CTAs of a launch that splits units
 
 cudaError_t launch_rope(int D, const bf16* x, int64_t x_stride, int heads, const int* positions,
                         const bf16* gamma, float eps, int rows, bf16* y, int64_t y_stride,

@@ -29,7 +29,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kSlotRows = 16;       // rows of a partial result's slot
 constexpr int kThreads = 192;       // four softmax warps, the MMA warp, the TMA warp
 constexpr int kSoftmax = 128;
 constexpr int kMmaWarp = 4;
@@ -40,7 +39,6 @@ constexpr int kTmaWarp = 5;
 constexpr float kPShift = 4096.0f;
 constexpr float kLag = 3.0f;
 constexpr int kParts = 4;
-constexpr int kMergeParts = 32;     // parts whose weights lie in shared memory at a time
 
 template <int D>
 struct Dec {
@@ -93,7 +91,7 @@ struct DecSmem {
   uint64_t full[Dec<D>::kStages], empty[Dec<D>::kStages];
   uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done;
   uint32_t tmem;
-  int last, abort, seq, tile;
+  int abort, seq, tile;
   long long front;
   long long scan[kThreads / 32];
 };
@@ -358,19 +356,18 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 
 // The softmax warps' part of key tiles [t0, t1) of a unit.  whole: they are all of
 // the unit's, and the output is written; else the partial result goes to slot
-// `slot`, and the last of the `parts` CTAs to arrive at counter `c0` merges them all
-// in order (the first part lies in slot 2 c0 + 1, the others in 2 (c0 + i)).
+// `slot` for k_attn_merge.
 template <int D, int R>
 __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0, int t1,
-                                       bool whole, int slot, int c0, int parts, const bf16* q,
-                                       int64_t q_stride, bf16* out, int64_t out_stride,
-                                       const AttnSplit& sp, uint8_t* ring, uint32_t tmem_base,
-                                       DecSmem<D>& sm, Phases& ph) {
+                                       bool whole, int slot, const bf16* q, int64_t q_stride,
+                                       bf16* out, int64_t out_stride, const AttnSplit& sp,
+                                       uint8_t* ring, uint32_t tmem_base, DecSmem<D>& sm,
+                                       Phases& ph) {
   using C = Dec<D>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t tmem = tmem_base + ((uint32_t)(warp * 32) << 16);  // this warp's lanes
   int* abort = &sm.abort;
-  softmax_sync();  // the last segment's merge has read what is written now
+  softmax_sync();  // the last segment's sums have been read
   stage_queries<D, R>(a, u, q, q_stride, sm);
   tc::fence_async_smem();
   softmax_sync();
@@ -583,99 +580,23 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
             out[(int64_t)(u.v.row0 + u.tok0 + tok) * out_stride + (u.h * a.g + r - tok * a.g) * D +
                 d] = __float2bfloat16_rn(o * inv);
           } else {
-            __stcg(sp.o + ((size_t)slot * kSlotRows + r) * D + d, o);
+            __stcg(sp.o + ((size_t)slot * kAttnSlotRows + r) * D + d, o);
           }
         }
       }
     }
   }
   tc::fence_before_sync();
-  if (whole) return;
-  if (tid < u.rows)
-    __stcg(sp.ml + (size_t)slot * kSlotRows + tid,
+  if (!whole && tid < u.rows)
+    __stcg(sp.ml + (size_t)slot * kAttnSlotRows + tid,
            make_float2(sm.m[tid], sm.l[0][tid] + sm.l[1][tid] + sm.l[2][tid] + sm.l[3][tid]));
-  __threadfence();
-  softmax_sync();
-  if (tid == 0) {
-    const int n = atomicAdd(sp.arrived + c0, 1);
-    sm.last = n == parts - 1;
-    if (sm.last) sp.arrived[c0] = 0;
-  }
-  softmax_sync();
-  if (!sm.last) return;
-  __threadfence();
-  const auto at = [&](int p, int r) {
-    return (size_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kSlotRows + r;
-  };
-  // the rows' references over all parts: thread (p, r) takes every eighth part
-  const int rows = u.rows, mr = tid & 15;
-  float m = -INFINITY;
-  if (mr < rows)
-#pragma unroll 4
-    for (int p = tid >> 4; p < parts; p += 8) m = fmaxf(m, __ldcg(&sp.ml[at(p, mr)].x));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-  if (lane < 16) sm.l[warp][mr] = m;
-  softmax_sync();
-  m = fmaxf(fmaxf(sm.l[0][mr], sm.l[1][mr]), fmaxf(sm.l[2][mr], sm.l[3][mr]));
-  // weighted sums, a chunk of parts at a time; the parts' weights and weighted row
-  // sums lie where the weights of the keys did
-  constexpr int kItems = (R * (D / 4) + kSoftmax - 1) / kSoftmax;
-  float2(*wl)[16] = reinterpret_cast<float2(*)[16]>(sm.p);
-  float4 x[kItems];
-  float sum[kItems];
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    sum[i] = 0.0f;
-  }
-  for (int b = 0; b < parts; b += kMergeParts) {
-    const int n = min(kMergeParts, parts - b);
-    softmax_sync();
-    if (mr < rows)
-#pragma unroll
-      for (int i = 0; i < kMergeParts / 8; ++i) {
-        const int p = (tid >> 4) + 8 * i;
-        if (p < n) {
-          const float2 ml = __ldcg(sp.ml + at(b + p, mr));
-          const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
-          wl[p][mr] = make_float2(f, ml.y * f);
-        }
-      }
-    softmax_sync();
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int e = tid + i * kSoftmax, row = e / (D / 4), d = (e % (D / 4)) * 4;
-      if (row >= rows) continue;
-#pragma unroll 8
-      for (int p = 0; p < n; ++p) {
-        const float4 y =
-            __ldcg(reinterpret_cast<const float4*>(sp.o + at(b + p, row) * D + d));
-        const float2 f = wl[p][row];
-        sum[i] += f.y;
-        x[i] = make_float4(fmaf(y.x, f.x, x[i].x), fmaf(y.y, f.x, x[i].y),
-                           fmaf(y.z, f.x, x[i].z), fmaf(y.w, f.x, x[i].w));
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const int e = tid + i * kSoftmax, row = e / (D / 4), d = (e % (D / 4)) * 4;
-    if (row >= rows) continue;
-    const float inv = sum[i] == 0.0f ? 0.0f : __fdividef(1.0f, sum[i]);
-    const int tok = row / a.g;
-    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[i].x * inv, x[i].y * inv);
-    const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[i].z * inv, x[i].w * inv);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t*>(&y0);
-    w.y = *reinterpret_cast<const uint32_t*>(&y1);
-    *reinterpret_cast<uint2*>(out + (int64_t)(u.v.row0 + u.tok0 + tok) * out_stride +
-                              (u.h * a.g + row - tok * a.g) * D + d) = w;
-  }
 }
 
 // kSplit: the key tiles of all units, in unit order, are dealt to the CTAs in
-// equal runs, whatever the sequences' lengths are; a unit that several CTAs share
-// is merged by the last of them.  Else a CTA per unit.  All roles walk the same run.
+// equal runs, whatever the sequences' lengths are.  Of a unit that several CTAs
+// share, the first CTA's part lies in its second slot and the others' in their first,
+// and the first CTA names the unit to k_attn_merge (sp.shared).  Else a CTA per unit.
+// All roles walk the same run.
 template <int D, int R, bool kSplit>
 // (the bounds ask for 128 registers: with more, two CTAs' six warps do not fit an SM)
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
@@ -733,11 +654,17 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
       if (w < warp) front += sm.scan[w];
       total += sm.scan[w];
     }
-    if (total == 0) return;
+    if (total == 0) {
+      if (tid == 0) sp.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
     per = div_ll(total + gridDim.x - 1, gridDim.x);
     begin = per * blockIdx.x;
     end = min(begin + per, total);
-    if (begin >= end) return;
+    if (begin >= end) {
+      if (tid == 0) sp.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
     // the thread whose run holds the first tile finds its unit
     if (mine > 0 && front <= begin && begin < front + mine) {
       bool found = false;
@@ -796,7 +723,9 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
     u.h = (int)div_ll(begin - f, u.kt1 - u.kt0);
   }
   pdl_wait();
+  pdl_trigger();  // the merge may take its places and wait
   Phases ph;
+  int4 shared = make_int4(0, 0, 0, 0);
   long long at = begin;
   while (at < end) {
     const int w = u.kt1 - u.kt0;
@@ -808,11 +737,12 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
     } else if (warp == kMmaWarp) {
       issue<D, R>(a, t0, t1, tc::smem_u32(ring), tmem, sm, ph);
     } else {
-      const bool whole = at == u_first && stop == u_first + w;
-      const int c0 = (int)div_ll(u_first, per), c1 = (int)div_ll(u_first + w - 1, per);
-      const int slot = at == u_first ? 2 * c0 + 1 : 2 * (int)blockIdx.x;
-      soften<D, R>(a, u, t0, t1, whole, slot, c0, c1 - c0 + 1, q, q_stride, out, out_stride, sp,
-                   ring, tmem, sm, ph);
+      const bool first = at == u_first, whole = first && stop == u_first + w;
+      if (first && !whole)  // parts, valid rows, first row, key head
+        shared = make_int4((int)(div_ll(u_first + w - 1, per) - blockIdx.x) + 1, u.rows,
+                           u.v.row0 + u.tok0, u.h);
+      soften<D, R>(a, u, t0, t1, whole, 2 * (int)blockIdx.x + (first ? 1 : 0), q, q_stride, out,
+                   out_stride, sp, ring, tmem, sm, ph);
     }
     at = stop;
     if (at >= end) break;
@@ -827,6 +757,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
       unit_range<R>(a, u);
     }
   }
+  if (kSplit && tid == 0) sp.shared[blockIdx.x] = shared;
   if (warp >= kMmaWarp && *(volatile int*)&sm.abort) {
     // a wait gave up: time for this CTA's copies and MMAs in flight to end before its
     // memory goes back
@@ -841,6 +772,74 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::kTmemCols);
   }
+}
+
+// Joins the parts of the units that CTAs of a split launch shared: block (c, row)
+// looks at the unit that CTA c was the first to work on.  Parts are weighted by
+// their references and added in a fixed order: four interleaved runs, then those.
+template <int D>
+__global__ void __launch_bounds__(D)
+    k_attn_merge(AttnSplit sp, int g, bf16* out, int64_t out_stride) {
+  constexpr int kCols = D / 4;          // threads of a run, four values each
+  constexpr int kRuns = 4;
+  constexpr int kWarps = D / 32;
+  __shared__ float s_w[kAttnMaxCtas];   // the parts' weights
+  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float4 s_x[kRuns - 1][kCols];
+  const int c0 = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  pdl_wait();
+  const int4 unit = __ldcg(sp.shared + c0);
+  const int parts = unit.x;
+  if (row >= unit.y || parts == 0) return;
+  const auto slot = [&](int p) {
+    return (size_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kAttnSlotRows + row;
+  };
+  // the largest reference, then the weights and the sum
+  float m = -INFINITY;
+  for (int p = tid; p < parts; p += D) m = fmaxf(m, __ldcg(&sp.ml[slot(p)].x));
+  m = warp_max(m);
+  if ((tid & 31) == 0) s_m[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w]);
+  float l = 0.0f;
+  for (int p = tid; p < parts; p += D) {
+    const float2 ml = __ldcg(sp.ml + slot(p));
+    const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
+    s_w[p] = f;
+    l = fmaf(ml.y, f, l);
+  }
+  l = warp_sum(l);
+  if ((tid & 31) == 0) s_l[tid >> 5] = l;
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) l += s_l[w];
+  const int col = tid % kCols, run = tid / kCols;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+  for (int p = run; p < parts; p += kRuns) {
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(sp.o + slot(p) * D) + col);
+    const float f = s_w[p];
+    x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+  }
+  if (run > 0) s_x[run - 1][col] = x;
+  __syncthreads();
+  if (run > 0) return;
+#pragma unroll
+  for (int i = 0; i < kRuns - 1; ++i) {
+    const float4 y = s_x[i][col];
+    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  }
+  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+  const int tok = row / g;
+  const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x * inv, x.y * inv);
+  const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+  uint2 w;
+  w.x = *reinterpret_cast<const uint32_t*>(&y0);
+  w.y = *reinterpret_cast<const uint32_t*>(&y1);
+  *reinterpret_cast<uint2*>(out + (int64_t)(unit.z + tok) * out_stride +
+                            (unit.w * g + row - tok * g) * D + 4 * col) = w;
 }
 
 template <int D, int R>
@@ -866,8 +865,11 @@ cudaError_t launch_dr(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64
                       bf16* out, int64_t out_stride, const AttnSplit& sp, int grid, bool split,
                       bool pdl, cudaStream_t s) {
   auto* kernel = split ? k_attn_decode<D, R, true> : k_attn_decode<D, R, false>;
-  return launch_pdl(kernel, dim3(grid), dim3(kThreads), dec_smem_bytes<D>(), s, pdl, m.k, m.v, a,
-                    q, q_stride, out, out_stride, sp);
+  const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kThreads), dec_smem_bytes<D>(), s, pdl,
+                                   m.k, m.v, a, q, q_stride, out, out_stride, sp);
+  // (one CTA shares no unit)
+  if (e != cudaSuccess || !split || grid == 1) return e;
+  return launch_pdl(k_attn_merge<D>, dim3(grid, R), dim3(D), 0, s, true, sp, a.g, out, out_stride);
 }
 
 }  // namespace
