@@ -33,6 +33,8 @@ struct moe_attn {
 namespace {
 
 constexpr int kDecTileRows = kAttnSlotRows;
+constexpr int kPromptRows = 32;  // rows of a sequence (tokens x query heads of a key head)
+                                 // above which the prompt kernel takes them
 
 struct Device {
   int prev = -1;
@@ -88,8 +90,11 @@ Sizes sizes_of(const moe_attn_config* c) {
   const size_t slots = 2 * (size_t)kAttnMaxCtas;
   s.turns = up256((size_t)std::max(c->rotary_dim / 2, 1) * 8);
   s.q = up256((size_t)c->max_rows * c->q_heads * c->head_dim * 2);
-  s.part_o = up256(slots * kDecTileRows * c->head_dim * 4);
-  s.part_ml = up256(slots * kDecTileRows * 8);
+  // the larger of the decode kernel's and the prompt kernel's partial results
+  const size_t rows =
+      std::max(slots * kAttnSlotRows, (size_t)kAttnPromptCtas * kAttnPromptRows);
+  s.part_o = up256(rows * c->head_dim * 4);
+  s.part_ml = up256(rows * 8);
   s.shared = up256((size_t)kAttnMaxCtas * 16);
   s.status = 256;
   return s;
@@ -218,6 +223,21 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const long long cap = (long long)b->pages_stride << c->page_shift;
   const long long keys = b->max_kv_len > 0 ? std::min<long long>(b->max_kv_len, cap) : cap;
   const int seq_rows = b->max_seq_rows > 0 ? std::min(b->max_seq_rows, b->rows) : b->rows;
+  AttnMaps maps;
+  if (!make_attn_maps(&maps, a, D)) return MOE_ERR_CUDA;
+  // Many rows of a sequence: the prompt kernel, whose row tiles hold 128.
+  if ((long long)seq_rows * a.g > kPromptRows) {
+    const long long units = b->rows / attn_prompt_tokens(D, a.g) + (long long)b->n_seqs;
+    const long long heads = units * a.Hkv, tiles = (keys + 127) / 128;
+    long long splits = 1;
+    if (heads < c->sm_count && heads <= kAttnPromptCtas)
+      splits = std::max<long long>(
+          1, std::min<long long>(std::min(c->sm_count, kAttnPromptCtas) / heads, tiles / 2));
+    return launch_attn_prompt(D, a, maps, q, q_stride, out, out_stride, c->split, (int)units,
+                              (int)splits, pdl, s) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+  }
   // eight rows to a tile where one holds a sequence's: less work per key
   const int tile_rows = (long long)seq_rows * a.g <= 8 ? 8 : kDecTileRows;
   const int tq = tile_rows / a.g;
@@ -232,8 +252,6 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
     const long long tiles = units * a.Hkv * ((span + kAttnKeys - 1) / kAttnKeys);
     grid = std::max<long long>(1, std::min<long long>((tiles + 1) / 2, c->dec_slots));
   }
-  AttnMaps maps;
-  if (!make_attn_maps(&maps, a, D)) return MOE_ERR_CUDA;
   return launch_attn_decode(D, tile_rows, a, maps, q, q_stride, out, out_stride, c->split, (int)grid, split, pdl,
                             s) == cudaSuccess
              ? MOE_OK
@@ -298,7 +316,8 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out) {
       ok = cudaMemcpy(p[0], t.data(), t.size() * 8, cudaMemcpyHostToDevice) == cudaSuccess &&
            cudaMemset(p[5], 0, z.status) == cudaSuccess &&
            cudaDeviceSynchronize() == cudaSuccess &&
-           setup_attn_decode(cfg->head_dim) == cudaSuccess;
+           setup_attn_decode(cfg->head_dim) == cudaSuccess &&
+           setup_attn_prompt(cfg->head_dim) == cudaSuccess;
     }
     if (ok) c->dec_slots = std::min(attn_decode_slots(cfg->head_dim, c->sm_count), kAttnMaxCtas);
   } catch (const std::bad_alloc&) {

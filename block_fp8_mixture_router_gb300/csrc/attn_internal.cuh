@@ -54,6 +54,8 @@ struct AttnSplit {
                    // its parts (0: none), rows, first row, key head
 };
 constexpr int kAttnSlotRows = 16;
+constexpr int kAttnPromptRows = 256;  // rows of a slot of the prompt kernel
+constexpr int kAttnPromptCtas = 160;  // most CTAs of a launch of it that splits keys
 constexpr int kAttnMaxCtas = 512;  // CTAs of a launch that splits units
 
 cudaError_t launch_rope(int D, const bf16* x, int64_t x_stride, int heads, const int* positions,
@@ -90,6 +92,15 @@ int attn_decode_slots(int D, int sm_count);  // CTAs of a full grid
 cudaError_t launch_attn_decode(int D, int tile_rows, const AttnArgs& a, const AttnMaps& m,
                                const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
                                const AttnSplit& sp, int grid, bool split, bool pdl,
+                               cudaStream_t s);
+
+// The prompt kernel: `units` row blocks of attn_prompt_tokens tokens (at most, over
+// all sequences) and `splits` shares of the keys for each.
+int attn_prompt_tokens(int D, int g);
+cudaError_t setup_attn_prompt(int D);
+cudaError_t launch_attn_prompt(int D, const AttnArgs& a, const AttnMaps& m, const bf16* q,
+                               int64_t q_stride, bf16* out, int64_t out_stride,
+                               const AttnSplit& sp, int units, int splits, bool pdl,
                                cudaStream_t s);
 
 }  // namespace moe

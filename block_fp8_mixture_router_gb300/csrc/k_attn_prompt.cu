@@ -1,0 +1,893 @@
+// Attention over the 8-bit paged cache for many rows of a sequence (prompts and
+// chunks of them): commit "the Drama 3 text backbone on CUDA" (full attention with
+// shared key heads); the cache's format is this library's.
+//
+//   S = Q K^T,  P = 2^(scale S - m),  O += P V,  out = O / sum P
+//
+// in one pass over the keys with a running reference m and sum for each row.  Bound
+// by the tensor cores and, close behind, by the exponentials.  A CTA holds 256 rows
+// (128 at head_dim 256): row tiles of 128, the g query heads of a key head times
+// 128/g tokens.
+//
+// - S: kind::f8f6f4 on the keys' codes as they are stored; a query of 8 significant
+//   bits is two e4m3 values, Qhi + Qlo, multiplied in two passes at twice the
+//   16-bit rate: the same time as one 16-bit product, without converting K.
+// - P V: kind::f16; four warps widen V's codes to fp16 once for all the CTA's rows, P
+//   goes to tensor memory as fp16 over the scores it came from.
+// - Two row tiles take turns: while the softmax warps of one work, the tensor cores
+//   have the other's products.
+//
+// Warps: 0-3 and 4-7 softmax of the two row tiles (a thread per row; at head_dim 256
+// of the two score buffers' one tile: 0-3 alone), 8-11 widen V, 12 issues MMAs,
+// 13 copies by TMA.
+#include "attn_tc.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kPThreads = 448;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kKeys = 128;          // keys of a tile
+constexpr int kChunk = 64;          // keys of a widened piece of V
+constexpr int kMeta = 8;            // tiles whose scales are kept
+// Weights as p x 2^10 in fp16, p against a reference that may lag the row's maximum
+// by kLag powers of two: sums are scaled again only when a score outgrows that.
+constexpr float kShiftLog = 10.0f;
+constexpr float kLag = 5.0f;
+
+template <int D>
+struct Pr {
+  static constexpr int kTiles = D == 256 ? 1 : 2;      // row tiles of a CTA
+  static constexpr bool kWide = D >= 128;
+  static constexpr int kRowBytes = kWide ? 128 : 64;
+  static constexpr int kPanels = D / kRowBytes;
+  static constexpr int kPanelBytes = kKeys * kRowBytes;
+  static constexpr int kTileBytes = kKeys * D;         // keys or values of a tile, as stored
+  static constexpr int kQBytes = 128 * D;              // one part of a row tile's queries
+  static constexpr int kKStages = D == 256 ? 2 : 3;
+  static constexpr int kVStages = D == 256 ? 1 : 2;
+  static constexpr int kCStages = D == 256 ? 2 : 4;    // widened pieces
+  static constexpr int kCBytes = kChunk * D * 2;
+};
+
+struct alignas(16) Meta {
+  float ks, log_vs, inv_vs, vs;  // ks < 0: the page does not exist (or is not needed)
+};
+
+template <int D>
+struct PrSmem {
+  float fac[Pr<D>::kTiles * 128]; // score factors of the rows, but for the key's scale
+  Meta meta[kMeta][kKeys / 16];
+  float top[kMeta];              // a tile's largest value scale
+  uint32_t poison[kMeta][4];     // keys of a tile that have a NaN value
+  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], c_full[4], c_empty[4];
+  uint64_t meta_full[kMeta], poison_full[kMeta];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint32_t tmem;
+  int abort;
+};
+
+template <int D>
+constexpr size_t pr_smem_bytes() {
+  using C = Pr<D>;
+  return 1024 + (size_t)C::kTiles * 2 * C::kQBytes + (size_t)C::kKStages * C::kTileBytes +
+         (size_t)C::kVStages * C::kTileBytes + (size_t)C::kCStages * C::kCBytes +
+         sizeof(PrSmem<D>);
+}
+
+static_assert(pr_smem_bytes<64>() <= 232448 && pr_smem_bytes<128>() <= 232448 &&
+                  pr_smem_bytes<256>() <= 232448,
+              "a CTA's shared memory");
+
+// Byte of (row, byte b) in a [rows][128] or [rows][64] operand under its swizzle.
+template <bool kWide>
+__device__ __forceinline__ int swz(int row, int b) {
+  const int col = b >> 4;
+  return kWide ? row * 128 + ((col ^ (row & 7)) << 4) + (b & 15)
+               : row * 64 + ((col ^ ((row >> 1) & 3)) << 4) + (b & 15);
+}
+
+// D[tmem] (+)= A[tmem, fp16] * B[smem, fp16]: issued by lane 0 of a warp that runs
+// in uniform control flow.
+__device__ __forceinline__ void mma_ts_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .u32 ln;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.u32 ln, %%laneid;\n setp.eq.u32 e, ln, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(h) : "f"(hi), "f"(lo));
+  return h;
+}
+
+__device__ __forceinline__ uint32_t widen(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)w));
+  return h;
+}
+
+// a * b + c and a + b on pairs of floats (one instruction each).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mov.b64 z, {%6, %7};\n fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// A CTA's rows and keys.
+struct Work {
+  int s, h;
+  SeqView v;
+  int tq;          // tokens of a row tile
+  int tok0;        // first token
+  int toks;        // tokens of the CTA (all row tiles)
+  int tiles;       // row tiles that hold any
+  int lo, hi;      // keys that any row can see
+  int t0, t1;      // key tiles of this CTA
+  int part, parts; // its share of the key tiles
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort, int* status) {
+  return tc::wait_bounded(bar, parity, abort, status);
+}
+
+// The queries of one row tile as e4m3 parts (see k_attn_decode.cu), by its softmax
+// warps.
+template <int D>
+__device__ __forceinline__ void stage_queries(const AttnArgs& a, const Work& w, int tile,
+                                              const bf16* q, int64_t q_stride, uint8_t* sq,
+                                              float* fac) {
+  using C = Pr<D>;
+  constexpr int kPer = D / 8;
+  const int t = threadIdx.x & 127;
+  const int c = t % kPer, sub = t / kPer;
+  const int valid = min(w.tq, w.toks - tile * w.tq) * a.g;
+  constexpr int kStep = 128 / kPer;
+#pragma unroll 4
+  for (int r = sub; r < 128; r += kStep) {
+    const int tok = r / a.g;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (r < valid)
+      raw = *reinterpret_cast<const uint4*>(
+          q + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * q_stride +
+          (w.h * a.g + r - tok * a.g) * D + 8 * c);
+    float x[8];
+    unpack8(raw, x);
+    float mx = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      odd |= !is_finite(x[i]);
+      mx = fmaxf(mx, fabsf(x[i]));
+    }
+    if (odd) mx = __int_as_float(0x7F800000);
+#pragma unroll
+    for (int o = kPer / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    uint2 hi = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), lo = make_uint2(0, 0);  // NaN scores
+    float f = 0.0f;
+    if (is_finite(mx)) {
+      const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      f = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * a.scale;
+      uint32_t p[2], z[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = x[4 * i + k] * up;
+        p[i] = e4m3x4(y[0], y[1], y[2], y[3]);
+        const uint32_t h01 = widen(p[i]), h23 = widen(p[i] >> 16);
+        const float2 b01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+        const float2 b23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+        z[i] = e4m3x4(y[0] - b01.x, y[1] - b01.y, y[2] - b23.x, y[3] - b23.y);
+      }
+      hi = make_uint2(p[0], p[1]);
+      lo = make_uint2(z[0], z[1]);
+    }
+    const int panel = 8 * c / C::kRowBytes, b = 8 * c % C::kRowBytes;
+    uint8_t* at = sq + panel * 128 * C::kRowBytes + swz<C::kWide>(r, b);
+    *reinterpret_cast<uint2*>(at) = hi;
+    *reinterpret_cast<uint2*>(at + C::kQBytes) = lo;
+    if (c == 0) fac[r] = f;
+  }
+}
+
+// ---- the TMA warp ------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
+                                           const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                           uint8_t* sk, uint8_t* sv, PrSmem<D>& sm) {
+  using C = Pr<D>;
+  const int lane = threadIdx.x & 31;
+  const int box = 1 << a.page_shift;
+  const int per_tile = kKeys / box;
+  const int batch = 32 / per_tile;
+  const int y = w.h << a.page_shift;
+  Ring rk, rv;
+  const auto copy = [&](uint8_t* to, const CUtensorMap* map, int sub, int page, uint64_t* bar) {
+#pragma unroll
+    for (int p = 0; p < C::kPanels; ++p)
+      tc::tma_load_3d(to + p * C::kPanelBytes + sub * box * C::kRowBytes, map, p * 128, y, page,
+                      bar);
+  };
+  // keys of tile kt + 1 go out before the values of tile kt: they are needed first
+  int page = 0, page_next = 0;
+  bool on = false, on_next = false;
+  float ks = -1.0f, vs = 1.0f;
+  int base = w.t0;                 // first tile of the lanes' boxes
+  const auto look_up = [&](int kt0) {
+    const int tiles = min(batch, w.t1 - kt0);
+    const int key = kt0 * kKeys + lane * box;
+    on_next = lane < tiles * per_tile && key < w.hi && key + box > w.lo;
+    ks = -1.0f;
+    vs = 1.0f;
+    page_next = 0;
+    if (on_next) {
+      page_next = page_at(a, w.s, key >> a.page_shift);
+      if (page_next < 0) {
+        atomicOr(a.status, kAttnBadBatch);
+        on_next = false;
+      } else {
+        ks = a.ks[(size_t)page_next * a.Hkv + w.h];
+        vs = a.vs[(size_t)page_next * a.Hkv + w.h];
+      }
+    }
+  };
+  int v_page = 0, v_boxes = 0, v_sub = -1;
+  bool v_on = false;
+  for (int kt = w.t0; kt <= w.t1; ++kt) {
+    int sub = -1;
+    uint32_t boxes = 0;
+    if (kt < w.t1) {
+      if ((kt - w.t0) % batch == 0) {
+        base = kt;
+        look_up(kt);
+        page = page_next;
+        on = on_next;
+      }
+      sub = lane - (kt - base) * per_tile;
+      const bool mine = sub >= 0 && sub < per_tile;
+      boxes = __popc(__ballot_sync(0xffffffffu, mine && on));
+      const int slot = (kt - w.t0) & (kMeta - 1);
+      // (the softmax warps are at most a few tiles behind the keys' copies)
+      if (mine)
+        for (int g = sub * box / 16; g < (sub + 1) * box / 16; ++g)
+          sm.meta[slot][g] = Meta{ks, __log2f(vs), __fdiv_rn(1.0f, vs), vs};
+      float top = mine && on ? vs : 0.0f;
+      top = warp_max(top);
+      if (lane == 0) sm.top[slot] = top;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.meta_full[slot]);
+      wait(&sm.k_empty[rk.i], rk.phase ^ 1, &sm.abort, a.status);
+      if (*(volatile int*)&sm.abort) return;
+      if (lane == 0) tc::mbar_arrive_expect_tx(&sm.k_full[rk.i], boxes * box * D);
+      __syncwarp();
+      if (mine && on) copy(sk + (size_t)rk.i * C::kTileBytes, kmap, sub, page, &sm.k_full[rk.i]);
+      rk.next(C::kKStages);
+    }
+    if (kt > w.t0) {
+      wait(&sm.v_empty[rv.i], rv.phase ^ 1, &sm.abort, a.status);
+      if (*(volatile int*)&sm.abort) return;
+      if (lane == 0) tc::mbar_arrive_expect_tx(&sm.v_full[rv.i], v_boxes * box * D);
+      __syncwarp();
+      if (v_on) copy(sv + (size_t)rv.i * C::kTileBytes, vmap, v_sub, v_page, &sm.v_full[rv.i]);
+      rv.next(C::kVStages);
+    }
+    v_on = sub >= 0 && sub < per_tile && on;
+    v_sub = sub;
+    v_page = page;
+    v_boxes = (int)boxes;
+  }
+}
+
+// Whether a tile needs its keys looked at one by one: some row of [pos0, pos1] does
+// not see all of them.
+__device__ __forceinline__ bool edge_tile(const AttnArgs& a, const Work& w, int kt, int pos0,
+                                          int pos1) {
+  const int key0 = kt * kKeys;
+  return key0 + kKeys - 1 > pos0 || key0 < w.lo || (a.window && key0 <= pos1 - a.window);
+}
+
+// ---- the warps that widen V -----------------------------------------------------
+template <int D>
+__device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, const uint8_t* sv,
+                                            uint8_t* sc, PrSmem<D>& sm) {
+  using C = Pr<D>;
+  const int t = threadIdx.x - kConvWarp * 32, lane = t & 31, warp = t >> 5;
+  const int k = t & 63, h = t >> 6;   // key of a piece, half of its row
+  const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
+  Ring rv, rc;
+  for (int kt = w.t0; kt < w.t1; ++kt) {
+    const int n = kt - w.t0, slot = n & (kMeta - 1);
+    wait(&sm.meta_full[slot], (n / kMeta) & 1, &sm.abort, a.status);
+    wait(&sm.v_full[rv.i], rv.phase, &sm.abort, a.status);
+    const uint8_t* v = sv + (size_t)rv.i * C::kTileBytes;
+    bool whole = !edge_tile(a, w, kt, pos0, pos1);
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g) whole &= sm.meta[slot][g].ks >= 0.0f;
+    if (!whole) {
+      if (t < 4) sm.poison[slot][t] = 0;
+      asm volatile("bar.sync 2, 128;\n" ::: "memory");
+    }
+    for (int c = 0; c < 2; ++c) {
+      wait(&sm.c_empty[rc.i], rc.phase ^ 1, &sm.abort, a.status);
+      uint8_t* out = sc + (size_t)rc.i * C::kCBytes;
+      const int key = c * kChunk + k;
+      bool live = true, poison = false;
+      if (!whole)
+        live = kt * kKeys + key >= w.lo && kt * kKeys + key < w.hi &&
+               sm.meta[slot][key >> 4].ks >= 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int b = h * (D / 2) + 16 * i;        // first of 16 values
+        uint4 x = *reinterpret_cast<const uint4*>(v + b / C::kRowBytes * C::kPanelBytes +
+                                                  swz<C::kWide>(key, b % C::kRowBytes));
+        if (!whole) {
+          // values that do not exist become zeros, and NaN codes too: the rows that do see
+          // such a key get a NaN weight instead (0 x NaN would reach the others)
+          if (!live) x = make_uint4(0, 0, 0, 0);
+          const uint32_t n0 = e4m3_nan_bytes(x.x), n1 = e4m3_nan_bytes(x.y),
+                         n2 = e4m3_nan_bytes(x.z), n3 = e4m3_nan_bytes(x.w);
+          if (n0 | n1 | n2 | n3) {
+            poison = true;
+            x.x &= ~((n0 >> 7) * 0xFFu);
+            x.y &= ~((n1 >> 7) * 0xFFu);
+            x.z &= ~((n2 >> 7) * 0xFFu);
+            x.w &= ~((n3 >> 7) * 0xFFu);
+          }
+        }
+        uint8_t* row = out + b / 64 * (kChunk * 128);
+        const int col = (b % 64) / 8;              // 16-byte column of eight fp16
+        *reinterpret_cast<uint4*>(row + k * 128 + ((col ^ (k & 7)) << 4)) =
+            make_uint4(widen(x.x), widen(x.x >> 16), widen(x.y), widen(x.y >> 16));
+        *reinterpret_cast<uint4*>(row + k * 128 + (((col + 1) ^ (k & 7)) << 4)) =
+            make_uint4(widen(x.z), widen(x.z >> 16), widen(x.w), widen(x.w >> 16));
+      }
+      if (!whole) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, poison);
+        if (lane == 0 && bits) atomicOr(&sm.poison[slot][2 * c + (warp & 1)], bits);
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.c_full[rc.i]);
+      rc.next(C::kCStages);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      tc::mbar_arrive(&sm.v_empty[rv.i]);
+      tc::mbar_arrive(&sm.poison_full[slot]);
+    }
+    rv.next(C::kVStages);
+  }
+}
+
+// ---- the MMA warp ----------------------------------------------------------------
+// Score buffer of (tile kt, row tile m): two row tiles have one each; one row tile
+// alternates between the two.
+template <int D>
+__device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t sq, uint32_t sk,
+                                      uint32_t sc, uint32_t tmem, PrSmem<D>& sm) {
+  using C = Pr<D>;
+  constexpr uint32_t id_s = tc::idesc_f8(128, kKeys);
+  constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                            ((uint32_t)(128 >> 4) << 24);  // fp16, B stored N-major
+  int* abort = &sm.abort;
+  const int tiles = w.tiles;
+  const int n = w.t1 - w.t0;
+  Ring rk, rc;
+  uint32_t p_phase[2] = {0, 0}, pv_phase[2] = {0, 0};
+  for (int m = 0; m < tiles; ++m) wait(&sm.q_full[m], 0, abort, a.status);
+
+  const auto scores = [&](int m, int buf) {  // of the keys in stage rk.i
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int panel = 32 * i / C::kRowBytes, b = 32 * i % C::kRowBytes;
+        tc::mma_warp<true>(
+            tmem + buf * 128,
+            tc::swz_desc(sq + (2 * m + part) * C::kQBytes + panel * 128 * C::kRowBytes + b,
+                         C::kWide),
+            tc::swz_desc(sk + rk.i * C::kTileBytes + panel * C::kPanelBytes + b, C::kWide), id_s,
+            part > 0 || i > 0);
+      }
+    tc::commit_warp(&sm.s_full[buf]);
+  };
+  const auto values = [&](int m, int buf, bool first, const Ring& from) {
+    Ring r = from;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (m == 0) {
+        wait(&sm.c_full[r.i], r.phase, abort, a.status);
+        tc::fence_after_sync();
+      }
+#pragma unroll
+      for (int i = 0; i < kChunk / 16; ++i) {
+        // 16 keys: two groups of eight rows of 1024 bytes; blocks of 64 values behind
+        const uint64_t b = tc::swz_desc(sc + r.i * C::kCBytes + i * 2048, true, kChunk * 128);
+        mma_ts_warp(tmem + 256 + m * D, tmem + buf * 128 + c * 32 + i * 8, b, id_o,
+                    !first || c > 0 || i > 0);
+      }
+      if (m == tiles - 1) tc::commit_warp(&sm.c_empty[r.i]);
+      r.next(C::kCStages);
+    }
+    tc::commit_warp(&sm.pv_done[buf]);
+    return r;
+  };
+
+  if constexpr (C::kTiles == 2) {
+    // S(0, t0) S(1, t0) | then for every tile and row tile: its values, its next scores
+    wait(&sm.k_full[0], 0, abort, a.status);
+    tc::fence_after_sync();
+    for (int m = 0; m < tiles; ++m) scores(m, m);
+    tc::commit_warp(&sm.k_empty[0]);
+    rk.next(C::kKStages);
+    for (int i = 0; i < n; ++i) {
+      Ring after = rc;
+      for (int m = 0; m < tiles; ++m) {
+        wait(&sm.p_full[m], p_phase[m], abort, a.status);
+        p_phase[m] ^= 1;
+        tc::fence_after_sync();
+        after = values(m, m, i == 0, rc);
+        if (i + 1 < n) {
+          if (m == 0) wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
+          // the weights lie where the scores go
+          wait(&sm.pv_done[m], pv_phase[m], abort, a.status);
+          tc::fence_after_sync();
+          scores(m, m);
+          if (m == tiles - 1) {
+            tc::commit_warp(&sm.k_empty[rk.i]);
+            rk.next(C::kKStages);
+          }
+        }
+        pv_phase[m] ^= 1;
+      }
+      rc = after;
+    }
+  } else {
+    // one row tile, two score buffers: the next tile's scores before this tile's values
+    const auto next_scores = [&](int i) {
+      wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
+      if (i >= 2) {
+        wait(&sm.pv_done[i & 1], pv_phase[i & 1], abort, a.status);
+        pv_phase[i & 1] ^= 1;
+      }
+      tc::fence_after_sync();
+      scores(0, i & 1);
+      tc::commit_warp(&sm.k_empty[rk.i]);
+      rk.next(C::kKStages);
+    };
+    next_scores(0);
+    for (int i = 0; i < n; ++i) {
+      if (i + 1 < n) next_scores(i + 1);
+      wait(&sm.p_full[i & 1], p_phase[i & 1], abort, a.status);
+      p_phase[i & 1] ^= 1;
+      tc::fence_after_sync();
+      rc = values(0, i & 1, i == 0, rc);
+    }
+  }
+}
+
+// ---- the softmax warps --------------------------------------------------------------
+// One row of one key tile: the largest score over the reference, or the weights.
+struct RowMask {
+  int low, high;        // columns [low, high] are seen
+  uint32_t absent;      // 16-key groups without a page
+  uint32_t poison[4];   // columns with a NaN value
+};
+
+// Weights of 32 columns (two 16-key groups) from the scores in v, packed to fp16.
+template <bool kEdge>
+__device__ __forceinline__ void weigh32(const uint32_t (&v)[32], uint32_t (&p)[16], int col0,
+                                        const float (&f)[2], const float (&base)[2],
+                                        const float (&inv)[2], const RowMask& mk, float& l) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float2 ff = make_float2(f[g], f[g]), bb = make_float2(base[g], base[g]);
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = 16 * g + 2 * i;
+      float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), ff, bb);
+      x.x = exp2_approx(x.x);
+      x.y = exp2_approx(x.y);
+      if constexpr (kEdge) {
+        const uint32_t bad = mk.poison[col0 / 32];
+        if (bad & (1u << c)) x.x = __int_as_float(0x7FFFFFFF);
+        if (bad & (2u << c)) x.y = __int_as_float(0x7FFFFFFF);
+        const bool none = (mk.absent >> (col0 / 16 + g)) & 1;
+        if (none || col0 + c < mk.low || col0 + c > mk.high) x.x = 0.0f;
+        if (none || col0 + c + 1 < mk.low || col0 + c + 1 > mk.high) x.y = 0.0f;
+      }
+      sum = add2(sum, x);
+      p[8 * g + i] = f16x2_of(x.x, x.y);
+    }
+    l = fmaf(sum.x + sum.y, inv[g], l);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int tile, uint32_t tmem,
+                                       const float* fac_of, PrSmem<D>& sm, float& m_out,
+                                       float& l_out, float& vref_out) {
+  using C = Pr<D>;
+  const int row = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(row & 96) << 16;
+  const uint32_t t_o = tmem + lanes + 256 + tile * D;
+  int* abort = &sm.abort;
+  const int first = w.v.first + w.tok0 + tile * w.tq;        // earliest row of the tile
+  const int toks = min(w.tq, w.toks - tile * w.tq);
+  const int pos = first + min(row / a.g, toks - 1);
+  // tiles are looked at key by key, and their NaN values taken out of V, by what the
+  // CTA's rows see: a row tile that sees all keys has to know of those values too
+  const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
+  const float fac = fac_of[row];
+  float m = -INFINITY, l = 0.0f, vref = 0x1p-126f, log_up = 0.0f, down = 0.0f;
+  uint32_t s_phase[2] = {0, 0}, pv_phase[2] = {0, 0};
+  const int n = w.t1 - w.t0;
+  for (int i = 0; i < n; ++i) {
+    const int kt = w.t0 + i, slot = i & (kMeta - 1);
+    const int buf = C::kTiles == 2 ? tile : (i & 1);
+    const int last_buf = C::kTiles == 2 ? tile : (buf ^ 1);
+    wait(&sm.meta_full[slot], (i / kMeta) & 1, abort, a.status);
+    const float top = sm.top[slot];
+    uint32_t absent = 0;
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g) absent |= sm.meta[slot][g].ks < 0.0f ? 1u << g : 0u;
+    const bool edge = edge_tile(a, w, kt, pos0, pos1) || absent != 0;
+    RowMask mk;
+    if (edge) {
+      wait(&sm.poison_full[slot], (i / kMeta) & 1, abort, a.status);
+      mk.high = min(pos - kt * kKeys, kKeys);
+      mk.low = a.window ? pos - a.window + 1 - kt * kKeys : -1;
+      mk.absent = absent;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mk.poison[k] = sm.poison[slot][k];
+    }
+    wait(&sm.s_full[buf], s_phase[buf], abort, a.status);
+    s_phase[buf] ^= 1;
+    tc::fence_after_sync();
+    __syncwarp();
+    const uint32_t t_s = tmem + lanes + buf * 128;
+    // the row's largest score, 32 columns at a time
+    float peak = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kKeys; b += 32) {
+      uint32_t v[32];
+      tc::tmem_ld_async(t_s + b, v);
+      tc::wait_ld();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int c = 16 * g; c < 16 * g + 16; ++c) {
+          const float y = __uint_as_float(v[c]);
+          if (!edge || (b + c >= mk.low && b + c <= mk.high)) x = fmaxf(x, y);
+        }
+        const float f = fac * sm.meta[slot][b / 16 + g].ks;
+        if (edge && ((absent >> (b / 16 + g)) & 1)) x = -INFINITY;
+        if (x != -INFINITY) peak = fmaxf(peak, x * f);
+      }
+    }
+    if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
+      // new references for the warp's rows, and their sums brought to them
+      const float m_new = fmaxf(m, peak);
+      const float alpha = m_new == -INFINITY ? 1.0f : exp2_approx(m - m_new);
+      const float vf = top > vref ? __fdiv_rn(vref, top) : 1.0f;
+      m = m_new;
+      l *= alpha;
+      vref = fmaxf(vref, top);
+      log_up = kShiftLog - __log2f(vref);
+      down = vref * 0x1p-10f;
+      if (i > 0) {
+        wait(&sm.pv_done[last_buf], pv_phase[last_buf] ^ 1, abort, a.status);
+        tc::fence_after_sync();
+        __syncwarp();
+        const float f = alpha * vf;
+#pragma unroll 1
+        for (int b = 0; b < D; b += 32) {
+          uint32_t v[32];
+          tc::tmem_ld_async(t_o + b, v);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+          tc::tmem_st(t_o + b, v);
+        }
+        tc::wait_st();
+      }
+    }
+    const float m_base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int b = 0; b < kKeys; b += 32) {
+      uint32_t v[32], p[16];
+      tc::tmem_ld_async(t_s + b, v);
+      float f[2], base[2], inv[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const Meta me = sm.meta[slot][b / 16 + g];
+        f[g] = fac * me.ks;
+        // a page below 2^-70 of the largest adds no value that counts
+        base[g] = fmaxf(me.log_vs + log_up, -60.0f) - m_base;
+        inv[g] = fminf(me.inv_vs * down, 0x1p60f);
+      }
+      tc::wait_ld();
+      if (edge)
+        weigh32<true>(v, p, b, f, base, inv, mk, l);
+      else
+        weigh32<false>(v, p, b, f, base, inv, mk, l);
+      // over scores that have been read: columns b/2 .. b/2 + 15
+      tc::tmem_st(t_s + b / 2, p);
+    }
+    tc::wait_st();
+    tc::fence_before_sync();
+    tc::mbar_arrive(&sm.p_full[buf]);
+    pv_phase[buf] ^= 1;
+  }
+  const int last = C::kTiles == 2 ? tile : ((n - 1) & 1);
+  wait(&sm.pv_done[last], pv_phase[last] ^ 1, abort, a.status);
+  tc::fence_after_sync();
+  __syncwarp();
+  m_out = m;
+  l_out = l;
+  vref_out = vref;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+    k_attn_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const AttnArgs a, const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
+                  const AttnSplit sp, int units, int splits) {
+  using C = Pr<D>;
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* sq = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sk = sq + (size_t)C::kTiles * 2 * C::kQBytes;
+  uint8_t* sv = sk + (size_t)C::kKStages * C::kTileBytes;
+  uint8_t* sc = sv + (size_t)C::kVStages * C::kTileBytes;
+  PrSmem<D>& sm = *reinterpret_cast<PrSmem<D>*>(sc + (size_t)C::kCStages * C::kCBytes);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  // late rows of a prompt see the most keys: they go first
+  Work w;
+  w.part = blockIdx.x % splits;
+  w.parts = splits;
+  const int uh = blockIdx.x / splits;
+  w.h = uh % a.Hkv;
+  const int unit = units - 1 - uh / a.Hkv;
+  w.tq = 128 / a.g;
+  const int per = C::kTiles * w.tq;
+  int u0;
+  w.s = unit_seq(a, per, 1, unit, &u0);
+  w.v = seq_view(a, w.s);
+  if (!w.v.ok && tid == 0) atomicOr(a.status, kAttnBadBatch);
+  w.tok0 = (unit - u0) * per;
+  const bool none = unit < u0 || w.tok0 >= w.v.n;
+  if (none) {
+    if (splits > 1 && tid == 0) sp.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  w.toks = min(per, w.v.n - w.tok0);
+  w.tiles = (w.toks + w.tq - 1) / w.tq;
+  w.hi = max(min(w.v.len, w.v.first + w.tok0 + w.toks), 0);
+  w.lo = a.window ? max(0, w.v.first + w.tok0 - a.window + 1) : 0;
+  w.lo = min(w.lo, w.hi);
+  {
+    const int k0 = w.lo / kKeys;
+    const int k1 = max((int)(((long long)w.hi + kKeys - 1) / kKeys), k0 + 1);
+    const int n = k1 - k0;
+    w.t0 = k0 + (int)((long long)n * w.part / splits);
+    w.t1 = k0 + (int)((long long)n * (w.part + 1) / splits);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      tc::mbar_init(&sm.k_full[i], 1);
+      tc::mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.v_full[i], 1);
+      tc::mbar_init(&sm.v_empty[i], 4);
+      tc::mbar_init(&sm.q_full[i], 128);
+      tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.p_full[i], 128);
+      tc::mbar_init(&sm.pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sm.c_full[i], 4);
+      tc::mbar_init(&sm.c_empty[i], 1);
+    }
+    for (int i = 0; i < kMeta; ++i) {
+      tc::mbar_init(&sm.meta_full[i], 1);
+      tc::mbar_init(&sm.poison_full[i], 4);
+    }
+    sm.abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::tmem_alloc(&sm.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == kTmaWarp && (tid & 31) == 0) {
+    tc::tma_prefetch_map(&kmap);
+    tc::tma_prefetch_map(&vmap);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait();
+  pdl_trigger();
+  const bool any = w.t0 < w.t1;  // (a share of fewer tiles than shares may be empty)
+  if (warp == kTmaWarp) {
+    if (any) copy_tiles<D>(a, w, &kmap, &vmap, sk, sv, sm);
+  } else if (warp == kMmaWarp) {
+    if (any) issue<D>(a, w, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc), tmem, sm);
+  } else if (warp >= kConvWarp) {
+    if (any) widen_tiles<D>(a, w, sv, sc, sm);
+  } else if (warp < 4 * C::kTiles && warp / 4 < w.tiles) {
+    const int tile = warp / 4, row = tid & 127;
+    float* fac = sm.fac + tile * 128;
+    stage_queries<D>(a, w, tile, q, q_stride, sq + (size_t)tile * 2 * C::kQBytes, fac);
+    tc::fence_async_smem();
+    tc::mbar_arrive(&sm.q_full[tile]);
+    asm volatile("bar.sync %0, 128;\n" ::"r"(3 + tile) : "memory");  // fac is complete
+    float m = -INFINITY, l = 0.0f, vref = 0x1p-126f;
+    if (any) soften<D>(a, w, tile, tmem, fac, sm, m, l, vref);
+    const int tok = row / a.g, toks = min(w.tq, w.toks - tile * w.tq);
+    const bool valid = tok < toks;
+    const uint32_t t_o = tmem + ((uint32_t)(row & 96) << 16) + 256 + tile * D;
+    float scale = vref * 0x1p-10f;
+    if (splits == 1) scale *= l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+    bf16* to = out + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * out_stride +
+               (w.h * a.g + row - tok * a.g) * D;
+    const size_t slot = (size_t)blockIdx.x * kAttnPromptRows + tile * 128 + row;
+#pragma unroll 1
+    for (int b = 0; b < D; b += 32) {
+      uint32_t v[32];
+      if (any) {
+        __syncwarp();
+        tc::tmem_ld_async(t_o + b, v);
+        tc::wait_ld();
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = 0;
+      }
+      if (!valid) continue;
+      if (splits == 1) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[k + e]) * scale;
+          *reinterpret_cast<uint4*>(to + b + k) = pack8(x);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+          __stcg(reinterpret_cast<float4*>(sp.o + slot * D + b + k),
+                 make_float4(__uint_as_float(v[k]) * scale, __uint_as_float(v[k + 1]) * scale,
+                             __uint_as_float(v[k + 2]) * scale,
+                             __uint_as_float(v[k + 3]) * scale));
+      }
+    }
+    if (splits > 1 && valid) __stcg(sp.ml + slot, make_float2(m, l));
+  }
+  if (splits > 1 && tid == 0)  // parts, tokens, first row, key head
+    sp.shared[blockIdx.x] =
+        w.part == 0 ? make_int4(splits, w.toks, w.v.row0 + w.tok0, w.h) : make_int4(0, 0, 0, 0);
+  if (warp >= kConvWarp && *(volatile int*)&sm.abort) {
+    // a wait gave up: time for this CTA's copies and MMAs in flight to end before its
+    // memory goes back
+    const unsigned long long t = tc::global_ns();
+    while (tc::global_ns() - t < 2000000ull) {
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the shares of the units' keys: a warp for each row of the unit that block x
+// was the first to work on.
+template <int D>
+__global__ void __launch_bounds__(256)
+    k_prompt_merge(AttnSplit sp, int g, int splits, bf16* out, int64_t out_stride) {
+  pdl_wait();
+  const int c0 = blockIdx.x * splits, lane = threadIdx.x & 31;
+  const int4 unit = __ldcg(sp.shared + c0);
+  const int parts = unit.x, tq = 128 / g;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);  // of the unit's row tiles
+  const int tile = row >> 7, r = row & 127, in = r / g;
+  const int tok = tile * tq + in;
+  if (parts == 0 || in >= tq || tok >= unit.y) return;
+  const auto slot = [&](int p) { return (size_t)(c0 + p) * kAttnPromptRows + row; };
+  float m = -INFINITY;
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, __ldcg(&sp.ml[slot(p)].x));
+  float l = 0.0f, x[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) x[i] = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = __ldcg(sp.ml + slot(p));
+    const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    const float* o = sp.o + slot(p) * D + lane * (D / 32);
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(o + i));
+      x[i] = fmaf(y.x, f, x[i]);
+      x[i + 1] = fmaf(y.y, f, x[i + 1]);
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+  bf16* to = out + (int64_t)(unit.z + tok) * out_stride + (unit.w * g + r - in * g) * D +
+             lane * (D / 32);
+#pragma unroll
+  for (int i = 0; i < D / 32; i += 2)
+    *reinterpret_cast<__nv_bfloat162*>(to + i) = __floats2bfloat162_rn(x[i] * inv, x[i + 1] * inv);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64_t q_stride,
+                     bf16* out, int64_t out_stride, const AttnSplit& sp, int units, int splits,
+                     bool pdl, cudaStream_t s) {
+  const int heads = units * a.Hkv;
+  const cudaError_t e =
+      launch_pdl(k_attn_prompt<D>, dim3(heads * splits), dim3(kPThreads), pr_smem_bytes<D>(), s,
+                 pdl, m.k, m.v, a, q, q_stride, out, out_stride, sp, units, splits);
+  if (e != cudaSuccess || splits == 1) return e;
+  return launch_pdl(k_prompt_merge<D>, dim3(heads, Pr<D>::kTiles * 16), dim3(256), 0, s, true, sp,
+                    a.g, splits, out, out_stride);
+}
+
+}  // namespace
+
+int attn_prompt_tokens(int D, int g) { return (D == 256 ? 1 : 2) * (128 / g); }
+
+cudaError_t setup_attn_prompt(int D) {
+  const auto set = [](auto* kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  };
+  return D == 64    ? set(k_attn_prompt<64>, pr_smem_bytes<64>())
+         : D == 128 ? set(k_attn_prompt<128>, pr_smem_bytes<128>())
+                    : set(k_attn_prompt<256>, pr_smem_bytes<256>());
+}
+
+cudaError_t launch_attn_prompt(int D, const AttnArgs& a, const AttnMaps& m, const bf16* q,
+                               int64_t q_stride, bf16* out, int64_t out_stride,
+                               const AttnSplit& sp, int units, int splits, bool pdl,
+                               cudaStream_t s) {
+  auto* f = D == 64 ? launch_d<64> : D == 128 ? launch_d<128> : launch_d<256>;
+  return f(a, m, q, q_stride, out, out_stride, sp, units, splits, pdl, s);
+}
+
+}  // namespace moe
