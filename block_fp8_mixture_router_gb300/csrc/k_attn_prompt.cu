@@ -30,7 +30,6 @@ constexpr int kPThreads = 448;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 13;
 constexpr int kKeys = 128;          // keys of a tile
 constexpr int kChunk = 64;          // keys of a widened piece of V
-constexpr int kMeta = 8;            // tiles whose scales are kept
 // Weights as p x 2^10 in fp16, p against a reference that may lag the row's maximum
 // by kLag powers of two: sums are scaled again only when a score outgrows that.
 constexpr float kShiftLog = 10.0f;
@@ -49,6 +48,9 @@ struct Pr {
   static constexpr int kVStages = D == 256 ? 1 : 2;
   static constexpr int kCStages = D == 256 ? 2 : 4;    // widened pieces
   static constexpr int kCBytes = kChunk * D * 2;
+  // tiles whose scales are kept: the softmax warps read a tile's when the TMA warp writes
+  // those of the fourth behind it (two stages of keys) or the fifth (three) at the latest
+  static constexpr int kMeta = D == 256 ? 6 : 8;
 };
 
 struct alignas(16) Meta {
@@ -57,9 +59,11 @@ struct alignas(16) Meta {
 
 template <int D>
 struct PrSmem {
+  static constexpr int kMeta = Pr<D>::kMeta;
   float fac[Pr<D>::kTiles * 128]; // score factors of the rows, but for the key's scale
   Meta meta[kMeta][kKeys / 16];
   float top[kMeta];              // a tile's largest value scale
+  uint32_t absent[kMeta];        // a tile's 16-key groups without a page
   uint32_t poison[kMeta][4];     // keys of a tile that have a NaN value
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], c_full[4], c_empty[4];
   uint64_t meta_full[kMeta], poison_full[kMeta];
@@ -275,14 +279,18 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
       sub = lane - (kt - base) * per_tile;
       const bool mine = sub >= 0 && sub < per_tile;
       boxes = __popc(__ballot_sync(0xffffffffu, mine && on));
-      const int slot = (kt - w.t0) & (kMeta - 1);
+      const int slot = (kt - w.t0) % C::kMeta;
       // (the softmax warps are at most a few tiles behind the keys' copies)
       if (mine)
         for (int g = sub * box / 16; g < (sub + 1) * box / 16; ++g)
           sm.meta[slot][g] = Meta{ks, __log2f(vs), __fdiv_rn(1.0f, vs), vs};
-      float top = mine && on ? vs : 0.0f;
-      top = warp_max(top);
-      if (lane == 0) sm.top[slot] = top;
+      const float top = warp_max(mine && on ? vs : 0.0f);
+      const uint32_t absent = __reduce_or_sync(
+          0xffffffffu, mine && !on ? ((1u << (box / 16)) - 1) << (sub * box / 16) : 0u);
+      if (lane == 0) {
+        sm.top[slot] = top;
+        sm.absent[slot] = absent;
+      }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.meta_full[slot]);
       wait(&sm.k_empty[rk.i], rk.phase ^ 1, &sm.abort, a.status);
@@ -325,13 +333,11 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
   const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
   Ring rv, rc;
   for (int kt = w.t0; kt < w.t1; ++kt) {
-    const int n = kt - w.t0, slot = n & (kMeta - 1);
-    wait(&sm.meta_full[slot], (n / kMeta) & 1, &sm.abort, a.status);
+    const int n = kt - w.t0, slot = n % C::kMeta;
+    wait(&sm.meta_full[slot], (n / C::kMeta) & 1, &sm.abort, a.status);
     wait(&sm.v_full[rv.i], rv.phase, &sm.abort, a.status);
     const uint8_t* v = sv + (size_t)rv.i * C::kTileBytes;
-    bool whole = !edge_tile(a, w, kt, pos0, pos1);
-#pragma unroll
-    for (int g = 0; g < kKeys / 16; ++g) whole &= sm.meta[slot][g].ks >= 0.0f;
+    const bool whole = !edge_tile(a, w, kt, pos0, pos1) && sm.absent[slot] == 0;
     if (!whole) {
       if (t < 4) sm.poison[slot][t] = 0;
       asm volatile("bar.sync 2, 128;\n" ::: "memory");
@@ -503,10 +509,48 @@ struct RowMask {
   uint32_t poison[4];   // columns with a NaN value
 };
 
+// Largest score of 16 columns, in the queries' units.
+template <bool kEdge>
+__device__ __forceinline__ float peak16(const uint32_t* v, int col0, const RowMask& mk) {
+  float x[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    x[c] = __uint_as_float(v[c]);
+    if (kEdge && (col0 + c < mk.low || col0 + c > mk.high)) x[c] = -INFINITY;
+  }
+  if (kEdge && ((mk.absent >> (col0 / 16)) & 1)) return -INFINITY;
+  float y[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    y[c] = fmaxf(fmaxf(x[4 * c], x[4 * c + 1]), fmaxf(x[4 * c + 2], x[4 * c + 3]));
+  return fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+}
+
+// The row's largest score over a tile, in log2 units (f: the groups' factors).
+template <bool kEdge>
+__device__ __forceinline__ float tile_peak(uint32_t t_s, const float (&f)[kKeys / 16],
+                                           const RowMask& mk) {
+  float peak = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < kKeys; b += 64) {
+    uint32_t v[2][32];
+    tc::tmem_ld_async(t_s + b, v[0]);
+    tc::tmem_ld_async(t_s + b + 32, v[1]);
+    tc::wait_ld();
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float x = peak16<kEdge>(&v[g >> 1][16 * (g & 1)], b + 16 * g, mk);
+      peak = kEdge ? (x == -INFINITY ? peak : fmaxf(peak, x * f[b / 16 + g]))
+                   : fmaxf(peak, x * f[b / 16 + g]);
+    }
+  }
+  return peak;
+}
+
 // Weights of 32 columns (two 16-key groups) from the scores in v, packed to fp16.
 template <bool kEdge>
 __device__ __forceinline__ void weigh32(const uint32_t (&v)[32], uint32_t (&p)[16], int col0,
-                                        const float (&f)[2], const float (&base)[2],
+                                        const float* f, const float (&base)[2],
                                         const float (&inv)[2], const RowMask& mk, float& l) {
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
@@ -553,21 +597,21 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
   uint32_t s_phase[2] = {0, 0}, pv_phase[2] = {0, 0};
   const int n = w.t1 - w.t0;
   for (int i = 0; i < n; ++i) {
-    const int kt = w.t0 + i, slot = i & (kMeta - 1);
+    const int kt = w.t0 + i, slot = i % C::kMeta;
     const int buf = C::kTiles == 2 ? tile : (i & 1);
     const int last_buf = C::kTiles == 2 ? tile : (buf ^ 1);
-    wait(&sm.meta_full[slot], (i / kMeta) & 1, abort, a.status);
+    wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
     const float top = sm.top[slot];
-    uint32_t absent = 0;
+    const bool edge = edge_tile(a, w, kt, pos0, pos1) || sm.absent[slot] != 0;
+    float f[kKeys / 16];
 #pragma unroll
-    for (int g = 0; g < kKeys / 16; ++g) absent |= sm.meta[slot][g].ks < 0.0f ? 1u << g : 0u;
-    const bool edge = edge_tile(a, w, kt, pos0, pos1) || absent != 0;
+    for (int g = 0; g < kKeys / 16; ++g) f[g] = fac * sm.meta[slot][g].ks;
     RowMask mk;
     if (edge) {
-      wait(&sm.poison_full[slot], (i / kMeta) & 1, abort, a.status);
+      wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
       mk.high = min(pos - kt * kKeys, kKeys);
       mk.low = a.window ? pos - a.window + 1 - kt * kKeys : -1;
-      mk.absent = absent;
+      mk.absent = sm.absent[slot];
 #pragma unroll
       for (int k = 0; k < 4; ++k) mk.poison[k] = sm.poison[slot][k];
     }
@@ -576,26 +620,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
     tc::fence_after_sync();
     __syncwarp();
     const uint32_t t_s = tmem + lanes + buf * 128;
-    // the row's largest score, 32 columns at a time
-    float peak = -INFINITY;
-#pragma unroll
-    for (int b = 0; b < kKeys; b += 32) {
-      uint32_t v[32];
-      tc::tmem_ld_async(t_s + b, v);
-      tc::wait_ld();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int c = 16 * g; c < 16 * g + 16; ++c) {
-          const float y = __uint_as_float(v[c]);
-          if (!edge || (b + c >= mk.low && b + c <= mk.high)) x = fmaxf(x, y);
-        }
-        const float f = fac * sm.meta[slot][b / 16 + g].ks;
-        if (edge && ((absent >> (b / 16 + g)) & 1)) x = -INFINITY;
-        if (x != -INFINITY) peak = fmaxf(peak, x * f);
-      }
-    }
+    const float peak = edge ? tile_peak<true>(t_s, f, mk) : tile_peak<false>(t_s, f, mk);
     if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
       // new references for the warp's rows, and their sums brought to them
       const float m_new = fmaxf(m, peak);
@@ -628,20 +653,19 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
     for (int b = 0; b < kKeys; b += 32) {
       uint32_t v[32], p[16];
       tc::tmem_ld_async(t_s + b, v);
-      float f[2], base[2], inv[2];
+      float base[2], inv[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const Meta me = sm.meta[slot][b / 16 + g];
-        f[g] = fac * me.ks;
         // a page below 2^-70 of the largest adds no value that counts
         base[g] = fmaxf(me.log_vs + log_up, -60.0f) - m_base;
         inv[g] = fminf(me.inv_vs * down, 0x1p60f);
       }
       tc::wait_ld();
       if (edge)
-        weigh32<true>(v, p, b, f, base, inv, mk, l);
+        weigh32<true>(v, p, b, f + b / 16, base, inv, mk, l);
       else
-        weigh32<false>(v, p, b, f, base, inv, mk, l);
+        weigh32<false>(v, p, b, f + b / 16, base, inv, mk, l);
       // over scores that have been read: columns b/2 .. b/2 + 15
       tc::tmem_st(t_s + b / 2, p);
     }
@@ -720,7 +744,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc::mbar_init(&sm.c_full[i], 4);
       tc::mbar_init(&sm.c_empty[i], 1);
     }
-    for (int i = 0; i < kMeta; ++i) {
+    for (int i = 0; i < C::kMeta; ++i) {
       tc::mbar_init(&sm.meta_full[i], 1);
       tc::mbar_init(&sm.poison_full[i], 4);
     }
