@@ -53,17 +53,20 @@ struct Pr {
   static constexpr int kMeta = D == 256 ? 6 : 8;
 };
 
+// What the softmax warps need of a tile's pages, for each of its 16-key groups.
 struct alignas(16) Meta {
-  float ks, log_vs, inv_vs, vs;  // ks < 0: the page does not exist (or is not needed)
+  float ks[kKeys / 16];       // key scales
+  float log_vs[kKeys / 16];   // value scales: log2, and one over
+  float inv_vs[kKeys / 16];
+  float top;                  // the largest value scale
+  uint32_t absent;            // groups whose page does not exist (or is not needed)
 };
 
 template <int D>
 struct PrSmem {
   static constexpr int kMeta = Pr<D>::kMeta;
   float fac[Pr<D>::kTiles * 128]; // score factors of the rows, but for the key's scale
-  Meta meta[kMeta][kKeys / 16];
-  float top[kMeta];              // a tile's largest value scale
-  uint32_t absent[kMeta];        // a tile's 16-key groups without a page
+  Meta meta[kMeta];
   uint32_t poison[kMeta][4];     // keys of a tile that have a NaN value
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], c_full[4], c_empty[4];
   uint64_t meta_full[kMeta], poison_full[kMeta];
@@ -283,13 +286,17 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
       // (the softmax warps are at most a few tiles behind the keys' copies)
       if (mine)
         for (int g = sub * box / 16; g < (sub + 1) * box / 16; ++g)
-          sm.meta[slot][g] = Meta{ks, __log2f(vs), __fdiv_rn(1.0f, vs), vs};
+        {
+          sm.meta[slot].ks[g] = ks;
+          sm.meta[slot].log_vs[g] = __log2f(vs);
+          sm.meta[slot].inv_vs[g] = __fdiv_rn(1.0f, vs);
+        }
       const float top = warp_max(mine && on ? vs : 0.0f);
       const uint32_t absent = __reduce_or_sync(
           0xffffffffu, mine && !on ? ((1u << (box / 16)) - 1) << (sub * box / 16) : 0u);
       if (lane == 0) {
-        sm.top[slot] = top;
-        sm.absent[slot] = absent;
+        sm.meta[slot].top = top;
+        sm.meta[slot].absent = absent;
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.meta_full[slot]);
@@ -337,7 +344,7 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
     wait(&sm.meta_full[slot], (n / C::kMeta) & 1, &sm.abort, a.status);
     wait(&sm.v_full[rv.i], rv.phase, &sm.abort, a.status);
     const uint8_t* v = sv + (size_t)rv.i * C::kTileBytes;
-    const bool whole = !edge_tile(a, w, kt, pos0, pos1) && sm.absent[slot] == 0;
+    const bool whole = !edge_tile(a, w, kt, pos0, pos1) && sm.meta[slot].absent == 0;
     if (!whole) {
       if (t < 4) sm.poison[slot][t] = 0;
       asm volatile("bar.sync 2, 128;\n" ::: "memory");
@@ -349,7 +356,7 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
       bool live = true, poison = false;
       if (!whole)
         live = kt * kKeys + key >= w.lo && kt * kKeys + key < w.hi &&
-               sm.meta[slot][key >> 4].ks >= 0.0f;
+               !((sm.meta[slot].absent >> (key >> 4)) & 1);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int b = h * (D / 2) + 16 * i;        // first of 16 values
@@ -509,72 +516,92 @@ struct RowMask {
   uint32_t poison[4];   // columns with a NaN value
 };
 
-// Largest score of 16 columns, in the queries' units.
+// The largest score of a row over a tile, in log2 units, from tensor memory; the
+// next columns are on their way while 32 are looked at.
 template <bool kEdge>
-__device__ __forceinline__ float peak16(const uint32_t* v, int col0, const RowMask& mk) {
-  float x[16];
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    x[c] = __uint_as_float(v[c]);
-    if (kEdge && (col0 + c < mk.low || col0 + c > mk.high)) x[c] = -INFINITY;
-  }
-  if (kEdge && ((mk.absent >> (col0 / 16)) & 1)) return -INFINITY;
-  float y[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    y[c] = fmaxf(fmaxf(x[4 * c], x[4 * c + 1]), fmaxf(x[4 * c + 2], x[4 * c + 3]));
-  return fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-}
-
-// The row's largest score over a tile, in log2 units (f: the groups' factors).
-template <bool kEdge>
-__device__ __forceinline__ float tile_peak(uint32_t t_s, const float (&f)[kKeys / 16],
+__device__ __forceinline__ float tile_peak(uint32_t t_s, const Meta& me, float fac,
                                            const RowMask& mk) {
   float peak = -INFINITY;
+  uint32_t v[2][32];
+  tc::tmem_ld_async(t_s, v[0]);
+  float2 ks = *reinterpret_cast<const float2*>(me.ks);
 #pragma unroll
-  for (int b = 0; b < kKeys; b += 64) {
-    uint32_t v[2][32];
-    tc::tmem_ld_async(t_s + b, v[0]);
-    tc::tmem_ld_async(t_s + b + 32, v[1]);
+  for (int b = 0; b < kKeys / 32; ++b) {
+    const float f[2] = {fac * ks.x, fac * ks.y};
     tc::wait_ld();
+    if (b + 1 < kKeys / 32) {
+      tc::tmem_ld_async(t_s + 32 * (b + 1), v[(b + 1) & 1]);
+      ks = *reinterpret_cast<const float2*>(me.ks + 2 * (b + 1));
+    }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float x = peak16<kEdge>(&v[g >> 1][16 * (g & 1)], b + 16 * g, mk);
-      peak = kEdge ? (x == -INFINITY ? peak : fmaxf(peak, x * f[b / 16 + g]))
-                   : fmaxf(peak, x * f[b / 16 + g]);
+    for (int g = 0; g < 2; ++g) {
+      float x[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        x[c] = __uint_as_float(v[b & 1][16 * g + c]);
+        const int col = 32 * b + 16 * g + c;
+        if (kEdge && (col < mk.low || col > mk.high)) x[c] = -INFINITY;
+      }
+      float y[5];
+#pragma unroll
+      for (int c = 0; c < 5; ++c) y[c] = fmaxf(fmaxf(x[3 * c], x[3 * c + 1]), x[3 * c + 2]);
+      float m = fmaxf(fmaxf(y[0], y[1]), y[2]);
+      m = fmaxf(fmaxf(m, y[3]), y[4]);
+      m = fmaxf(m, x[15]);
+      if (kEdge && (((mk.absent >> (2 * b + g)) & 1) || m == -INFINITY)) continue;
+      peak = fmaxf(peak, m * f[g]);
     }
   }
   return peak;
 }
 
-// Weights of 32 columns (two 16-key groups) from the scores in v, packed to fp16.
+// Weights of a row over a tile, 2^(s f + base) by groups of 16 keys, as fp16 over the
+// scores that have been read; returns their sum freed of the pages' value scales.
 template <bool kEdge>
-__device__ __forceinline__ void weigh32(const uint32_t (&v)[32], uint32_t (&p)[16], int col0,
-                                        const float* f, const float (&base)[2],
-                                        const float (&inv)[2], const RowMask& mk, float& l) {
+__device__ __forceinline__ float weigh(uint32_t t_s, const Meta& me, float fac, float log_up,
+                                       float down, float m_base, const RowMask& mk) {
+  float sum = 0.0f;
+  uint32_t v[2][16], p[16];
+  tc::tmem_ld_async(t_s, v[0]);
+  float ks = me.ks[0], lv = me.log_vs[0], iv = me.inv_vs[0];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float2 ff = make_float2(f[g], f[g]), bb = make_float2(base[g], base[g]);
-    float2 sum = make_float2(0.0f, 0.0f);
+  for (int g = 0; g < kKeys / 16; ++g) {
+    const float f = fac * ks;
+    // a page below 2^-70 of the largest adds no value that counts
+    const float base = fmaxf(lv + log_up, -60.0f) - m_base;
+    const float inv = fminf(iv * down, 0x1p60f);
+    tc::wait_ld();
+    if (g + 1 < kKeys / 16) {
+      tc::tmem_ld_async(t_s + 16 * (g + 1), v[(g + 1) & 1]);
+      ks = me.ks[g + 1];
+      lv = me.log_vs[g + 1];
+      iv = me.inv_vs[g + 1];
+    }
+    const uint32_t(&s)[16] = v[g & 1];
+    const float2 ff = make_float2(f, f), bb = make_float2(base, base);
+    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = 16 * g + 2 * i;
-      float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), ff, bb);
+      float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, bb);
       x.x = exp2_approx(x.x);
       x.y = exp2_approx(x.y);
       if constexpr (kEdge) {
-        const uint32_t bad = mk.poison[col0 / 32];
-        if (bad & (1u << c)) x.x = __int_as_float(0x7FFFFFFF);
-        if (bad & (2u << c)) x.y = __int_as_float(0x7FFFFFFF);
-        const bool none = (mk.absent >> (col0 / 16 + g)) & 1;
-        if (none || col0 + c < mk.low || col0 + c > mk.high) x.x = 0.0f;
-        if (none || col0 + c + 1 < mk.low || col0 + c + 1 > mk.high) x.y = 0.0f;
+        const int c = 16 * g + 2 * i;
+        const bool there = !((mk.absent >> g) & 1);
+        const uint32_t bad = mk.poison[g >> 1] >> (16 * (g & 1) + 2 * i);
+        if (bad & 1) x.x = __int_as_float(0x7FFFFFFF);
+        if (bad & 2) x.y = __int_as_float(0x7FFFFFFF);
+        if (!there || c < mk.low || c > mk.high) x.x = 0.0f;
+        if (!there || c + 1 < mk.low || c + 1 > mk.high) x.y = 0.0f;
       }
-      sum = add2(sum, x);
-      p[8 * g + i] = f16x2_of(x.x, x.y);
+      acc[i & 1] = add2(acc[i & 1], x);
+      p[8 * (g & 1) + i] = f16x2_of(x.x, x.y);
     }
-    l = fmaf(sum.x + sum.y, inv[g], l);
+    const float2 t = add2(acc[0], acc[1]);
+    sum = fmaf(t.x + t.y, inv, sum);
+    if (g & 1) tc::tmem_st(t_s + 8 * (g - 1), p);
   }
+  return sum;
 }
 
 template <int D>
@@ -601,17 +628,15 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
     const int buf = C::kTiles == 2 ? tile : (i & 1);
     const int last_buf = C::kTiles == 2 ? tile : (buf ^ 1);
     wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
-    const float top = sm.top[slot];
-    const bool edge = edge_tile(a, w, kt, pos0, pos1) || sm.absent[slot] != 0;
-    float f[kKeys / 16];
-#pragma unroll
-    for (int g = 0; g < kKeys / 16; ++g) f[g] = fac * sm.meta[slot][g].ks;
+    const Meta& me = sm.meta[slot];
+    const float top = me.top;
+    const bool edge = edge_tile(a, w, kt, pos0, pos1) || me.absent != 0;
     RowMask mk;
     if (edge) {
       wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
       mk.high = min(pos - kt * kKeys, kKeys);
       mk.low = a.window ? pos - a.window + 1 - kt * kKeys : -1;
-      mk.absent = sm.absent[slot];
+      mk.absent = me.absent;
 #pragma unroll
       for (int k = 0; k < 4; ++k) mk.poison[k] = sm.poison[slot][k];
     }
@@ -620,7 +645,8 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
     tc::fence_after_sync();
     __syncwarp();
     const uint32_t t_s = tmem + lanes + buf * 128;
-    const float peak = edge ? tile_peak<true>(t_s, f, mk) : tile_peak<false>(t_s, f, mk);
+    const float peak =
+        edge ? tile_peak<true>(t_s, me, fac, mk) : tile_peak<false>(t_s, me, fac, mk);
     if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
       // new references for the warp's rows, and their sums brought to them
       const float m_new = fmaxf(m, peak);
@@ -649,26 +675,8 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       }
     }
     const float m_base = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int b = 0; b < kKeys; b += 32) {
-      uint32_t v[32], p[16];
-      tc::tmem_ld_async(t_s + b, v);
-      float base[2], inv[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const Meta me = sm.meta[slot][b / 16 + g];
-        // a page below 2^-70 of the largest adds no value that counts
-        base[g] = fmaxf(me.log_vs + log_up, -60.0f) - m_base;
-        inv[g] = fminf(me.inv_vs * down, 0x1p60f);
-      }
-      tc::wait_ld();
-      if (edge)
-        weigh32<true>(v, p, b, f + b / 16, base, inv, mk, l);
-      else
-        weigh32<false>(v, p, b, f + b / 16, base, inv, mk, l);
-      // over scores that have been read: columns b/2 .. b/2 + 15
-      tc::tmem_st(t_s + b / 2, p);
-    }
+    l += edge ? weigh<true>(t_s, me, fac, log_up, down, m_base, mk)
+              : weigh<false>(t_s, me, fac, log_up, down, m_base, mk);
     tc::wait_st();
     tc::fence_before_sync();
     tc::mbar_arrive(&sm.p_full[buf]);
@@ -771,7 +779,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (any) copy_tiles<D>(a, w, &kmap, &vmap, sk, sv, sm);
   } else if (warp == kMmaWarp) {
     if (any) issue<D>(a, w, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc), tmem, sm);
-  } else if (warp >= kConvWarp) {
+  } else if (warp >= kConvWarp && warp < kMmaWarp) {
     if (any) widen_tiles<D>(a, w, sv, sc, sm);
   } else if (warp < 4 * C::kTiles && warp / 4 < w.tiles) {
     const int tile = warp / 4, row = tid & 127;
