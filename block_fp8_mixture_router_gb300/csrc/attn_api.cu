@@ -201,14 +201,14 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-bool encode_pool(CUtensorMap* m, const void* pool, const AttnArgs& a, int D) {
+bool encode_pool(CUtensorMap* m, const void* pool, const AttnArgs& a, int D, int most) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   if (!encode) return false;
   const cuuint64_t tokens = (cuuint64_t)a.Hkv << a.page_shift;
   const cuuint64_t dims[3] = {(cuuint64_t)D, tokens, (cuuint64_t)a.n_pages};
   const cuuint64_t strides[2] = {(cuuint64_t)D, tokens * D};
   const cuuint32_t box[3] = {(cuuint32_t)std::min(D, 128),
-                             (cuuint32_t)std::min(1 << a.page_shift, kAttnKeys), 1};
+                             (cuuint32_t)std::min(1 << a.page_shift, most), 1};
   const cuuint32_t unit[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
                 unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -223,10 +223,11 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const long long cap = (long long)b->pages_stride << c->page_shift;
   const long long keys = b->max_kv_len > 0 ? std::min<long long>(b->max_kv_len, cap) : cap;
   const int seq_rows = b->max_seq_rows > 0 ? std::min(b->max_seq_rows, b->rows) : b->rows;
-  AttnMaps maps;
-  if (!make_attn_maps(&maps, a, D)) return MOE_ERR_CUDA;
   // Many rows of a sequence: the prompt kernel, whose row tiles hold 128.
-  if ((long long)seq_rows * a.g > kPromptRows) {
+  const bool prompt = (long long)seq_rows * a.g > kPromptRows;
+  AttnMaps maps;
+  if (!make_attn_maps(&maps, a, D, prompt)) return MOE_ERR_CUDA;
+  if (prompt) {
     const long long units = b->rows / attn_prompt_tokens(D, a.g) + (long long)b->n_seqs;
     const long long heads = units * a.Hkv, tiles = (keys + 127) / 128;
     long long splits = 1;
@@ -261,8 +262,9 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
 }  // namespace
 
 namespace moe {
-bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D) {
-  return encode_pool(&m->k, a.kc, a, D) && encode_pool(&m->v, a.vc, a, D);
+bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D, bool prompt) {
+  return encode_pool(&m->k, a.kc, a, D, 128) &&
+         (prompt ? encode_pool(&m->v64, a.vc, a, D, 64) : encode_pool(&m->v, a.vc, a, D, 128));
 }
 }  // namespace moe
 

@@ -79,12 +79,13 @@ struct AppendArgs {
 cudaError_t launch_append(int D, const AttnArgs& a, const AppendArgs& p, cudaStream_t s);
 
 // The cache's codes as the TMA sees them: [page][kv_heads x page_tokens][head_dim],
-// a box of a page's tokens of a head, 128 bytes of each (64 at
-// head_dim 64), stored with the swizzle of that width.
+// a box of a page's tokens of a head (v64: at most 64 of them), 128 bytes of each (64
+// at head_dim 64), stored with the swizzle of that width.
 struct AttnMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v, v64;
 };
-bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D);
+// Encodes k and v, or, for the prompt kernel, k and v64.
+bool make_attn_maps(AttnMaps* m, const AttnArgs& a, int D, bool prompt);
 
 cudaError_t setup_attn_decode(int D);
 int attn_decode_slots(int D, int sm_count);  // CTAs of a full grid

@@ -260,7 +260,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
     const int y = u.h << a.page_shift;
     for (int i = 0; i < tiles; ++i) {
       tc::wait_bounded(&sm.empty[r.stage], r.phase ^ 1, &sm.abort, a.status);
-      if (*(volatile int*)&sm.abort) return;
+      if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) return;
       const int sub = lane - i * per_tile;  // this lane's box in the tile
       const bool mine = sub >= 0 && sub < per_tile;
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine && on));

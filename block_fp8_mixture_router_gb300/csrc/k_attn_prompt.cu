@@ -13,7 +13,7 @@
 //   bits is two e4m3 values, Qhi + Qlo, multiplied in two passes at twice the
 //   16-bit rate: the same time as one 16-bit product, without converting K.
 // - P V: kind::f16; four warps widen V's codes to fp16 once for all the CTA's rows, P
-//   goes to tensor memory as fp16 over the scores it came from.
+//   goes through shared memory (tensor memory at head_dim 256) as fp16.
 // - Two row tiles take turns: while the softmax warps of one work, the tensor cores
 //   have the other's products.
 //
@@ -38,19 +38,26 @@ constexpr float kLag = 5.0f;
 template <int D>
 struct Pr {
   static constexpr int kTiles = D == 256 ? 1 : 2;      // row tiles of a CTA
+  // Where the weights go: with two row tiles to shared memory, so that a row tile's one
+  // score buffer is free for the next tile's scores once they have been read; with one
+  // row tile and two score buffers to tensor memory, over the scores they came from.
+  static constexpr bool kPSmem = kTiles == 2;
   static constexpr bool kWide = D >= 128;
   static constexpr int kRowBytes = kWide ? 128 : 64;
   static constexpr int kPanels = D / kRowBytes;
   static constexpr int kPanelBytes = kKeys * kRowBytes;
-  static constexpr int kTileBytes = kKeys * D;         // keys or values of a tile, as stored
+  static constexpr int kTileBytes = kKeys * D;         // keys of a tile, as stored
   static constexpr int kQBytes = 128 * D;              // one part of a row tile's queries
-  static constexpr int kKStages = D == 256 ? 2 : 3;
-  static constexpr int kVStages = D == 256 ? 1 : 2;
-  static constexpr int kCStages = D == 256 ? 2 : 4;    // widened pieces
+  static constexpr int kPBytes = kPSmem ? 128 * kKeys * 2 : 0;  // a row tile's weights
+  static constexpr int kKStages = D == 64 ? 3 : 2;
+  static constexpr int kVStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // pieces of V, as stored
+  static constexpr int kVPanelBytes = kChunk * kRowBytes;
+  static constexpr int kVBytes = kChunk * D;
+  static constexpr int kCStages = D == 64 ? 4 : 2;     // pieces of V, widened
   static constexpr int kCBytes = kChunk * D * 2;
   // tiles whose scales are kept: the softmax warps read a tile's when the TMA warp writes
   // those of the fourth behind it (two stages of keys) or the fifth (three) at the latest
-  static constexpr int kMeta = D == 256 ? 6 : 8;
+  static constexpr int kMeta = 6;
 };
 
 // What the softmax warps need of a tile's pages, for each of its 16-key groups.
@@ -68,7 +75,7 @@ struct PrSmem {
   float fac[Pr<D>::kTiles * 128]; // score factors of the rows, but for the key's scale
   Meta meta[kMeta];
   uint32_t poison[kMeta][4];     // keys of a tile that have a NaN value
-  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], c_full[4], c_empty[4];
+  uint64_t k_full[3], k_empty[3], v_full[4], v_empty[4], c_full[4], c_empty[4];
   uint64_t meta_full[kMeta], poison_full[kMeta];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
   uint32_t tmem;
@@ -78,9 +85,9 @@ struct PrSmem {
 template <int D>
 constexpr size_t pr_smem_bytes() {
   using C = Pr<D>;
-  return 1024 + (size_t)C::kTiles * 2 * C::kQBytes + (size_t)C::kKStages * C::kTileBytes +
-         (size_t)C::kVStages * C::kTileBytes + (size_t)C::kCStages * C::kCBytes +
-         sizeof(PrSmem<D>);
+  return 1024 + (size_t)C::kTiles * (2 * C::kQBytes + C::kPBytes) +
+         (size_t)C::kKStages * C::kTileBytes + (size_t)C::kVStages * C::kVBytes +
+         (size_t)C::kCStages * C::kCBytes + sizeof(PrSmem<D>);
 }
 
 static_assert(pr_smem_bytes<64>() <= 232448 && pr_smem_bytes<128>() <= 232448 &&
@@ -135,6 +142,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// D[tmem] (+)= A[smem, fp16] * B[smem, fp16], as above.
+__device__ __forceinline__ void mma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  tc::mma_warp<false>(d, a, b, idesc, accumulate);
 }
 
 struct Ring {
@@ -237,13 +256,8 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
   const int per_tile = kKeys / box;
   const int batch = 32 / per_tile;
   const int y = w.h << a.page_shift;
+  const int vbox = min(box, kChunk), v_per = kChunk / vbox;  // boxes of a piece of V
   Ring rk, rv;
-  const auto copy = [&](uint8_t* to, const CUtensorMap* map, int sub, int page, uint64_t* bar) {
-#pragma unroll
-    for (int p = 0; p < C::kPanels; ++p)
-      tc::tma_load_3d(to + p * C::kPanelBytes + sub * box * C::kRowBytes, map, p * 128, y, page,
-                      bar);
-  };
   // keys of tile kt + 1 go out before the values of tile kt: they are needed first
   int page = 0, page_next = 0;
   bool on = false, on_next = false;
@@ -267,7 +281,7 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
       }
     }
   };
-  int v_page = 0, v_boxes = 0, v_sub = -1;
+  int v_page = 0, v_sub = -1;
   bool v_on = false;
   for (int kt = w.t0; kt <= w.t1; ++kt) {
     int sub = -1;
@@ -301,24 +315,40 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.meta_full[slot]);
       wait(&sm.k_empty[rk.i], rk.phase ^ 1, &sm.abort, a.status);
-      if (*(volatile int*)&sm.abort) return;
+      if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) return;
       if (lane == 0) tc::mbar_arrive_expect_tx(&sm.k_full[rk.i], boxes * box * D);
       __syncwarp();
-      if (mine && on) copy(sk + (size_t)rk.i * C::kTileBytes, kmap, sub, page, &sm.k_full[rk.i]);
+      if (mine && on)
+#pragma unroll
+        for (int p = 0; p < C::kPanels; ++p)
+          tc::tma_load_3d(sk + (size_t)rk.i * C::kTileBytes + p * C::kPanelBytes +
+                              sub * box * C::kRowBytes,
+                          kmap, p * 128, y, page, &sm.k_full[rk.i]);
       rk.next(C::kKStages);
     }
     if (kt > w.t0) {
-      wait(&sm.v_empty[rv.i], rv.phase ^ 1, &sm.abort, a.status);
-      if (*(volatile int*)&sm.abort) return;
-      if (lane == 0) tc::mbar_arrive_expect_tx(&sm.v_full[rv.i], v_boxes * box * D);
-      __syncwarp();
-      if (v_on) copy(sv + (size_t)rv.i * C::kTileBytes, vmap, v_sub, v_page, &sm.v_full[rv.i]);
-      rv.next(C::kVStages);
+      for (int c = 0; c < kKeys / kChunk; ++c) {
+        // (a page of 128 tokens has a box in both pieces)
+        const int at = box > kChunk ? 0 : v_sub - c * v_per;
+        const bool mine = v_on && at >= 0 && at < v_per;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+        wait(&sm.v_empty[rv.i], rv.phase ^ 1, &sm.abort, a.status);
+        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) return;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&sm.v_full[rv.i], n * vbox * D);
+        __syncwarp();
+        if (mine)
+#pragma unroll
+          for (int p = 0; p < C::kPanels; ++p)
+            tc::tma_load_3d(sv + (size_t)rv.i * C::kVBytes + p * C::kVPanelBytes +
+                                at * vbox * C::kRowBytes,
+                            vmap, p * 128, y + (box > kChunk ? c * kChunk : 0), v_page,
+                            &sm.v_full[rv.i]);
+        rv.next(C::kVStages);
+      }
     }
     v_on = sub >= 0 && sub < per_tile && on;
     v_sub = sub;
     v_page = page;
-    v_boxes = (int)boxes;
   }
 }
 
@@ -342,15 +372,15 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
   for (int kt = w.t0; kt < w.t1; ++kt) {
     const int n = kt - w.t0, slot = n % C::kMeta;
     wait(&sm.meta_full[slot], (n / C::kMeta) & 1, &sm.abort, a.status);
-    wait(&sm.v_full[rv.i], rv.phase, &sm.abort, a.status);
-    const uint8_t* v = sv + (size_t)rv.i * C::kTileBytes;
     const bool whole = !edge_tile(a, w, kt, pos0, pos1) && sm.meta[slot].absent == 0;
     if (!whole) {
       if (t < 4) sm.poison[slot][t] = 0;
       asm volatile("bar.sync 2, 128;\n" ::: "memory");
     }
     for (int c = 0; c < 2; ++c) {
+      wait(&sm.v_full[rv.i], rv.phase, &sm.abort, a.status);
       wait(&sm.c_empty[rc.i], rc.phase ^ 1, &sm.abort, a.status);
+      const uint8_t* v = sv + (size_t)rv.i * C::kVBytes;
       uint8_t* out = sc + (size_t)rc.i * C::kCBytes;
       const int key = c * kChunk + k;
       bool live = true, poison = false;
@@ -360,8 +390,8 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int b = h * (D / 2) + 16 * i;        // first of 16 values
-        uint4 x = *reinterpret_cast<const uint4*>(v + b / C::kRowBytes * C::kPanelBytes +
-                                                  swz<C::kWide>(key, b % C::kRowBytes));
+        uint4 x = *reinterpret_cast<const uint4*>(v + b / C::kRowBytes * C::kVPanelBytes +
+                                                  swz<C::kWide>(k, b % C::kRowBytes));
         if (!whole) {
           // values that do not exist become zeros, and NaN codes too: the rows that do see
           // such a key get a NaN weight instead (0 x NaN would reach the others)
@@ -389,15 +419,15 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
       }
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.c_full[rc.i]);
+      if (lane == 0) {
+        tc::mbar_arrive(&sm.c_full[rc.i]);
+        tc::mbar_arrive(&sm.v_empty[rv.i]);
+      }
       rc.next(C::kCStages);
+      rv.next(C::kVStages);
     }
     __syncwarp();
-    if (lane == 0) {
-      tc::mbar_arrive(&sm.v_empty[rv.i]);
-      tc::mbar_arrive(&sm.poison_full[slot]);
-    }
-    rv.next(C::kVStages);
+    if (lane == 0) tc::mbar_arrive(&sm.poison_full[slot]);
   }
 }
 
@@ -406,7 +436,7 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
 // alternates between the two.
 template <int D>
 __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t sq, uint32_t sk,
-                                      uint32_t sc, uint32_t tmem, PrSmem<D>& sm) {
+                                      uint32_t sc, uint32_t sp, uint32_t tmem, PrSmem<D>& sm) {
   using C = Pr<D>;
   constexpr uint32_t id_s = tc::idesc_f8(128, kKeys);
   constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
@@ -415,7 +445,8 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t
   const int tiles = w.tiles;
   const int n = w.t1 - w.t0;
   Ring rk, rc;
-  uint32_t p_phase[2] = {0, 0}, pv_phase[2] = {0, 0};
+  uint32_t p_phase[2] = {0, 0};
+  [[maybe_unused]] uint32_t pv_phase[2] = {0, 0};
   for (int m = 0; m < tiles; ++m) wait(&sm.q_full[m], 0, abort, a.status);
 
   const auto scores = [&](int m, int buf) {  // of the keys in stage rk.i
@@ -445,8 +476,13 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t
       for (int i = 0; i < kChunk / 16; ++i) {
         // 16 keys: two groups of eight rows of 1024 bytes; blocks of 64 values behind
         const uint64_t b = tc::swz_desc(sc + r.i * C::kCBytes + i * 2048, true, kChunk * 128);
-        mma_ts_warp(tmem + 256 + m * D, tmem + buf * 128 + c * 32 + i * 8, b, id_o,
-                    !first || c > 0 || i > 0);
+        const uint32_t acc = !first || c > 0 || i > 0;
+        if constexpr (C::kPSmem)
+          mma_ss_warp(tmem + 256 + m * D,
+                      tc::swz_desc(sp + m * C::kPBytes + c * (128 * 128) + i * 32, true), b, id_o,
+                      acc);
+        else
+          mma_ts_warp(tmem + 256 + m * D, tmem + buf * 128 + c * 32 + i * 8, b, id_o, acc);
       }
       if (m == tiles - 1) tc::commit_warp(&sm.c_empty[r.i]);
       r.next(C::kCStages);
@@ -456,7 +492,7 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t
   };
 
   if constexpr (C::kTiles == 2) {
-    // S(0, t0) S(1, t0) | then for every tile and row tile: its values, its next scores
+    // S(0, t0) S(1, t0) | then for every tile and row tile: its next scores, its values
     wait(&sm.k_full[0], 0, abort, a.status);
     tc::fence_after_sync();
     for (int m = 0; m < tiles; ++m) scores(m, m);
@@ -467,12 +503,8 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t
       for (int m = 0; m < tiles; ++m) {
         wait(&sm.p_full[m], p_phase[m], abort, a.status);
         p_phase[m] ^= 1;
-        tc::fence_after_sync();
-        after = values(m, m, i == 0, rc);
         if (i + 1 < n) {
           if (m == 0) wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
-          // the weights lie where the scores go
-          wait(&sm.pv_done[m], pv_phase[m], abort, a.status);
           tc::fence_after_sync();
           scores(m, m);
           if (m == tiles - 1) {
@@ -480,7 +512,8 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t
             rk.next(C::kKStages);
           }
         }
-        pv_phase[m] ^= 1;
+        tc::fence_after_sync();
+        after = values(m, m, i == 0, rc);
       }
       rc = after;
     }
@@ -544,10 +577,8 @@ __device__ __forceinline__ float tile_peak(uint32_t t_s, const Meta& me, float f
       }
       float y[5];
 #pragma unroll
-      for (int c = 0; c < 5; ++c) y[c] = fmaxf(fmaxf(x[3 * c], x[3 * c + 1]), x[3 * c + 2]);
-      float m = fmaxf(fmaxf(y[0], y[1]), y[2]);
-      m = fmaxf(fmaxf(m, y[3]), y[4]);
-      m = fmaxf(m, x[15]);
+      for (int c = 0; c < 5; ++c) y[c] = max3(x[3 * c], x[3 * c + 1], x[3 * c + 2]);
+      const float m = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15]), -INFINITY);
       if (kEdge && (((mk.absent >> (2 * b + g)) & 1) || m == -INFINITY)) continue;
       peak = fmaxf(peak, m * f[g]);
     }
@@ -555,11 +586,14 @@ __device__ __forceinline__ float tile_peak(uint32_t t_s, const Meta& me, float f
   return peak;
 }
 
-// Weights of a row over a tile, 2^(s f + base) by groups of 16 keys, as fp16 over the
-// scores that have been read; returns their sum freed of the pages' value scales.
-template <bool kEdge>
-__device__ __forceinline__ float weigh(uint32_t t_s, const Meta& me, float fac, float log_up,
-                                       float down, float m_base, const RowMask& mk) {
+// Weights of a row over a tile, 2^(s f + base) by groups of 16 keys, as fp16: to
+// shared memory (p_row: the row's 128 bytes of each 64 keys, its 16-byte columns swizzled
+// by the row), or over the scores that have been read.  Returns their sum freed of the
+// pages' value scales.
+template <bool kEdge, bool kPSmem>
+__device__ __forceinline__ float weigh(uint32_t t_s, uint8_t* p_row, const Meta& me, float fac,
+                                       float log_up, float down, float m_base,
+                                       const RowMask& mk) {
   float sum = 0.0f;
   uint32_t v[2][16], p[16];
   tc::tmem_ld_async(t_s, v[0]);
@@ -599,19 +633,30 @@ __device__ __forceinline__ float weigh(uint32_t t_s, const Meta& me, float fac, 
     }
     const float2 t = add2(acc[0], acc[1]);
     sum = fmaf(t.x + t.y, inv, sum);
-    if (g & 1) tc::tmem_st(t_s + 8 * (g - 1), p);
+    if constexpr (kPSmem) {
+      // columns 2 (g % 4), 2 (g % 4) + 1 of keys 64 (g / 4) on
+      const int x = (threadIdx.x & 7) << 4, b = (g & 1) * 8;
+      uint8_t* to = p_row + (g >> 2) * (128 * 128);
+      *reinterpret_cast<uint4*>(to + (((2 * (g & 3)) << 4) ^ x)) =
+          make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]);
+      *reinterpret_cast<uint4*>(to + (((2 * (g & 3) + 1) << 4) ^ x)) =
+          make_uint4(p[b + 4], p[b + 5], p[b + 6], p[b + 7]);
+    } else if (g & 1) {
+      tc::tmem_st(t_s + 8 * (g - 1), p);
+    }
   }
   return sum;
 }
 
 template <int D>
 __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int tile, uint32_t tmem,
-                                       const float* fac_of, PrSmem<D>& sm, float& m_out,
+                                       const float* fac_of, uint8_t* sp, PrSmem<D>& sm, float& m_out,
                                        float& l_out, float& vref_out) {
   using C = Pr<D>;
   const int row = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(row & 96) << 16;
   const uint32_t t_o = tmem + lanes + 256 + tile * D;
+  uint8_t* p_row = sp + (size_t)tile * C::kPBytes + row * 128;
   int* abort = &sm.abort;
   const int first = w.v.first + w.tok0 + tile * w.tq;        // earliest row of the tile
   const int toks = min(w.tq, w.toks - tile * w.tq);
@@ -675,9 +720,14 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       }
     }
     const float m_base = m == -INFINITY ? 0.0f : m;
-    l += edge ? weigh<true>(t_s, me, fac, log_up, down, m_base, mk)
-              : weigh<false>(t_s, me, fac, log_up, down, m_base, mk);
-    tc::wait_st();
+    // (shared memory: the last tile's weights have been multiplied)
+    if (C::kPSmem && i > 0) wait(&sm.pv_done[last_buf], pv_phase[last_buf] ^ 1, abort, a.status);
+    l += edge ? weigh<true, C::kPSmem>(t_s, p_row, me, fac, log_up, down, m_base, mk)
+              : weigh<false, C::kPSmem>(t_s, p_row, me, fac, log_up, down, m_base, mk);
+    if constexpr (C::kPSmem)
+      tc::fence_async_smem();
+    else
+      tc::wait_st();
     tc::fence_before_sync();
     tc::mbar_arrive(&sm.p_full[buf]);
     pv_phase[buf] ^= 1;
@@ -699,9 +749,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   using C = Pr<D>;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* sq = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* sk = sq + (size_t)C::kTiles * 2 * C::kQBytes;
+  uint8_t* spw = sq + (size_t)C::kTiles * 2 * C::kQBytes;   // weights
+  uint8_t* sk = spw + (size_t)C::kTiles * C::kPBytes;
   uint8_t* sv = sk + (size_t)C::kKStages * C::kTileBytes;
-  uint8_t* sc = sv + (size_t)C::kVStages * C::kTileBytes;
+  uint8_t* sc = sv + (size_t)C::kVStages * C::kVBytes;
   PrSmem<D>& sm = *reinterpret_cast<PrSmem<D>*>(sc + (size_t)C::kCStages * C::kCBytes);
   const int tid = threadIdx.x, warp = tid >> 5;
   // late rows of a prompt see the most keys: they go first
@@ -741,14 +792,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc::mbar_init(&sm.k_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.v_full[i], 1);
-      tc::mbar_init(&sm.v_empty[i], 4);
       tc::mbar_init(&sm.q_full[i], 128);
       tc::mbar_init(&sm.s_full[i], 1);
       tc::mbar_init(&sm.p_full[i], 128);
       tc::mbar_init(&sm.pv_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sm.v_full[i], 1);
+      tc::mbar_init(&sm.v_empty[i], 4);
       tc::mbar_init(&sm.c_full[i], 4);
       tc::mbar_init(&sm.c_empty[i], 1);
     }
@@ -778,7 +829,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (warp == kTmaWarp) {
     if (any) copy_tiles<D>(a, w, &kmap, &vmap, sk, sv, sm);
   } else if (warp == kMmaWarp) {
-    if (any) issue<D>(a, w, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc), tmem, sm);
+    if (any) issue<D>(a, w, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc),
+                      tc::smem_u32(spw), tmem, sm);
   } else if (warp >= kConvWarp && warp < kMmaWarp) {
     if (any) widen_tiles<D>(a, w, sv, sc, sm);
   } else if (warp < 4 * C::kTiles && warp / 4 < w.tiles) {
@@ -789,7 +841,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc::mbar_arrive(&sm.q_full[tile]);
     asm volatile("bar.sync %0, 128;\n" ::"r"(3 + tile) : "memory");  // fac is complete
     float m = -INFINITY, l = 0.0f, vref = 0x1p-126f;
-    if (any) soften<D>(a, w, tile, tmem, fac, sm, m, l, vref);
+    if (any) soften<D>(a, w, tile, tmem, fac, spw, sm, m, l, vref);
     const int tok = row / a.g, toks = min(w.tq, w.toks - tile * w.tq);
     const bool valid = tok < toks;
     const uint32_t t_o = tmem + ((uint32_t)(row & 96) << 16) + 256 + tile * D;
@@ -895,7 +947,7 @@ cudaError_t launch_d(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64_
   const int heads = units * a.Hkv;
   const cudaError_t e =
       launch_pdl(k_attn_prompt<D>, dim3(heads * splits), dim3(kPThreads), pr_smem_bytes<D>(), s,
-                 pdl, m.k, m.v, a, q, q_stride, out, out_stride, sp, units, splits);
+                 pdl, m.k, m.v64, a, q, q_stride, out, out_stride, sp, units, splits);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_pdl(k_prompt_merge<D>, dim3(heads, Pr<D>::kTiles * 16), dim3(256), 0, s, true, sp,
                     a.g, splits, out, out_stride);
