@@ -102,6 +102,64 @@ __device__ __forceinline__ uint64_t swz_desc(uint32_t saddr, bool wide, uint32_t
          ((uint64_t)(wide ? 2 : 4) << 61);
 }
 
+// MMAs and commits issued by the lane whose `leader` is set, of a warp that runs them in
+// uniform control flow.  Descriptors are taken apart into the changing low word (start
+// address and the offset to the next M or N) and the constant high one, and the leader is
+// found once: an MMA that looks up its lane and builds its descriptors in 64 bits takes
+// the issuing warp about 75 cycles, more than the product takes the tensor cores.
+struct Desc {
+  uint32_t lo, hi;
+};
+
+__device__ __forceinline__ Desc desc_of(uint32_t saddr, bool wide, uint32_t next_m = 16) {
+  const uint64_t d = swz_desc(saddr, wide, next_m);
+  return Desc{(uint32_t)d, (uint32_t)(d >> 32)};
+}
+
+// The same operand `bytes` further on.
+__device__ __forceinline__ Desc operator+(Desc d, uint32_t bytes) {
+  return Desc{d.lo + (bytes >> 4), d.hi};
+}
+
+template <bool kF8>
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, Desc b, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t leader) {
+  if constexpr (kF8)
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+        " mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+        " mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+// A in tensor memory, fp16.
+__device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, Desc b, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 e, %6, 0;\n"
+      " mov.b64 y, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
 // Instruction descriptor bits beside idesc_f8: A stored M-major, B of type e5m2.
 constexpr uint32_t kIdescAMajorM = 1u << 15;
 constexpr uint32_t kIdescBE5m2 = 1u << 10;

@@ -5,31 +5,33 @@
 //   S = Q K^T,  P = 2^(scale S - m),  O += P V,  out = O / sum P
 //
 // in one pass over the keys with a running reference m and sum for each row.  Bound
-// by the tensor cores and, close behind, by the exponentials.  A CTA holds 256 rows
-// (128 at head_dim 256): row tiles of 128, the g query heads of a key head times
-// 128/g tokens.
+// by the tensor cores and the shared memory that feeds them.  A CTA holds 256 rows
+// (128 at head_dim 256): row tiles of 128, the g query heads of a key head times 128/g
+// tokens, and takes the keys 64 at a time.
 //
 // - S: kind::f8f6f4 on the keys' codes as they are stored; a query of 8 significant
 //   bits is two e4m3 values, Qhi + Qlo, multiplied in two passes at twice the
 //   16-bit rate: the same time as one 16-bit product, without converting K.
 // - P V: kind::f16; four warps widen V's codes to fp16 once for all the CTA's rows, P
-//   goes through shared memory (tensor memory at head_dim 256) as fp16.
-// - Two row tiles take turns: while the softmax warps of one work, the tensor cores
-//   have the other's products.
+//   goes to tensor memory as fp16 over the scores it came from.  (P through shared
+//   memory would free the scores' place sooner, but the operands' traffic, 400 KB for
+//   256 rows x 128 keys, then takes longer than the products.)
+// - A row tile has two score buffers of 64 keys: while its softmax warps work on one, the
+//   tensor cores fill the other, so that neither waits for the other's round trip.  (One
+//   buffer of 128 keys left the tensor cores half idle: 1019 us at 16384 rows.)
 //
-// Warps: 0-3 and 4-7 softmax of the two row tiles (a thread per row; at head_dim 256
-// of the two score buffers' one tile: 0-3 alone), 8-11 widen V, 12 issues MMAs,
-// 13 copies by TMA.
+// Warps: 0-3 and 4-7 softmax of the two row tiles (a thread per row), 8-11 widen V, 12
+// and 13 issue a row tile's MMAs each, 14 copies by TMA.
 #include "attn_tc.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kPThreads = 448;
-constexpr int kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kPThreads = 480;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 14;
 constexpr int kKeys = 128;          // keys of a tile
-constexpr int kChunk = 64;          // keys of a widened piece of V
+constexpr int kChunk = 64;          // keys of a step: a score buffer, a piece of V
 // Weights as p x 2^10 in fp16, p against a reference that may lag the row's maximum
 // by kLag powers of two: sums are scaled again only when a score outgrows that.
 constexpr float kShiftLog = 10.0f;
@@ -38,22 +40,17 @@ constexpr float kLag = 5.0f;
 template <int D>
 struct Pr {
   static constexpr int kTiles = D == 256 ? 1 : 2;      // row tiles of a CTA
-  // Where the weights go: with two row tiles to shared memory, so that a row tile's one
-  // score buffer is free for the next tile's scores once they have been read; with one
-  // row tile and two score buffers to tensor memory, over the scores they came from.
-  static constexpr bool kPSmem = kTiles == 2;
   static constexpr bool kWide = D >= 128;
   static constexpr int kRowBytes = kWide ? 128 : 64;
   static constexpr int kPanels = D / kRowBytes;
   static constexpr int kPanelBytes = kKeys * kRowBytes;
   static constexpr int kTileBytes = kKeys * D;         // keys of a tile, as stored
   static constexpr int kQBytes = 128 * D;              // one part of a row tile's queries
-  static constexpr int kPBytes = kPSmem ? 128 * kKeys * 2 : 0;  // a row tile's weights
-  static constexpr int kKStages = D == 64 ? 3 : 2;
-  static constexpr int kVStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // pieces of V, as stored
+  static constexpr int kKStages = D == 256 ? 2 : 3;
+  static constexpr int kVStages = D == 256 ? 2 : 4;    // pieces of V, as stored
   static constexpr int kVPanelBytes = kChunk * kRowBytes;
   static constexpr int kVBytes = kChunk * D;
-  static constexpr int kCStages = D == 64 ? 4 : 2;     // pieces of V, widened
+  static constexpr int kCStages = D == 256 ? 2 : 4;    // pieces of V, widened
   static constexpr int kCBytes = kChunk * D * 2;
   // tiles whose scales are kept: the softmax warps read a tile's when the TMA warp writes
   // those of the fourth behind it (two stages of keys) or the fifth (three) at the latest
@@ -77,7 +74,7 @@ struct PrSmem {
   uint32_t poison[kMeta][4];     // keys of a tile that have a NaN value
   uint64_t k_full[3], k_empty[3], v_full[4], v_empty[4], c_full[4], c_empty[4];
   uint64_t meta_full[kMeta], poison_full[kMeta];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], s_full[4], p_full[4], pv_done[4];  // [row tile][buffer]
   uint32_t tmem;
   int abort;
 };
@@ -85,7 +82,7 @@ struct PrSmem {
 template <int D>
 constexpr size_t pr_smem_bytes() {
   using C = Pr<D>;
-  return 1024 + (size_t)C::kTiles * (2 * C::kQBytes + C::kPBytes) +
+  return 1024 + (size_t)C::kTiles * 2 * C::kQBytes +
          (size_t)C::kKStages * C::kTileBytes + (size_t)C::kVStages * C::kVBytes +
          (size_t)C::kCStages * C::kCBytes + sizeof(PrSmem<D>);
 }
@@ -100,18 +97,6 @@ __device__ __forceinline__ int swz(int row, int b) {
   const int col = b >> 4;
   return kWide ? row * 128 + ((col ^ (row & 7)) << 4) + (b & 15)
                : row * 64 + ((col ^ ((row >> 1) & 3)) << 4) + (b & 15);
-}
-
-// D[tmem] (+)= A[tmem, fp16] * B[smem, fp16]: issued by lane 0 of a warp that runs
-// in uniform control flow.
-__device__ __forceinline__ void mma_ts_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .u32 ln;\n setp.ne.b32 p, %4, 0;\n"
-      " mov.u32 ln, %%laneid;\n setp.eq.u32 e, ln, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
@@ -148,12 +133,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// D[tmem] (+)= A[smem, fp16] * B[smem, fp16], as above.
-__device__ __forceinline__ void mma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  tc::mma_warp<false>(d, a, b, idesc, accumulate);
 }
 
 struct Ring {
@@ -431,232 +410,154 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
   }
 }
 
-// ---- the MMA warp ----------------------------------------------------------------
-// Score buffer of (tile kt, row tile m): two row tiles have one each; one row tile
-// alternates between the two.
+// ---- the MMA warps: one for each row tile ---------------------------------------
+// Step j is 64 keys; its scores go to the row tile's buffer j & 1.
 template <int D>
-__device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, uint32_t sq, uint32_t sk,
-                                      uint32_t sc, uint32_t sp, uint32_t tmem, PrSmem<D>& sm) {
+__device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, int m, uint32_t sq,
+                                      uint32_t sk, uint32_t sc, uint32_t tmem, PrSmem<D>& sm) {
   using C = Pr<D>;
-  constexpr uint32_t id_s = tc::idesc_f8(128, kKeys);
+  constexpr uint32_t id_s = tc::idesc_f8(128, kChunk);
   constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                             ((uint32_t)(128 >> 4) << 24);  // fp16, B stored N-major
   int* abort = &sm.abort;
-  const int tiles = w.tiles;
-  const int n = w.t1 - w.t0;
-  Ring rk, rc;
-  uint32_t p_phase[2] = {0, 0};
-  [[maybe_unused]] uint32_t pv_phase[2] = {0, 0};
-  for (int m = 0; m < tiles; ++m) wait(&sm.q_full[m], 0, abort, a.status);
+  const uint32_t leader = (threadIdx.x & 31) == 0;
+  const int n = 2 * (w.t1 - w.t0);
+  const uint32_t t_s = tmem + m * 128, t_o = tmem + 256 + m * D;
+  const tc::Desc dq = tc::desc_of(sq + 2 * m * C::kQBytes, C::kWide);
+  const tc::Desc dk = tc::desc_of(sk, C::kWide);
+  const tc::Desc dv = tc::desc_of(sc, true, kChunk * 128);
+  Ring rc, rk;
+  wait(&sm.q_full[m], 0, abort, a.status);
 
-  const auto scores = [&](int m, int buf) {  // of the keys in stage rk.i
+  const auto scores = [&](int j) {
+    if ((j & 1) == 0) wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
+    // the buffer's weights of two steps ago have been multiplied
+    if (j >= 2) wait(&sm.pv_done[2 * m + (j & 1)], ((j >> 1) - 1) & 1, abort, a.status);
+    tc::fence_after_sync();
+    const tc::Desc k = dk + (rk.i * C::kTileBytes + (j & 1) * kChunk * C::kRowBytes);
+    const uint32_t to = t_s + (j & 1) * kChunk;
 #pragma unroll
     for (int part = 0; part < 2; ++part)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int panel = 32 * i / C::kRowBytes, b = 32 * i % C::kRowBytes;
-        tc::mma_warp<true>(
-            tmem + buf * 128,
-            tc::swz_desc(sq + (2 * m + part) * C::kQBytes + panel * 128 * C::kRowBytes + b,
-                         C::kWide),
-            tc::swz_desc(sk + rk.i * C::kTileBytes + panel * C::kPanelBytes + b, C::kWide), id_s,
-            part > 0 || i > 0);
+        tc::mma_ss<true>(to, dq + (part * C::kQBytes + panel * 128 * C::kRowBytes + b),
+                         k + (panel * C::kPanelBytes + b), id_s, part > 0 || i > 0, leader);
       }
-    tc::commit_warp(&sm.s_full[buf]);
-  };
-  const auto values = [&](int m, int buf, bool first, const Ring& from) {
-    Ring r = from;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (m == 0) {
-        wait(&sm.c_full[r.i], r.phase, abort, a.status);
-        tc::fence_after_sync();
-      }
-#pragma unroll
-      for (int i = 0; i < kChunk / 16; ++i) {
-        // 16 keys: two groups of eight rows of 1024 bytes; blocks of 64 values behind
-        const uint64_t b = tc::swz_desc(sc + r.i * C::kCBytes + i * 2048, true, kChunk * 128);
-        const uint32_t acc = !first || c > 0 || i > 0;
-        if constexpr (C::kPSmem)
-          mma_ss_warp(tmem + 256 + m * D,
-                      tc::swz_desc(sp + m * C::kPBytes + c * (128 * 128) + i * 32, true), b, id_o,
-                      acc);
-        else
-          mma_ts_warp(tmem + 256 + m * D, tmem + buf * 128 + c * 32 + i * 8, b, id_o, acc);
-      }
-      if (m == tiles - 1) tc::commit_warp(&sm.c_empty[r.i]);
-      r.next(C::kCStages);
+    tc::commit_by(&sm.s_full[2 * m + (j & 1)], leader);
+    if (j & 1) {
+      tc::commit_by(&sm.k_empty[rk.i], leader);
+      rk.next(C::kKStages);
     }
-    tc::commit_warp(&sm.pv_done[buf]);
-    return r;
   };
 
-  if constexpr (C::kTiles == 2) {
-    // S(0, t0) S(1, t0) | then for every tile and row tile: its next scores, its values
-    wait(&sm.k_full[0], 0, abort, a.status);
+  scores(0);
+  scores(1);
+  for (int j = 0; j < n; ++j) {
+    wait(&sm.c_full[rc.i], rc.phase, abort, a.status);
+    wait(&sm.p_full[2 * m + (j & 1)], (j >> 1) & 1, abort, a.status);
     tc::fence_after_sync();
-    for (int m = 0; m < tiles; ++m) scores(m, m);
-    tc::commit_warp(&sm.k_empty[0]);
-    rk.next(C::kKStages);
-    for (int i = 0; i < n; ++i) {
-      Ring after = rc;
-      for (int m = 0; m < tiles; ++m) {
-        wait(&sm.p_full[m], p_phase[m], abort, a.status);
-        p_phase[m] ^= 1;
-        if (i + 1 < n) {
-          if (m == 0) wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
-          tc::fence_after_sync();
-          scores(m, m);
-          if (m == tiles - 1) {
-            tc::commit_warp(&sm.k_empty[rk.i]);
-            rk.next(C::kKStages);
-          }
-        }
-        tc::fence_after_sync();
-        after = values(m, m, i == 0, rc);
-      }
-      rc = after;
-    }
-  } else {
-    // one row tile, two score buffers: the next tile's scores before this tile's values
-    const auto next_scores = [&](int i) {
-      wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
-      if (i >= 2) {
-        wait(&sm.pv_done[i & 1], pv_phase[i & 1], abort, a.status);
-        pv_phase[i & 1] ^= 1;
-      }
-      tc::fence_after_sync();
-      scores(0, i & 1);
-      tc::commit_warp(&sm.k_empty[rk.i]);
-      rk.next(C::kKStages);
-    };
-    next_scores(0);
-    for (int i = 0; i < n; ++i) {
-      if (i + 1 < n) next_scores(i + 1);
-      wait(&sm.p_full[i & 1], p_phase[i & 1], abort, a.status);
-      p_phase[i & 1] ^= 1;
-      tc::fence_after_sync();
-      rc = values(0, i & 1, i == 0, rc);
-    }
+    const tc::Desc v = dv + rc.i * C::kCBytes;
+#pragma unroll
+    for (int i = 0; i < kChunk / 16; ++i)
+      // 16 keys: two groups of eight rows of 1024 bytes; blocks of 64 values behind
+      tc::mma_ts_f16(t_o, t_s + (j & 1) * kChunk + i * 8, v + i * 2048, id_o, j > 0 || i > 0,
+                     leader);
+    tc::commit_by(&sm.pv_done[2 * m + (j & 1)], leader);
+    tc::commit_by(&sm.c_empty[rc.i], leader);
+    rc.next(C::kCStages);
+    if (j + 2 < n) scores(j + 2);
   }
 }
 
 // ---- the softmax warps --------------------------------------------------------------
-// One row of one key tile: the largest score over the reference, or the weights.
+// What a row sees of 64 keys.
 struct RowMask {
-  int low, high;        // columns [low, high] are seen
-  uint32_t absent;      // 16-key groups without a page
-  uint32_t poison[4];   // columns with a NaN value
+  int low, high;        // columns [low, high]
+  uint32_t absent;      // but for 16-key groups without a page
+  uint32_t poison[2];   // columns with a NaN value
 };
 
-// The largest score of a row over a tile, in log2 units, from tensor memory; the
-// next columns are on their way while 32 are looked at.
+// The largest of a row's 64 scores, in log2 units.
 template <bool kEdge>
-__device__ __forceinline__ float tile_peak(uint32_t t_s, const Meta& me, float fac,
-                                           const RowMask& mk) {
+__device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float (&f)[4],
+                                        const RowMask& mk) {
   float peak = -INFINITY;
-  uint32_t v[2][32];
-  tc::tmem_ld_async(t_s, v[0]);
-  float2 ks = *reinterpret_cast<const float2*>(me.ks);
 #pragma unroll
-  for (int b = 0; b < kKeys / 32; ++b) {
-    const float f[2] = {fac * ks.x, fac * ks.y};
-    tc::wait_ld();
-    if (b + 1 < kKeys / 32) {
-      tc::tmem_ld_async(t_s + 32 * (b + 1), v[(b + 1) & 1]);
-      ks = *reinterpret_cast<const float2*>(me.ks + 2 * (b + 1));
+  for (int g = 0; g < 4; ++g) {
+    float x[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      x[c] = __uint_as_float(v[g >> 1][16 * (g & 1) + c]);
+      if (kEdge && (16 * g + c < mk.low || 16 * g + c > mk.high)) x[c] = -INFINITY;
     }
+    float y[5];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      float x[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        x[c] = __uint_as_float(v[b & 1][16 * g + c]);
-        const int col = 32 * b + 16 * g + c;
-        if (kEdge && (col < mk.low || col > mk.high)) x[c] = -INFINITY;
-      }
-      float y[5];
-#pragma unroll
-      for (int c = 0; c < 5; ++c) y[c] = max3(x[3 * c], x[3 * c + 1], x[3 * c + 2]);
-      const float m = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15]), -INFINITY);
-      if (kEdge && (((mk.absent >> (2 * b + g)) & 1) || m == -INFINITY)) continue;
-      peak = fmaxf(peak, m * f[g]);
-    }
+    for (int c = 0; c < 5; ++c) y[c] = max3(x[3 * c], x[3 * c + 1], x[3 * c + 2]);
+    const float m = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15]));
+    if (kEdge && (((mk.absent >> g) & 1) || m == -INFINITY)) continue;
+    peak = fmaxf(peak, m * f[g]);
   }
   return peak;
 }
 
-// Weights of a row over a tile, 2^(s f + base) by groups of 16 keys, as fp16: to
-// shared memory (p_row: the row's 128 bytes of each 64 keys, its 16-byte columns swizzled
-// by the row), or over the scores that have been read.  Returns their sum freed of the
-// pages' value scales.
-template <bool kEdge, bool kPSmem>
-__device__ __forceinline__ float weigh(uint32_t t_s, uint8_t* p_row, const Meta& me, float fac,
-                                       float log_up, float down, float m_base,
-                                       const RowMask& mk) {
+// Weights of a row's 64 keys, 2^(s f + base) by groups of 16, as fp16 to tensor
+// memory; returns their sum freed of the pages' value scales.
+template <bool kEdge>
+__device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_p,
+                                         const float (&f)[4], const Meta& me, int group0,
+                                         float log_up, float down, float m_base,
+                                         const RowMask& mk) {
   float sum = 0.0f;
-  uint32_t v[2][16], p[16];
-  tc::tmem_ld_async(t_s, v[0]);
-  float ks = me.ks[0], lv = me.log_vs[0], iv = me.inv_vs[0];
+  const float4 lv = *reinterpret_cast<const float4*>(me.log_vs + group0);
+  const float4 iv = *reinterpret_cast<const float4*>(me.inv_vs + group0);
+  const float log_vs[4] = {lv.x, lv.y, lv.z, lv.w}, inv_vs[4] = {iv.x, iv.y, iv.z, iv.w};
 #pragma unroll
-  for (int g = 0; g < kKeys / 16; ++g) {
-    const float f = fac * ks;
-    // a page below 2^-70 of the largest adds no value that counts
-    const float base = fmaxf(lv + log_up, -60.0f) - m_base;
-    const float inv = fminf(iv * down, 0x1p60f);
-    tc::wait_ld();
-    if (g + 1 < kKeys / 16) {
-      tc::tmem_ld_async(t_s + 16 * (g + 1), v[(g + 1) & 1]);
-      ks = me.ks[g + 1];
-      lv = me.log_vs[g + 1];
-      iv = me.inv_vs[g + 1];
-    }
-    const uint32_t(&s)[16] = v[g & 1];
-    const float2 ff = make_float2(f, f), bb = make_float2(base, base);
-    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  for (int h = 0; h < 2; ++h) {
+    uint32_t p[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, bb);
-      x.x = exp2_approx(x.x);
-      x.y = exp2_approx(x.y);
-      if constexpr (kEdge) {
-        const int c = 16 * g + 2 * i;
-        const bool there = !((mk.absent >> g) & 1);
-        const uint32_t bad = mk.poison[g >> 1] >> (16 * (g & 1) + 2 * i);
-        if (bad & 1) x.x = __int_as_float(0x7FFFFFFF);
-        if (bad & 2) x.y = __int_as_float(0x7FFFFFFF);
-        if (!there || c < mk.low || c > mk.high) x.x = 0.0f;
-        if (!there || c + 1 < mk.low || c + 1 > mk.high) x.y = 0.0f;
+    for (int q = 0; q < 2; ++q) {
+      const int g = 2 * h + q;
+      // a page below 2^-70 of the largest adds no value that counts
+      const float base = fmaxf(log_vs[g] + log_up, -60.0f) - m_base;
+      const float inv = fminf(inv_vs[g] * down, 0x1p60f);
+      const float2 ff = make_float2(f[g], f[g]), bb = make_float2(base, base);
+      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 x = fma2(make_float2(__uint_as_float(v[h][16 * q + 2 * i]),
+                                    __uint_as_float(v[h][16 * q + 2 * i + 1])),
+                        ff, bb);
+        x.x = exp2_approx(x.x);
+        x.y = exp2_approx(x.y);
+        if constexpr (kEdge) {
+          const int c = 16 * g + 2 * i;
+          const bool there = !((mk.absent >> g) & 1);
+          const uint32_t bad = mk.poison[h] >> (16 * q + 2 * i);
+          if (bad & 1) x.x = __int_as_float(0x7FFFFFFF);
+          if (bad & 2) x.y = __int_as_float(0x7FFFFFFF);
+          if (!there || c < mk.low || c > mk.high) x.x = 0.0f;
+          if (!there || c + 1 < mk.low || c + 1 > mk.high) x.y = 0.0f;
+        }
+        acc[i & 1] = add2(acc[i & 1], x);
+        p[8 * q + i] = f16x2_of(x.x, x.y);
       }
-      acc[i & 1] = add2(acc[i & 1], x);
-      p[8 * (g & 1) + i] = f16x2_of(x.x, x.y);
+      const float2 t = add2(acc[0], acc[1]);
+      sum = fmaf(t.x + t.y, inv, sum);
     }
-    const float2 t = add2(acc[0], acc[1]);
-    sum = fmaf(t.x + t.y, inv, sum);
-    if constexpr (kPSmem) {
-      // columns 2 (g % 4), 2 (g % 4) + 1 of keys 64 (g / 4) on
-      const int x = (threadIdx.x & 7) << 4, b = (g & 1) * 8;
-      uint8_t* to = p_row + (g >> 2) * (128 * 128);
-      *reinterpret_cast<uint4*>(to + (((2 * (g & 3)) << 4) ^ x)) =
-          make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]);
-      *reinterpret_cast<uint4*>(to + (((2 * (g & 3) + 1) << 4) ^ x)) =
-          make_uint4(p[b + 4], p[b + 5], p[b + 6], p[b + 7]);
-    } else if (g & 1) {
-      tc::tmem_st(t_s + 8 * (g - 1), p);
-    }
+    tc::tmem_st(t_p + 16 * h, p);
   }
   return sum;
 }
 
 template <int D>
 __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int tile, uint32_t tmem,
-                                       const float* fac_of, uint8_t* sp, PrSmem<D>& sm, float& m_out,
+                                       const float* fac_of, PrSmem<D>& sm, float& m_out,
                                        float& l_out, float& vref_out) {
   using C = Pr<D>;
   const int row = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(row & 96) << 16;
   const uint32_t t_o = tmem + lanes + 256 + tile * D;
-  uint8_t* p_row = sp + (size_t)tile * C::kPBytes + row * 128;
   int* abort = &sm.abort;
   const int first = w.v.first + w.tok0 + tile * w.tq;        // earliest row of the tile
   const int toks = min(w.tq, w.toks - tile * w.tq);
@@ -666,32 +567,35 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
   const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
   const float fac = fac_of[row];
   float m = -INFINITY, l = 0.0f, vref = 0x1p-126f, log_up = 0.0f, down = 0.0f;
-  uint32_t s_phase[2] = {0, 0}, pv_phase[2] = {0, 0};
-  const int n = w.t1 - w.t0;
-  for (int i = 0; i < n; ++i) {
-    const int kt = w.t0 + i, slot = i % C::kMeta;
-    const int buf = C::kTiles == 2 ? tile : (i & 1);
-    const int last_buf = C::kTiles == 2 ? tile : (buf ^ 1);
-    wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
+  const int n = 2 * (w.t1 - w.t0);
+  for (int j = 0; j < n; ++j) {
+    const int i = j >> 1, kt = w.t0 + i, slot = i % C::kMeta, buf = 2 * tile + (j & 1);
+    const int group0 = (j & 1) * 4;
+    if ((j & 1) == 0) wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
     const Meta& me = sm.meta[slot];
     const float top = me.top;
+    const float4 ks = *reinterpret_cast<const float4*>(me.ks + group0);
     const bool edge = edge_tile(a, w, kt, pos0, pos1) || me.absent != 0;
     RowMask mk;
     if (edge) {
-      wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
-      mk.high = min(pos - kt * kKeys, kKeys);
-      mk.low = a.window ? pos - a.window + 1 - kt * kKeys : -1;
-      mk.absent = me.absent;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mk.poison[k] = sm.poison[slot][k];
+      if ((j & 1) == 0) wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
+      const int key0 = kt * kKeys + (j & 1) * kChunk;
+      mk.high = min(pos - key0, kKeys);
+      mk.low = a.window ? pos - a.window + 1 - key0 : -1;
+      mk.absent = me.absent >> group0;
+      mk.poison[0] = sm.poison[slot][group0 / 2];
+      mk.poison[1] = sm.poison[slot][group0 / 2 + 1];
     }
-    wait(&sm.s_full[buf], s_phase[buf], abort, a.status);
-    s_phase[buf] ^= 1;
+    const float f[4] = {fac * ks.x, fac * ks.y, fac * ks.z, fac * ks.w};
+    wait(&sm.s_full[buf], i & 1, abort, a.status);
     tc::fence_after_sync();
     __syncwarp();
-    const uint32_t t_s = tmem + lanes + buf * 128;
-    const float peak =
-        edge ? tile_peak<true>(t_s, me, fac, mk) : tile_peak<false>(t_s, me, fac, mk);
+    const uint32_t t_s = tmem + lanes + tile * 128 + (j & 1) * kChunk;
+    uint32_t v[2][32];
+    tc::tmem_ld_async(t_s, v[0]);
+    tc::tmem_ld_async(t_s + 32, v[1]);
+    tc::wait_ld();
+    const float peak = edge ? peak64<true>(v, f, mk) : peak64<false>(v, f, mk);
     if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
       // new references for the warp's rows, and their sums brought to them
       const float m_new = fmaxf(m, peak);
@@ -702,38 +606,30 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       vref = fmaxf(vref, top);
       log_up = kShiftLog - __log2f(vref);
       down = vref * 0x1p-10f;
-      if (i > 0) {
-        wait(&sm.pv_done[last_buf], pv_phase[last_buf] ^ 1, abort, a.status);
+      if (j > 0) {
+        wait(&sm.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, abort, a.status);
         tc::fence_after_sync();
         __syncwarp();
-        const float f = alpha * vf;
+        const float g = alpha * vf;
 #pragma unroll 1
-        for (int b = 0; b < D; b += 32) {
-          uint32_t v[32];
-          tc::tmem_ld_async(t_o + b, v);
+        for (int b = 0; b < D; b += 16) {
+          uint32_t o[16];
+          tc::tmem_ld_async(t_o + b, o);
           tc::wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-          tc::tmem_st(t_o + b, v);
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
+          tc::tmem_st(t_o + b, o);
         }
-        tc::wait_st();
       }
     }
     const float m_base = m == -INFINITY ? 0.0f : m;
-    // (shared memory: the last tile's weights have been multiplied)
-    if (C::kPSmem && i > 0) wait(&sm.pv_done[last_buf], pv_phase[last_buf] ^ 1, abort, a.status);
-    l += edge ? weigh<true, C::kPSmem>(t_s, p_row, me, fac, log_up, down, m_base, mk)
-              : weigh<false, C::kPSmem>(t_s, p_row, me, fac, log_up, down, m_base, mk);
-    if constexpr (C::kPSmem)
-      tc::fence_async_smem();
-    else
-      tc::wait_st();
+    l += edge ? weigh64<true>(v, t_s, f, me, group0, log_up, down, m_base, mk)
+              : weigh64<false>(v, t_s, f, me, group0, log_up, down, m_base, mk);
+    tc::wait_st();
     tc::fence_before_sync();
     tc::mbar_arrive(&sm.p_full[buf]);
-    pv_phase[buf] ^= 1;
   }
-  const int last = C::kTiles == 2 ? tile : ((n - 1) & 1);
-  wait(&sm.pv_done[last], pv_phase[last] ^ 1, abort, a.status);
+  wait(&sm.pv_done[2 * tile + ((n - 1) & 1)], ((n - 1) >> 1) & 1, abort, a.status);
   tc::fence_after_sync();
   __syncwarp();
   m_out = m;
@@ -749,8 +645,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   using C = Pr<D>;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* sq = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* spw = sq + (size_t)C::kTiles * 2 * C::kQBytes;   // weights
-  uint8_t* sk = spw + (size_t)C::kTiles * C::kPBytes;
+  uint8_t* sk = sq + (size_t)C::kTiles * 2 * C::kQBytes;
   uint8_t* sv = sk + (size_t)C::kKStages * C::kTileBytes;
   uint8_t* sc = sv + (size_t)C::kVStages * C::kVBytes;
   PrSmem<D>& sm = *reinterpret_cast<PrSmem<D>*>(sc + (size_t)C::kCStages * C::kCBytes);
@@ -789,19 +684,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
       tc::mbar_init(&sm.k_full[i], 1);
-      tc::mbar_init(&sm.k_empty[i], 1);
+      tc::mbar_init(&sm.k_empty[i], w.tiles);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.q_full[i], 128);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.q_full[i], 128);
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
       tc::mbar_init(&sm.p_full[i], 128);
       tc::mbar_init(&sm.pv_done[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm.v_full[i], 1);
       tc::mbar_init(&sm.v_empty[i], 4);
       tc::mbar_init(&sm.c_full[i], 4);
-      tc::mbar_init(&sm.c_empty[i], 1);
+      tc::mbar_init(&sm.c_empty[i], w.tiles);
     }
     for (int i = 0; i < C::kMeta; ++i) {
       tc::mbar_init(&sm.meta_full[i], 1);
@@ -828,9 +721,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const bool any = w.t0 < w.t1;  // (a share of fewer tiles than shares may be empty)
   if (warp == kTmaWarp) {
     if (any) copy_tiles<D>(a, w, &kmap, &vmap, sk, sv, sm);
-  } else if (warp == kMmaWarp) {
-    if (any) issue<D>(a, w, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc),
-                      tc::smem_u32(spw), tmem, sm);
+  } else if (warp >= kMmaWarp) {
+    if (any && warp - kMmaWarp < w.tiles)
+      issue<D>(a, w, warp - kMmaWarp, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc), tmem,
+               sm);
   } else if (warp >= kConvWarp && warp < kMmaWarp) {
     if (any) widen_tiles<D>(a, w, sv, sc, sm);
   } else if (warp < 4 * C::kTiles && warp / 4 < w.tiles) {
@@ -841,7 +735,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc::mbar_arrive(&sm.q_full[tile]);
     asm volatile("bar.sync %0, 128;\n" ::"r"(3 + tile) : "memory");  // fac is complete
     float m = -INFINITY, l = 0.0f, vref = 0x1p-126f;
-    if (any) soften<D>(a, w, tile, tmem, fac, spw, sm, m, l, vref);
+    if (any) soften<D>(a, w, tile, tmem, fac, sm, m, l, vref);
     const int tok = row / a.g, toks = min(w.tq, w.toks - tile * w.tq);
     const bool valid = tok < toks;
     const uint32_t t_o = tmem + ((uint32_t)(row & 96) << 16) + 256 + tile * D;
