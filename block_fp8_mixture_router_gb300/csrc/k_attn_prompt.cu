@@ -7,7 +7,7 @@
 // in one pass over the keys with a running reference m and sum for each row.  Bound
 // by the tensor cores and the shared memory that feeds them.  A CTA holds 256 rows
 // (128 at head_dim 256): row tiles of 128, the g query heads of a key head times 128/g
-// tokens, and takes the keys 64 at a time.
+// tokens, and takes the keys 64 at a time (128 at head_dim 256).
 //
 // - S: kind::f8f6f4 on the keys' codes as they are stored; a query of 8 significant
 //   bits is two e4m3 values, Qhi + Qlo, multiplied in two passes at twice the
@@ -16,9 +16,16 @@
 //   goes to tensor memory as fp16 over the scores it came from.  (P through shared
 //   memory would free the scores' place sooner, but the operands' traffic, 400 KB for
 //   256 rows x 128 keys, then takes longer than the products.)
-// - A row tile has two score buffers of 64 keys: while its softmax warps work on one, the
-//   tensor cores fill the other, so that neither waits for the other's round trip.  (One
-//   buffer of 128 keys left the tensor cores half idle: 1019 us at 16384 rows.)
+// - A row tile has two score buffers: while its softmax warps work on one, the tensor
+//   cores fill the other, so that neither waits for the other's round trip.  Two row
+//   tiles' buffers have room for 64 keys each, although an MMA with N = 64 takes as long
+//   as one with N = 128.
+//
+// Slower at 16384 rows, 16 heads of 128 (969 us as it is): one buffer of 128 keys per row
+// tile, 1048 us (the row tiles fall into step, and both work while the tensor cores
+// idle); the same with the row tiles' softmax warps taking turns, 1161 us (reads of
+// tensor memory take twice as long beside running MMAs); a row's scores held in 192
+// registers, 1070 us; one warp for all MMAs, 1202 us.
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles (a thread per row), 8-11 widen V, 12
 // and 13 issue a row tile's MMAs each, 14 copies by TMA.
@@ -31,7 +38,7 @@ namespace {
 constexpr int kPThreads = 480;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 14;
 constexpr int kKeys = 128;          // keys of a tile
-constexpr int kChunk = 64;          // keys of a step: a score buffer, a piece of V
+constexpr int kChunk = 64;          // keys of a piece of V
 // Weights as p x 2^10 in fp16, p against a reference that may lag the row's maximum
 // by kLag powers of two: sums are scaled again only when a score outgrows that.
 constexpr float kShiftLog = 10.0f;
@@ -40,6 +47,8 @@ constexpr float kLag = 5.0f;
 template <int D>
 struct Pr {
   static constexpr int kTiles = D == 256 ? 1 : 2;      // row tiles of a CTA
+  static constexpr int kStep = D == 256 ? 128 : 64;    // keys of a score buffer
+  static constexpr int kPer = kKeys / kStep;           // steps of a key tile
   static constexpr bool kWide = D >= 128;
   static constexpr int kRowBytes = kWide ? 128 : 64;
   static constexpr int kPanels = D / kRowBytes;
@@ -411,17 +420,17 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
 }
 
 // ---- the MMA warps: one for each row tile ---------------------------------------
-// Step j is 64 keys; its scores go to the row tile's buffer j & 1.
+// Step j is kStep keys; its scores go to the row tile's buffer j & 1.
 template <int D>
 __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, int m, uint32_t sq,
                                       uint32_t sk, uint32_t sc, uint32_t tmem, PrSmem<D>& sm) {
   using C = Pr<D>;
-  constexpr uint32_t id_s = tc::idesc_f8(128, kChunk);
+  constexpr uint32_t id_s = tc::idesc_f8(128, C::kStep);
   constexpr uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                             ((uint32_t)(128 >> 4) << 24);  // fp16, B stored N-major
   int* abort = &sm.abort;
   const uint32_t leader = (threadIdx.x & 31) == 0;
-  const int n = 2 * (w.t1 - w.t0);
+  const int n = C::kPer * (w.t1 - w.t0);
   const uint32_t t_s = tmem + m * 128, t_o = tmem + 256 + m * D;
   const tc::Desc dq = tc::desc_of(sq + 2 * m * C::kQBytes, C::kWide);
   const tc::Desc dk = tc::desc_of(sk, C::kWide);
@@ -430,12 +439,13 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, int m, u
   wait(&sm.q_full[m], 0, abort, a.status);
 
   const auto scores = [&](int j) {
-    if ((j & 1) == 0) wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
+    const int part_of = j % C::kPer;  // of its key tile
+    if (part_of == 0) wait(&sm.k_full[rk.i], rk.phase, abort, a.status);
     // the buffer's weights of two steps ago have been multiplied
     if (j >= 2) wait(&sm.pv_done[2 * m + (j & 1)], ((j >> 1) - 1) & 1, abort, a.status);
     tc::fence_after_sync();
-    const tc::Desc k = dk + (rk.i * C::kTileBytes + (j & 1) * kChunk * C::kRowBytes);
-    const uint32_t to = t_s + (j & 1) * kChunk;
+    const tc::Desc k = dk + (rk.i * C::kTileBytes + part_of * C::kStep * C::kRowBytes);
+    const uint32_t to = t_s + (j & 1) * C::kStep;
 #pragma unroll
     for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -445,42 +455,45 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, int m, u
                          k + (panel * C::kPanelBytes + b), id_s, part > 0 || i > 0, leader);
       }
     tc::commit_by(&sm.s_full[2 * m + (j & 1)], leader);
-    if (j & 1) {
+    if (part_of == C::kPer - 1) {
       tc::commit_by(&sm.k_empty[rk.i], leader);
       rk.next(C::kKStages);
     }
   };
 
   scores(0);
-  scores(1);
+  if (n > 1) scores(1);
   for (int j = 0; j < n; ++j) {
-    wait(&sm.c_full[rc.i], rc.phase, abort, a.status);
-    wait(&sm.p_full[2 * m + (j & 1)], (j >> 1) & 1, abort, a.status);
-    tc::fence_after_sync();
-    const tc::Desc v = dv + rc.i * C::kCBytes;
 #pragma unroll
-    for (int i = 0; i < kChunk / 16; ++i)
-      // 16 keys: two groups of eight rows of 1024 bytes; blocks of 64 values behind
-      tc::mma_ts_f16(t_o, t_s + (j & 1) * kChunk + i * 8, v + i * 2048, id_o, j > 0 || i > 0,
-                     leader);
+    for (int c = 0; c < C::kStep / kChunk; ++c) {
+      wait(&sm.c_full[rc.i], rc.phase, abort, a.status);
+      if (c == 0) wait(&sm.p_full[2 * m + (j & 1)], (j >> 1) & 1, abort, a.status);
+      tc::fence_after_sync();
+      const tc::Desc v = dv + rc.i * C::kCBytes;
+#pragma unroll
+      for (int i = 0; i < kChunk / 16; ++i)
+        // 16 keys: two groups of eight rows of 1024 bytes; blocks of 64 values behind
+        tc::mma_ts_f16(t_o, t_s + (j & 1) * C::kStep + c * 32 + i * 8, v + i * 2048, id_o,
+                       j > 0 || c > 0 || i > 0, leader);
+      tc::commit_by(&sm.c_empty[rc.i], leader);
+      rc.next(C::kCStages);
+    }
     tc::commit_by(&sm.pv_done[2 * m + (j & 1)], leader);
-    tc::commit_by(&sm.c_empty[rc.i], leader);
-    rc.next(C::kCStages);
     if (j + 2 < n) scores(j + 2);
   }
 }
 
 // ---- the softmax warps --------------------------------------------------------------
-// What a row sees of 64 keys.
+// What a row sees of a step's keys.
 struct RowMask {
   int low, high;        // columns [low, high]
   uint32_t absent;      // but for 16-key groups without a page
-  uint32_t poison[2];   // columns with a NaN value
+  uint32_t poison[4];   // columns with a NaN value
 };
 
-// The largest of a row's 64 scores, in log2 units.
+// The largest of a row's 64 scores (columns col0 on), in log2 units.
 template <bool kEdge>
-__device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float (&f)[4],
+__device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float* f, int col0,
                                         const RowMask& mk) {
   float peak = -INFINITY;
 #pragma unroll
@@ -489,25 +502,25 @@ __device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float 
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       x[c] = __uint_as_float(v[g >> 1][16 * (g & 1) + c]);
-      if (kEdge && (16 * g + c < mk.low || 16 * g + c > mk.high)) x[c] = -INFINITY;
+      if (kEdge && (col0 + 16 * g + c < mk.low || col0 + 16 * g + c > mk.high)) x[c] = -INFINITY;
     }
     float y[5];
 #pragma unroll
     for (int c = 0; c < 5; ++c) y[c] = max3(x[3 * c], x[3 * c + 1], x[3 * c + 2]);
     const float m = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15]));
-    if (kEdge && (((mk.absent >> g) & 1) || m == -INFINITY)) continue;
+    if (kEdge && (((mk.absent >> (col0 / 16 + g)) & 1) || m == -INFINITY)) continue;
     peak = fmaxf(peak, m * f[g]);
   }
   return peak;
 }
 
-// Weights of a row's 64 keys, 2^(s f + base) by groups of 16, as fp16 to tensor
-// memory; returns their sum freed of the pages' value scales.
+// Weights of a row's 64 keys (columns col0 on, 16-key groups group0 on of the tile),
+// 2^(s f + base) by groups of 16, as fp16 to tensor memory; returns their sum freed of
+// the pages' value scales.
 template <bool kEdge>
-__device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_p,
-                                         const float (&f)[4], const Meta& me, int group0,
-                                         float log_up, float down, float m_base,
-                                         const RowMask& mk) {
+__device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_p, const float* f,
+                                         const Meta& me, int group0, int col0, float log_up,
+                                         float down, float m_base, const RowMask& mk) {
   float sum = 0.0f;
   const float4 lv = *reinterpret_cast<const float4*>(me.log_vs + group0);
   const float4 iv = *reinterpret_cast<const float4*>(me.inv_vs + group0);
@@ -531,9 +544,9 @@ __device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_
         x.x = exp2_approx(x.x);
         x.y = exp2_approx(x.y);
         if constexpr (kEdge) {
-          const int c = 16 * g + 2 * i;
-          const bool there = !((mk.absent >> g) & 1);
-          const uint32_t bad = mk.poison[h] >> (16 * q + 2 * i);
+          const int c = col0 + 16 * g + 2 * i;
+          const bool there = !((mk.absent >> (c / 16)) & 1);
+          const uint32_t bad = mk.poison[c / 32] >> (16 * q + 2 * i);
           if (bad & 1) x.x = __int_as_float(0x7FFFFFFF);
           if (bad & 2) x.y = __int_as_float(0x7FFFFFFF);
           if (!there || c < mk.low || c > mk.high) x.x = 0.0f;
@@ -567,35 +580,47 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
   const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
   const float fac = fac_of[row];
   float m = -INFINITY, l = 0.0f, vref = 0x1p-126f, log_up = 0.0f, down = 0.0f;
-  const int n = 2 * (w.t1 - w.t0);
+  const int n = C::kPer * (w.t1 - w.t0);
   for (int j = 0; j < n; ++j) {
-    const int i = j >> 1, kt = w.t0 + i, slot = i % C::kMeta, buf = 2 * tile + (j & 1);
-    const int group0 = (j & 1) * 4;
-    if ((j & 1) == 0) wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
+    const int i = j / C::kPer, kt = w.t0 + i, slot = i % C::kMeta, buf = 2 * tile + (j & 1);
+    const int part = j % C::kPer, group0 = part * (C::kStep / 16);
+    if (part == 0) wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
     const Meta& me = sm.meta[slot];
     const float top = me.top;
-    const float4 ks = *reinterpret_cast<const float4*>(me.ks + group0);
     const bool edge = edge_tile(a, w, kt, pos0, pos1) || me.absent != 0;
     RowMask mk;
     if (edge) {
-      if ((j & 1) == 0) wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
-      const int key0 = kt * kKeys + (j & 1) * kChunk;
+      if (part == 0) wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
+      const int key0 = kt * kKeys + part * C::kStep;
       mk.high = min(pos - key0, kKeys);
       mk.low = a.window ? pos - a.window + 1 - key0 : -1;
       mk.absent = me.absent >> group0;
-      mk.poison[0] = sm.poison[slot][group0 / 2];
-      mk.poison[1] = sm.poison[slot][group0 / 2 + 1];
+#pragma unroll
+      for (int k = 0; k < C::kStep / 32; ++k) mk.poison[k] = sm.poison[slot][group0 / 2 + k];
     }
-    const float f[4] = {fac * ks.x, fac * ks.y, fac * ks.z, fac * ks.w};
-    wait(&sm.s_full[buf], i & 1, abort, a.status);
+    float f[C::kStep / 16];
+#pragma unroll
+    for (int k = 0; k < C::kStep / 16; k += 4) {
+      const float4 ks = *reinterpret_cast<const float4*>(me.ks + group0 + k);
+      f[k] = fac * ks.x, f[k + 1] = fac * ks.y, f[k + 2] = fac * ks.z, f[k + 3] = fac * ks.w;
+    }
+    wait(&sm.s_full[buf], (j >> 1) & 1, abort, a.status);
     tc::fence_after_sync();
     __syncwarp();
-    const uint32_t t_s = tmem + lanes + tile * 128 + (j & 1) * kChunk;
+    const uint32_t t_s = tmem + lanes + tile * 128 + (j & 1) * C::kStep;
     uint32_t v[2][32];
-    tc::tmem_ld_async(t_s, v[0]);
-    tc::tmem_ld_async(t_s + 32, v[1]);
-    tc::wait_ld();
-    const float peak = edge ? peak64<true>(v, f, mk) : peak64<false>(v, f, mk);
+    const auto load = [&](int c) {
+      tc::tmem_ld_async(t_s + c * 64, v[0]);
+      tc::tmem_ld_async(t_s + c * 64 + 32, v[1]);
+      tc::wait_ld();
+    };
+    float peak = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < C::kStep / 64; ++c) {
+      load(c);
+      peak = fmaxf(peak, edge ? peak64<true>(v, f + 4 * c, 64 * c, mk)
+                              : peak64<false>(v, f + 4 * c, 64 * c, mk));
+    }
     if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
       // new references for the warp's rows, and their sums brought to them
       const float m_new = fmaxf(m, peak);
@@ -623,8 +648,14 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       }
     }
     const float m_base = m == -INFINITY ? 0.0f : m;
-    l += edge ? weigh64<true>(v, t_s, f, me, group0, log_up, down, m_base, mk)
-              : weigh64<false>(v, t_s, f, me, group0, log_up, down, m_base, mk);
+#pragma unroll
+    for (int c = 0; c < C::kStep / 64; ++c) {
+      if (C::kStep > 64) load(c);  // (64 scores are still in registers)
+      l += edge ? weigh64<true>(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, 64 * c, log_up,
+                                down, m_base, mk)
+                : weigh64<false>(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, 64 * c, log_up,
+                                 down, m_base, mk);
+    }
     tc::wait_st();
     tc::fence_before_sync();
     tc::mbar_arrive(&sm.p_full[buf]);
