@@ -27,8 +27,9 @@
 // tensor memory take twice as long beside running MMAs); a row's scores held in 192
 // registers, 1070 us; one warp for all MMAs, 1202 us.
 //
-// Warps: 0-3 and 4-7 softmax of the two row tiles (a thread per row), 8-11 widen V, 12
-// and 13 issue a row tile's MMAs each, 14 copies by TMA.
+// Warps: 0-3 and 4-7 softmax of the two row tiles (a thread per row), 8-11 widen V (at
+// head_dim 256, with one row tile, 4-11), 12 and 13 issue a row tile's MMAs each, 14
+// copies by TMA.
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -36,7 +37,7 @@ namespace moe {
 namespace {
 
 constexpr int kPThreads = 480;
-constexpr int kConvWarp = 8, kMmaWarp = 12, kTmaWarp = 14;
+constexpr int kMmaWarp = 12, kTmaWarp = 14;
 constexpr int kKeys = 128;          // keys of a tile
 constexpr int kChunk = 64;          // keys of a piece of V
 // Weights as p x 2^10 in fp16, p against a reference that may lag the row's maximum
@@ -48,6 +49,8 @@ template <int D>
 struct Pr {
   static constexpr int kTiles = D == 256 ? 1 : 2;      // row tiles of a CTA
   static constexpr int kStep = D == 256 ? 128 : 64;    // keys of a score buffer
+  static constexpr int kConvWarp = 4 * kTiles;         // first warp that widens V
+  static constexpr int kConvWarps = kMmaWarp - kConvWarp;
   static constexpr int kPer = kKeys / kStep;           // steps of a key tile
   static constexpr bool kWide = D >= 128;
   static constexpr int kRowBytes = kWide ? 128 : 64;
@@ -353,8 +356,9 @@ template <int D>
 __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, const uint8_t* sv,
                                             uint8_t* sc, PrSmem<D>& sm) {
   using C = Pr<D>;
-  const int t = threadIdx.x - kConvWarp * 32, lane = t & 31, warp = t >> 5;
-  const int k = t & 63, h = t >> 6;   // key of a piece, half of its row
+  constexpr int kShares = C::kConvWarps / 2;  // of a key's values
+  const int t = threadIdx.x - C::kConvWarp * 32, lane = t & 31, warp = t >> 5;
+  const int k = t & 63, h = t >> 6;           // key of a piece, share of its values
   const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
   Ring rv, rc;
   for (int kt = w.t0; kt < w.t1; ++kt) {
@@ -363,7 +367,7 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
     const bool whole = !edge_tile(a, w, kt, pos0, pos1) && sm.meta[slot].absent == 0;
     if (!whole) {
       if (t < 4) sm.poison[slot][t] = 0;
-      asm volatile("bar.sync 2, 128;\n" ::: "memory");
+      asm volatile("bar.sync 2, %0;\n" ::"n"(32 * C::kConvWarps) : "memory");
     }
     for (int c = 0; c < 2; ++c) {
       wait(&sm.v_full[rv.i], rv.phase, &sm.abort, a.status);
@@ -376,8 +380,8 @@ __device__ __forceinline__ void widen_tiles(const AttnArgs& a, const Work& w, co
         live = kt * kKeys + key >= w.lo && kt * kKeys + key < w.hi &&
                !((sm.meta[slot].absent >> (key >> 4)) & 1);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int b = h * (D / 2) + 16 * i;        // first of 16 values
+      for (int i = 0; i < D / 16 / kShares; ++i) {
+        const int b = h * (D / kShares) + 16 * i;  // first of 16 values
         uint4 x = *reinterpret_cast<const uint4*>(v + b / C::kRowBytes * C::kVPanelBytes +
                                                   swz<C::kWide>(k, b % C::kRowBytes));
         if (!whole) {
@@ -723,13 +727,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc::mbar_init(&sm.p_full[i], 128);
       tc::mbar_init(&sm.pv_done[i], 1);
       tc::mbar_init(&sm.v_full[i], 1);
-      tc::mbar_init(&sm.v_empty[i], 4);
-      tc::mbar_init(&sm.c_full[i], 4);
+      tc::mbar_init(&sm.v_empty[i], C::kConvWarps);
+      tc::mbar_init(&sm.c_full[i], C::kConvWarps);
       tc::mbar_init(&sm.c_empty[i], w.tiles);
     }
     for (int i = 0; i < C::kMeta; ++i) {
       tc::mbar_init(&sm.meta_full[i], 1);
-      tc::mbar_init(&sm.poison_full[i], 4);
+      tc::mbar_init(&sm.poison_full[i], C::kConvWarps);
     }
     sm.abort = 0;
     tc::fence_barrier_init();
@@ -756,9 +760,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (any && warp - kMmaWarp < w.tiles)
       issue<D>(a, w, warp - kMmaWarp, tc::smem_u32(sq), tc::smem_u32(sk), tc::smem_u32(sc), tmem,
                sm);
-  } else if (warp >= kConvWarp && warp < kMmaWarp) {
+  } else if (warp >= C::kConvWarp) {
     if (any) widen_tiles<D>(a, w, sv, sc, sm);
-  } else if (warp < 4 * C::kTiles && warp / 4 < w.tiles) {
+  } else if (warp / 4 < w.tiles) {
     const int tile = warp / 4, row = tid & 127;
     float* fac = sm.fac + tile * 128;
     stage_queries<D>(a, w, tile, q, q_stride, sq + (size_t)tile * 2 * C::kQBytes, fac);
@@ -809,7 +813,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (splits > 1 && tid == 0)  // parts, tokens, first row, key head
     sp.shared[blockIdx.x] =
         w.part == 0 ? make_int4(splits, w.toks, w.v.row0 + w.tok0, w.h) : make_int4(0, 0, 0, 0);
-  if (warp >= kConvWarp && *(volatile int*)&sm.abort) {
+  if (warp >= C::kConvWarp && *(volatile int*)&sm.abort) {
     // a wait gave up: time for this CTA's copies and MMAs in flight to end before its
     // memory goes back
     const unsigned long long t = tc::global_ns();
