@@ -50,6 +50,20 @@ __device__ __forceinline__ int unit_seq(const AttnArgs& a, int per, int extra, i
   return below;
 }
 
+// The same by each warp on its own, without a barrier: for few sequences.
+__device__ __forceinline__ int unit_seq_warp(const AttnArgs& a, int per, int extra, int u,
+                                             int* first) {
+  const int lane = threadIdx.x & 31;
+  int below = 0;
+  for (int b = 1; b < a.n_seqs; b += 32) {
+    const int s = b + lane;
+    const bool in = s < a.n_seqs && min(max(a.row_start[s], 0), a.rows) / per + extra * s <= u;
+    below += __popc(__ballot_sync(0xffffffffu, in));
+  }
+  *first = min(max(a.row_start[below], 0), a.rows) / per + extra * below;
+  return below;
+}
+
 __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll

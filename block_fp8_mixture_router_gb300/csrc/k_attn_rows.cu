@@ -184,15 +184,14 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 
 // One (page, head, K or V) of the call's rows: the values wait in registers
 // while the block agrees on the page's scale, so they are read once.
-template <int D, bool kStep>
+template <int D, int kMost, bool kStep>
 __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs& p, int unit,
                                             int h, bool is_v, float* swap) {
   using L = Lanes<D>;
-  constexpr int kMost = 128 / L::kRows;  // passes of a 128-token page
   __shared__ float s_max[kRowThreads / 32];
   const int P = 1 << a.page_shift;
   int u0;
-  const int s = unit_seq(a, P, 2, unit, &u0);
+  const int s = a.n_seqs <= 128 ? unit_seq_warp(a, P, 2, unit, &u0) : unit_seq(a, P, 2, unit, &u0);
   const SeqView v = seq_view(a, s);
   if (!v.ok && threadIdx.x == 0) atomicOr(a.status, kAttnBadBatch);
   if (v.n == 0 || v.len == 0 || unit < u0) return;
@@ -202,20 +201,12 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
   const int lo = (int)max((long long)start, t0);
   const int hi = (int)min((long long)v.len, t0 + P);
   if (lo >= hi) return;
-  const int page = page_at(a, s, j);
-  if (page < 0) {
-    if (threadIdx.x == 0) atomicOr(a.status, kAttnBadBatch);
-    return;
-  }
   const int slot0 = lo - (int)t0, m = hi - lo;
   const int row0 = v.row0 + (lo - v.first);
   const int c = threadIdx.x % L::kPer, sub = threadIdx.x / L::kPer;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
   const bf16* src = (is_v ? p.v : p.k) + (int64_t)row0 * stride + h * D + 8 * c;
-  const size_t block = (size_t)page * a.Hkv + h;
-  float* scale_at = (is_v ? a.vs : a.ks) + block;
-  const float old = slot0 > 0 ? *scale_at : 0.0f;
-
+  // the rows are on their way while the page is looked up
   uint4 raw[kMost];
 #pragma unroll
   for (int k = 0; k < kMost; ++k) {
@@ -223,6 +214,14 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
     raw[k] = make_uint4(0, 0, 0, 0);
     if (i < m) raw[k] = *reinterpret_cast<const uint4*>(src + i * stride);
   }
+  const int page = page_at(a, s, j);
+  if (page < 0) {
+    if (threadIdx.x == 0) atomicOr(a.status, kAttnBadBatch);
+    return;
+  }
+  const size_t block = (size_t)page * a.Hkv + h;
+  float* scale_at = (is_v ? a.vs : a.ks) + block;
+  const float old = slot0 > 0 ? *scale_at : 0.0f;
   float amax = 0.0f;
   uint32_t bad = 0;  // passes whose row holds an infinity or NaN
   const uint32_t my_lanes = (L::kPer == 32 ? 0xffffffffu : ((1u << (L::kPer & 31)) - 1u))
@@ -273,6 +272,9 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
       w[i] = q;
     }
   }
+  // a power of two divides by an exact product
+  const bool whole = (__float_as_uint(scale) & 0x807FFFFFu) == 0 && scale < 0x1p126f;
+  const float inv = __frcp_rn(scale);
 #pragma unroll
   for (int k = 0; k < kMost; ++k) {
     const int i = k * L::kRows + sub;
@@ -282,7 +284,10 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
     uint2 q;
     if (bad & (1u << k)) {
       q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    } else {
+    } else if (whole) {
+      q.x = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      q.y = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+    } else {  // (a scale of other code's)
       q.x = quant4(x[0], x[1], x[2], x[3], scale);
       q.y = quant4(x[4], x[5], x[6], x[7], scale);
     }
@@ -293,15 +298,16 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
 
 // Blocks [0, units * Hkv * 2) append; the blocks behind them (a step's
 // prologue only) norm and rotate the queries of block_rows rows each.
-template <int D, bool kStep>
-__global__ void __launch_bounds__(kRowThreads, 2)
+// kMost: passes of a page's tokens, which wait in registers.
+template <int D, int kMost, bool kStep>
+__global__ void __launch_bounds__(kRowThreads, kMost <= 4 ? 4 : kMost <= 8 ? 3 : 2)
     k_append(AttnArgs a, AppendArgs p, int append_blocks, int block_rows) {
   __shared__ float s_swap[kStep ? kRowThreads * 8 : 1];
   pdl_trigger();
   if ((int)blockIdx.x < append_blocks) {
     const int b = blockIdx.x;
     const int uh = b >> 1;
-    append_unit<D, kStep>(a, p, uh / a.Hkv, uh % a.Hkv, b & 1, s_swap);
+    append_unit<D, kMost, kStep>(a, p, uh / a.Hkv, uh % a.Hkv, b & 1, s_swap);
     return;
   }
   if constexpr (kStep) {
@@ -362,19 +368,32 @@ cudaError_t rope_d(const bf16* x, int64_t x_stride, int heads, const int* positi
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t append_d(const AttnArgs& a, const AppendArgs& p, cudaStream_t s) {
+template <int D, int kMost>
+cudaError_t append_dm(const AttnArgs& a, const AppendArgs& p, cudaStream_t s) {
   const int units = (a.rows >> a.page_shift) + 2 * a.n_seqs;
   const int blocks = units * a.Hkv * 2;
   if (!p.q) {
-    k_append<D, false><<<blocks, kRowThreads, 0, s>>>(a, p, blocks, 0);
+    k_append<D, kMost, false><<<blocks, kRowThreads, 0, s>>>(a, p, blocks, 0);
   } else {
     const int br = rope_block_rows<D>(a.Hq);
     const int q_blocks = (a.rows + br - 1) / br;
-    k_append<D, true><<<blocks + q_blocks, kRowThreads,
-                        (size_t)br * (p.rope.rot / 2) * sizeof(float2), s>>>(a, p, blocks, br);
+    k_append<D, kMost, true><<<blocks + q_blocks, kRowThreads,
+                               (size_t)br * (p.rope.rot / 2) * sizeof(float2), s>>>(a, p, blocks,
+                                                                                    br);
   }
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t append_d(const AttnArgs& a, const AppendArgs& p, cudaStream_t s) {
+  // passes of a page: a power of two from one to 128 tokens' worth
+  const int passes = (1 << a.page_shift) / Lanes<D>::kRows;
+  constexpr int kMax = 128 / Lanes<D>::kRows;
+  if (passes <= 1) return append_dm<D, 1>(a, p, s);
+  if (passes <= 2) return append_dm<D, 2>(a, p, s);
+  if (passes <= 4) return append_dm<D, 4>(a, p, s);
+  if (kMax == 8 || passes <= 8) return append_dm<D, (kMax < 8 ? kMax : 8)>(a, p, s);
+  return append_dm<D, kMax>(a, p, s);
 }
 
 }  // namespace
