@@ -141,7 +141,7 @@ __device__ __forceinline__ void rope_items(const bf16* x, int64_t x_stride, int 
 // A block takes `block_rows` rows (all of their heads, or one of gridDim.y
 // shares of them); the rows' sines are computed once for all heads.
 template <int D>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 6)
     k_rope(const bf16* x, int64_t x_stride, int heads, const int* positions, const bf16* gamma,
            float eps, int rows, bf16* y, int64_t y_stride, RopeArgs r, int block_rows) {
   extern __shared__ float2 s_table[];
