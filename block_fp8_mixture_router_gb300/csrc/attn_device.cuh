@@ -85,13 +85,12 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // Cosine and sine (times the amplitude) of pair i at a position.  The angle in
 // turns is the top 32 bits of position x turns[i] modulo 2^64, read as a signed
-// fraction: off by at most 2^-33 of a turn, and its float by 2^-25.
+// fraction: off by at most 2^-33 of a turn, and its float by 2^-25.  Between -pi and
+// pi the fast functions are good to 2^-21, far below the results' rounding to bf16.
 __device__ __forceinline__ float2 rope_cs(const RopeArgs& r, int i, int pos) {
   const unsigned long long t = (unsigned long long)(long long)pos * r.turns[i];
-  const float half_turns = (float)(int)(t >> 32) * 0x1p-31f;
-  float sn, cs;
-  sincospif(half_turns, &sn, &cs);
-  return make_float2(cs * r.amp, sn * r.amp);
+  const float angle = (float)(int)(t >> 32) * (0x1p-32f * 6.283185307f);
+  return make_float2(__cosf(angle) * r.amp, __sinf(angle) * r.amp);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

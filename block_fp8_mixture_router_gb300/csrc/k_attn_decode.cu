@@ -776,13 +776,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
 
 // Joins the parts of the units that CTAs of a split launch shared: block (c, row)
 // looks at the unit that CTA c was the first to work on.  Parts are weighted by
-// their references and added in a fixed order: four interleaved runs, then those.
+// their references and added in a fixed order: kRuns interleaved runs, then those.  Bound
+// by the latency of its loads: the parts' sums are on their way with their references.
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(2 * D)
     k_attn_merge(AttnSplit sp, int g, bf16* out, int64_t out_stride) {
-  constexpr int kCols = D / 4;          // threads of a run, four values each
-  constexpr int kRuns = 4;
-  constexpr int kWarps = D / 32;
+  constexpr int kThreadsM = 2 * D, kCols = D / 4, kRuns = 8, kWarps = kThreadsM / 32;
+  constexpr int kAhead = 8;             // parts of a run that are loaded at once
   __shared__ float s_w[kAttnMaxCtas];   // the parts' weights
   __shared__ float s_m[kWarps], s_l[kWarps];
   __shared__ float4 s_x[kRuns - 1][kCols];
@@ -794,17 +794,30 @@ __global__ void __launch_bounds__(D)
   const auto slot = [&](int p) {
     return (size_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kAttnSlotRows + row;
   };
-  // the largest reference, then the weights and the sum
-  float m = -INFINITY;
-  for (int p = tid; p < parts; p += D) m = fmaxf(m, __ldcg(&sp.ml[slot(p)].x));
+  const int col = tid % kCols, run = tid / kCols;
+  float4 y[kAhead];
+  const auto load = [&](int p0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + run + k * kRuns;
+      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p < parts) y[k] = __ldcg(reinterpret_cast<const float4*>(sp.o + slot(p) * D) + col);
+    }
+  };
+  // the first parts' references and sums; more parts than threads are read again
+  float2 ml = make_float2(-INFINITY, 0.0f);
+  if (tid < parts) ml = __ldcg(sp.ml + slot(tid));
+  load(0);
+  float m = ml.x;
+  for (int p = tid + kThreadsM; p < parts; p += kThreadsM) m = fmaxf(m, __ldcg(&sp.ml[slot(p)].x));
   m = warp_max(m);
   if ((tid & 31) == 0) s_m[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w]);
   float l = 0.0f;
-  for (int p = tid; p < parts; p += D) {
-    const float2 ml = __ldcg(sp.ml + slot(p));
+  for (int p = tid; p < parts; p += kThreadsM) {
+    if (p >= kThreadsM) ml = __ldcg(sp.ml + slot(p));
     const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
     s_w[p] = f;
     l = fmaf(ml.y, f, l);
@@ -815,21 +828,28 @@ __global__ void __launch_bounds__(D)
   l = 0.0f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) l += s_l[w];
-  const int col = tid % kCols, run = tid / kCols;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-  for (int p = run; p < parts; p += kRuns) {
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(sp.o + slot(p) * D) + col);
-    const float f = s_w[p];
-    x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+  for (int p0 = 0;;) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + run + k * kRuns;
+      if (p < parts) {
+        const float f = s_w[p];
+        x = make_float4(fmaf(y[k].x, f, x.x), fmaf(y[k].y, f, x.y), fmaf(y[k].z, f, x.z),
+                        fmaf(y[k].w, f, x.w));
+      }
+    }
+    p0 += kAhead * kRuns;
+    if (p0 >= parts) break;
+    load(p0);
   }
   if (run > 0) s_x[run - 1][col] = x;
   __syncthreads();
   if (run > 0) return;
 #pragma unroll
   for (int i = 0; i < kRuns - 1; ++i) {
-    const float4 y = s_x[i][col];
-    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    const float4 z = s_x[i][col];
+    x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
   }
   const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
   const int tok = row / g;
@@ -869,7 +889,8 @@ cudaError_t launch_dr(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64
                                    m.k, m.v, a, q, q_stride, out, out_stride, sp);
   // (one CTA shares no unit)
   if (e != cudaSuccess || !split || grid == 1) return e;
-  return launch_pdl(k_attn_merge<D>, dim3(grid, R), dim3(D), 0, s, true, sp, a.g, out, out_stride);
+  return launch_pdl(k_attn_merge<D>, dim3(grid, R), dim3(2 * D), 0, s, true, sp, a.g, out,
+                    out_stride);
 }
 
 }  // namespace
