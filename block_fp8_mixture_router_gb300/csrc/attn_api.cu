@@ -33,8 +33,18 @@ struct moe_attn {
 namespace {
 
 constexpr int kDecTileRows = kAttnSlotRows;
-constexpr int kPromptRows = 32;  // rows of a sequence (tokens x query heads of a key head)
-                                 // above which the prompt kernel takes them
+
+// The decode kernel takes a sequence whose rows (tokens x query heads of a key head) fit
+// one of its tiles, or few tiles in all: it reads the keys once for every tile.  The
+// prompt kernel takes the others, with 128 rows to a tile.  Tiles = sequences x key heads
+// x tiles of a sequence; measured over 300 to 200000 keys, prompt kernel's time over
+// decode kernel's, geometric means:
+//   head_dim    4 tiles     8     16     24     64
+//         64       0.91   0.85   0.78   0.67   0.63
+//        128       1.03   0.94   0.86   0.75   0.66
+//        256       1.31   1.15   1.12   0.95   0.78
+// hence more than head_dim / 16 tiles.
+constexpr int kPromptTiles = 16;
 
 struct Device {
   int prev = -1;
@@ -223,8 +233,14 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const long long cap = (long long)b->pages_stride << c->page_shift;
   const long long keys = b->max_kv_len > 0 ? std::min<long long>(b->max_kv_len, cap) : cap;
   const int seq_rows = b->max_seq_rows > 0 ? std::min(b->max_seq_rows, b->rows) : b->rows;
-  // Many rows of a sequence: the prompt kernel, whose row tiles hold 128.
-  const bool prompt = (long long)seq_rows * a.g > kPromptRows;
+  // Rows of a tile of the decode kernel: one row over 262143 keys with four query heads
+  // to a key head takes 50 us with eight rows to a tile and 72 with 16.
+  const int tile_rows = (long long)seq_rows * a.g <= 8 ? 8 : kDecTileRows;
+  const int tq = tile_rows / a.g;
+  const long long seq_tiles = (seq_rows + tq - 1) / tq;
+  const long long units = (long long)b->rows / tq + b->n_seqs;  // per key head, at most
+  const bool prompt = (long long)seq_rows * a.g > kDecTileRows &&
+                      std::min(units, seq_tiles * b->n_seqs) * a.Hkv > D / kPromptTiles;
   AttnMaps maps;
   if (!make_attn_maps(&maps, a, D, prompt)) return MOE_ERR_CUDA;
   if (prompt) {
@@ -239,13 +255,10 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
                ? MOE_OK
                : MOE_ERR_CUDA;
   }
-  // eight rows to a tile where one holds a sequence's: less work per key
-  const int tile_rows = (long long)seq_rows * a.g <= 8 ? 8 : kDecTileRows;
-  const int tq = tile_rows / a.g;
-  const long long units = (long long)b->rows / tq + b->n_seqs;  // per key head, at most
-  // Few row tiles: the key tiles of all of them in equal runs, at least two
-  // (256 keys) to a CTA.  Many: a CTA per row tile.
-  const bool split = units <= 2048 && (seq_rows + tq - 1) / tq <= 64;
+  // Few row tiles: the key tiles of all of them in equal runs, at least two (256 keys) to
+  // a CTA (one row over 4096 keys: 8.9 us, with one tile to a CTA 9.5).  Many: a CTA per
+  // row tile.
+  const bool split = units <= 2048 && seq_tiles <= 64;
   long long grid = units * a.Hkv;
   if (split) {
     long long span = keys;
@@ -253,8 +266,8 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
     const long long tiles = units * a.Hkv * ((span + kAttnKeys - 1) / kAttnKeys);
     grid = std::max<long long>(1, std::min<long long>((tiles + 1) / 2, c->dec_slots));
   }
-  return launch_attn_decode(D, tile_rows, a, maps, q, q_stride, out, out_stride, c->split, (int)grid, split, pdl,
-                            s) == cudaSuccess
+  return launch_attn_decode(D, tile_rows, a, maps, q, q_stride, out, out_stride, c->split,
+                            (int)grid, split, pdl, s) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }

@@ -829,43 +829,104 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 }
 
-// Joins the shares of the units' keys: a warp for each row of the unit that block x
-// was the first to work on.
-template <int D>
-__global__ void __launch_bounds__(256)
+// Joins the parts of a unit's rows, which CTAs of a launch that splits keys left: kRuns
+// warps take a row, each an interleaved share of the parts, and their sums are added in
+// order.  Bound by the latency of its loads: a row's references and sums are read at once,
+// a lane to a part, and kAhead parts' weighted sums with them.  One part after the other
+// made 128 rows over 50000 keys, 148 parts, 145 us; now 39.  Few parts get a warp to a
+// row: a chunk of 1024 rows over 4000 keys, in two parts, takes 58 us, with four warps 80.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeFew = 16, kMergeRuns = 4;
+
+template <int D, bool kFew>
+__global__ void __launch_bounds__(kMergeThreads)
     k_prompt_merge(AttnSplit sp, int g, int splits, bf16* out, int64_t out_stride) {
+  constexpr int kPer = D / 32;  // columns of a lane
+  constexpr int kMost = kFew ? kMergeFew : kAttnPromptCtas;
+  constexpr int kLoads = (kMost + 31) / 32;
+  constexpr int kAhead = kFew ? 2 : 8, kRuns = kFew ? 1 : kMergeRuns;
+  __shared__ float s_w[kMergeWarps][kMost];
+  __shared__ float s_x[kFew ? 1 : kMergeWarps][kPer][32];
   pdl_wait();
-  const int c0 = blockIdx.x * splits, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x * splits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 unit = __ldcg(sp.shared + c0);
-  const int parts = unit.x, tq = 128 / g;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);  // of the unit's row tiles
+  const int parts = unit.x, tq = 128 / g, run = warp % kRuns;
+  const int row = blockIdx.y * (kMergeWarps / kRuns) + warp / kRuns;  // of the unit's row tiles
   const int tile = row >> 7, r = row & 127, in = r / g;
   const int tok = tile * tq + in;
-  if (parts == 0 || in >= tq || tok >= unit.y) return;
+  const bool on = parts > 0 && in < tq && tok < unit.y;
   const auto slot = [&](int p) { return (size_t)(c0 + p) * kAttnPromptRows + row; };
-  float m = -INFINITY;
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, __ldcg(&sp.ml[slot(p)].x));
-  float l = 0.0f, x[D / 32];
+  float y[kAhead][kPer];
+  const auto load = [&](int p0) {
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = 0.0f;
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = __ldcg(sp.ml + slot(p));
-    const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    const float* o = sp.o + slot(p) * D + lane * (D / 32);
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + k * kRuns;
+      const float* o = sp.o + slot(p) * D + lane * kPer;
 #pragma unroll
-    for (int i = 0; i < D / 32; i += 2) {
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(o + i));
-      x[i] = fmaf(y.x, f, x[i]);
-      x[i + 1] = fmaf(y.y, f, x[i + 1]);
+      for (int i = 0; i < kPer; i += 2) {
+        float2 v = make_float2(0.0f, 0.0f);
+        if (p < parts) v = __ldcg(reinterpret_cast<const float2*>(o + i));
+        y[k][i] = v.x;
+        y[k][i + 1] = v.y;
+      }
+    }
+  };
+  float x[kPer], inv = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
+  if (on) {
+    float2 ml[kLoads];
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int p = k * 32 + lane;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      if (p < parts) ml[k] = __ldcg(sp.ml + slot(p));
+    }
+    load(run);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) m = fmaxf(m, ml[k].x);
+    m = warp_max(m);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int p = k * 32 + lane;
+      const float f = ml[k].x == -INFINITY ? 1.0f : exp2_approx(ml[k].x - m);
+      if (p < parts) s_w[warp][p] = f;
+      l = fmaf(ml[k].y, f, l);
+    }
+    l = warp_sum(l);
+    inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+    __syncwarp();
+    for (int p0 = run;;) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = p0 + k * kRuns;
+        if (p < parts) {
+          const float f = s_w[warp][p];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) x[i] = fmaf(y[k][i], f, x[i]);
+        }
+      }
+      p0 += kAhead * kRuns;
+      if (p0 >= parts) break;
+      load(p0);
     }
   }
-  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-  bf16* to = out + (int64_t)(unit.z + tok) * out_stride + (unit.w * g + r - in * g) * D +
-             lane * (D / 32);
+  if constexpr (!kFew) {
 #pragma unroll
-  for (int i = 0; i < D / 32; i += 2)
+    for (int i = 0; i < kPer; ++i) s_x[warp][i][lane] = x[i];
+    __syncthreads();
+    if (run > 0) return;
+#pragma unroll
+    for (int w = 1; w < kRuns; ++w)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] += s_x[warp + w][i][lane];
+  }
+  if (!on) return;
+  bf16* to = out + (int64_t)(unit.z + tok) * out_stride + (unit.w * g + r - in * g) * D +
+             lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
     *reinterpret_cast<__nv_bfloat162*>(to + i) = __floats2bfloat162_rn(x[i] * inv, x[i + 1] * inv);
 }
 
@@ -878,8 +939,12 @@ cudaError_t launch_d(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64_
       launch_pdl(k_attn_prompt<D>, dim3(heads * splits), dim3(kPThreads), pr_smem_bytes<D>(), s,
                  pdl, m.k, m.v64, a, q, q_stride, out, out_stride, sp, units, splits);
   if (e != cudaSuccess || splits == 1) return e;
-  return launch_pdl(k_prompt_merge<D>, dim3(heads, Pr<D>::kTiles * 16), dim3(256), 0, s, true, sp,
-                    a.g, splits, out, out_stride);
+  const int rows = Pr<D>::kTiles * 128;
+  if (splits <= kMergeFew)
+    return launch_pdl(k_prompt_merge<D, true>, dim3(heads, rows / kMergeWarps),
+                      dim3(kMergeThreads), 0, s, true, sp, a.g, splits, out, out_stride);
+  return launch_pdl(k_prompt_merge<D, false>, dim3(heads, rows * kMergeRuns / kMergeWarps),
+                    dim3(kMergeThreads), 0, s, true, sp, a.g, splits, out, out_stride);
 }
 
 }  // namespace

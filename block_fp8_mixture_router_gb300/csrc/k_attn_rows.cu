@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kRowThreads, 6)
   const int half = r.rot >> 1;
   rope_items<D>(x, x_stride, heads, row0, first, min(share, items - first), gamma, eps, y,
                 y_stride, r, s_table, s_swap, [&] {
+#pragma unroll 1
                   for (int i = threadIdx.x; i < nr * half; i += kRowThreads)
                     s_table[i] = rope_cs(r, i % half, __ldg(positions + row0 + i / half));
                   __syncthreads();
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(kRowThreads, kMost <= 4 ? 4 : kMost <= 8 ? 3 :
                     }
                     const int* start = in_smem ? s_start : a.row_start;
                     int last = -1, pos = 0;
+#pragma unroll 1
                     for (int i = threadIdx.x; i < nr * half; i += kRowThreads) {
                       const int row = i / half;
                       if (row != last) {
