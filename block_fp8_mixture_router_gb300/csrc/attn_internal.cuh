@@ -48,7 +48,8 @@ struct RopeArgs {
 // Partial results of key ranges that CTAs of one launch worked through: CTA c has
 // slots 2c and 2c + 1 of kAttnSlotRows rows.
 struct AttnSplit {
-  float* o;        // [slots][kAttnSlotRows][D]: weighted sums of the values
+  float* o;        // [slots][kAttnSlotRows][D]: weighted sums of the values (the prompt
+                   // kernel's: [CTAs][row tiles][D / 4][128 rows][4])
   float2* ml;      // [slots][kAttnSlotRows]: the rows' references (log2) and sums
   int4* shared;    // [CTAs]: the unit that begins in this CTA and goes on in others:
                    // its parts (0: none), rows, first row, key head

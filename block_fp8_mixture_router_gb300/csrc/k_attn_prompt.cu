@@ -147,6 +147,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ __nv_bfloat162 abs2(uint32_t w) {
+  w &= 0x7FFF7FFFu;
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
 struct Ring {
   int i = 0;
   uint32_t phase = 0;
@@ -186,53 +191,60 @@ __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Work& w, 
   const int t = threadIdx.x & 127;
   const int c = t % kPer, sub = t / kPer;
   const int valid = min(w.tq, w.toks - tile * w.tq) * a.g;
-  constexpr int kStep = 128 / kPer;
-#pragma unroll 4
-  for (int r = sub; r < 128; r += kStep) {
-    const int tok = r / a.g;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (r < valid)
-      raw = *reinterpret_cast<const uint4*>(
-          q + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * q_stride +
-          (w.h * a.g + r - tok * a.g) * D + 8 * c);
-    float x[8];
-    unpack8(raw, x);
-    float mx = 0.0f;
-    bool odd = false;
+  constexpr int kStep = 128 / kPer, kBatch = 8;  // rows of a pass; passes loaded at once
+  const uint32_t per_g = 65536u / a.g + 1;       // r / g = r per_g >> 16 for r below 128
+  // (with a pass's loads behind the pass before, 1024 rows at head_dim 256 took 15 us)
+#pragma unroll 1
+  for (int r0 = 0; r0 < 128; r0 += kBatch * kStep) {
+    uint4 raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      odd |= !is_finite(x[i]);
-      mx = fmaxf(mx, fabsf(x[i]));
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r0 + i * kStep + sub, tok = r * per_g >> 16;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (r < valid)
+        raw[i] = *reinterpret_cast<const uint4*>(
+            q + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * q_stride +
+            (w.h * a.g + r - tok * a.g) * D + 8 * c);
     }
-    if (odd) mx = __int_as_float(0x7F800000);
 #pragma unroll
-    for (int o = kPer / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    uint2 hi = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), lo = make_uint2(0, 0);  // NaN scores
-    float f = 0.0f;
-    if (is_finite(mx)) {
-      const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-      f = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * a.scale;
-      uint32_t p[2], z[2];
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r0 + i * kStep + sub;
+      // the row's largest magnitude, NaN if it has one
+      __nv_bfloat162 top = __hmax2_nan(__hmax2_nan(abs2(raw[i].x), abs2(raw[i].y)),
+                                       __hmax2_nan(abs2(raw[i].z), abs2(raw[i].w)));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float y[4];
+      for (int o = kPer / 2; o > 0; o >>= 1)
+        top = __hmax2_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mx = __bfloat162float(__hmax_nan(__low2bfloat16(top), __high2bfloat16(top)));
+      uint2 hi = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), lo = make_uint2(0, 0);  // NaN scores
+      float f = 0.0f;
+      if (is_finite(mx)) {
+        const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+        f = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * a.scale;
+        float x[8];
+        unpack8(raw[i], x);
+        uint32_t p[2], z[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = x[4 * i + k] * up;
-        p[i] = e4m3x4(y[0], y[1], y[2], y[3]);
-        const uint32_t h01 = widen(p[i]), h23 = widen(p[i] >> 16);
-        const float2 b01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-        const float2 b23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-        z[i] = e4m3x4(y[0] - b01.x, y[1] - b01.y, y[2] - b23.x, y[3] - b23.y);
+        for (int k = 0; k < 2; ++k) {
+          float y[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) y[n] = x[4 * k + n] * up;
+          p[k] = e4m3x4(y[0], y[1], y[2], y[3]);
+          const uint32_t h01 = widen(p[k]), h23 = widen(p[k] >> 16);
+          const float2 b01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+          const float2 b23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+          z[k] = e4m3x4(y[0] - b01.x, y[1] - b01.y, y[2] - b23.x, y[3] - b23.y);
+        }
+        hi = make_uint2(p[0], p[1]);
+        lo = make_uint2(z[0], z[1]);
       }
-      hi = make_uint2(p[0], p[1]);
-      lo = make_uint2(z[0], z[1]);
+      const int panel = 8 * c / C::kRowBytes, b = 8 * c % C::kRowBytes;
+      uint8_t* at = sq + panel * 128 * C::kRowBytes + swz<C::kWide>(r, b);
+      *reinterpret_cast<uint2*>(at) = hi;
+      *reinterpret_cast<uint2*>(at + C::kQBytes) = lo;
+      if (c == 0) fac[r] = f;
     }
-    const int panel = 8 * c / C::kRowBytes, b = 8 * c % C::kRowBytes;
-    uint8_t* at = sq + panel * 128 * C::kRowBytes + swz<C::kWide>(r, b);
-    *reinterpret_cast<uint2*>(at) = hi;
-    *reinterpret_cast<uint2*>(at + C::kQBytes) = lo;
-    if (c == 0) fac[r] = f;
   }
 }
 
@@ -488,43 +500,70 @@ __device__ __forceinline__ void issue(const AttnArgs& a, const Work& w, int m, u
 }
 
 // ---- the softmax warps --------------------------------------------------------------
-// What a row sees of a step's keys.
+// What a row does not see of 64 keys becomes minus infinity, and keys that it sees whose
+// values hold a NaN become NaN weights.  Done to the scores themselves, so that what
+// follows is the same for tiles with and without an edge: as compares at each use an edge
+// took 3.7 us of a CTA, now less than one.
 struct RowMask {
-  int low, high;        // columns [low, high]
-  uint32_t absent;      // but for 16-key groups without a page
-  uint32_t poison[4];   // columns with a NaN value
+  unsigned long long seen, nan;
 };
 
-// The largest of a row's 64 scores (columns col0 on), in log2 units.
-template <bool kEdge>
-__device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float* f, int col0,
-                                        const RowMask& mk) {
+// low, high: the columns [low, high] that the row sees; absent: 16-key groups that it does
+// not; poison: columns with a NaN value.
+__device__ __forceinline__ RowMask row_mask(int low, int high, uint32_t absent,
+                                            unsigned long long poison) {
+  RowMask mk;
+  mk.seen = high < 0 ? 0 : high >= 63 ? ~0ull : (2ull << high) - 1;
+  mk.seen &= low <= 0 ? ~0ull : low > 63 ? 0 : ~0ull << low;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if ((absent >> g) & 1) mk.seen &= ~(0xFFFFull << (16 * g));
+  mk.nan = mk.seen & poison;
+  return mk;
+}
+
+__device__ __forceinline__ void hide64(uint32_t (&v)[2][32], const RowMask& mk) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t seen = (uint32_t)(mk.seen >> (32 * h));
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((seen >> c) & 1)) v[h][c] = 0xFF800000u;
+  }
+  if (__any_sync(0xffffffffu, mk.nan != 0)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t nan = (uint32_t)(mk.nan >> (32 * h));
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if ((nan >> c) & 1) v[h][c] = 0x7FFFFFFFu;
+    }
+  }
+}
+
+// The largest of a row's 64 scores, in log2 units (NaN scores do not count).
+__device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float* f) {
   float peak = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float x[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      x[c] = __uint_as_float(v[g >> 1][16 * (g & 1) + c]);
-      if (kEdge && (col0 + 16 * g + c < mk.low || col0 + 16 * g + c > mk.high)) x[c] = -INFINITY;
-    }
+    for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(v[g >> 1][16 * (g & 1) + c]);
     float y[5];
 #pragma unroll
     for (int c = 0; c < 5; ++c) y[c] = max3(x[3 * c], x[3 * c + 1], x[3 * c + 2]);
     const float m = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15]));
-    if (kEdge && (((mk.absent >> (col0 / 16 + g)) & 1) || m == -INFINITY)) continue;
     peak = fmaxf(peak, m * f[g]);
   }
   return peak;
 }
 
-// Weights of a row's 64 keys (columns col0 on, 16-key groups group0 on of the tile),
+// Weights of a row's 64 keys (16-key groups group0 on of the tile),
 // 2^(s f + base) by groups of 16, as fp16 to tensor memory; returns their sum freed of
 // the pages' value scales.
-template <bool kEdge>
 __device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_p, const float* f,
-                                         const Meta& me, int group0, int col0, float log_up,
-                                         float down, float m_base, const RowMask& mk) {
+                                         const Meta& me, int group0, float log_up, float down,
+                                         float m_base) {
   float sum = 0.0f;
   const float4 lv = *reinterpret_cast<const float4*>(me.log_vs + group0);
   const float4 iv = *reinterpret_cast<const float4*>(me.inv_vs + group0);
@@ -547,15 +586,6 @@ __device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_
                         ff, bb);
         x.x = exp2_approx(x.x);
         x.y = exp2_approx(x.y);
-        if constexpr (kEdge) {
-          const int c = col0 + 16 * g + 2 * i;
-          const bool there = !((mk.absent >> (c / 16)) & 1);
-          const uint32_t bad = mk.poison[c / 32] >> (16 * q + 2 * i);
-          if (bad & 1) x.x = __int_as_float(0x7FFFFFFF);
-          if (bad & 2) x.y = __int_as_float(0x7FFFFFFF);
-          if (!there || c < mk.low || c > mk.high) x.x = 0.0f;
-          if (!there || c + 1 < mk.low || c + 1 > mk.high) x.y = 0.0f;
-        }
         acc[i & 1] = add2(acc[i & 1], x);
         p[8 * q + i] = f16x2_of(x.x, x.y);
       }
@@ -592,15 +622,18 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
     const Meta& me = sm.meta[slot];
     const float top = me.top;
     const bool edge = edge_tile(a, w, kt, pos0, pos1) || me.absent != 0;
-    RowMask mk;
+    RowMask mk[C::kStep / 64];
     if (edge) {
       if (part == 0) wait(&sm.poison_full[slot], (i / C::kMeta) & 1, abort, a.status);
       const int key0 = kt * kKeys + part * C::kStep;
-      mk.high = min(pos - key0, kKeys);
-      mk.low = a.window ? pos - a.window + 1 - key0 : -1;
-      mk.absent = me.absent >> group0;
+      const int high = min(pos - key0, kKeys);
+      const int low = a.window ? pos - a.window + 1 - key0 : -1;
 #pragma unroll
-      for (int k = 0; k < C::kStep / 32; ++k) mk.poison[k] = sm.poison[slot][group0 / 2 + k];
+      for (int c = 0; c < C::kStep / 64; ++c) {
+        const uint32_t* bits = sm.poison[slot] + group0 / 2 + 2 * c;
+        mk[c] = row_mask(low - 64 * c, high - 64 * c, me.absent >> (group0 + 4 * c),
+                         bits[0] | (unsigned long long)bits[1] << 32);
+      }
     }
     float f[C::kStep / 16];
 #pragma unroll
@@ -608,6 +641,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       const float4 ks = *reinterpret_cast<const float4*>(me.ks + group0 + k);
       f[k] = fac * ks.x, f[k + 1] = fac * ks.y, f[k + 2] = fac * ks.z, f[k + 3] = fac * ks.w;
     }
+    if (edge)  // (minus infinity times a factor that has become zero would be NaN)
+#pragma unroll
+      for (int k = 0; k < C::kStep / 16; ++k) f[k] = fmaxf(f[k], 0x1p-126f);
     wait(&sm.s_full[buf], (j >> 1) & 1, abort, a.status);
     tc::fence_after_sync();
     __syncwarp();
@@ -617,13 +653,13 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       tc::tmem_ld_async(t_s + c * 64, v[0]);
       tc::tmem_ld_async(t_s + c * 64 + 32, v[1]);
       tc::wait_ld();
+      if (edge) hide64(v, mk[c]);
     };
     float peak = -INFINITY;
 #pragma unroll
     for (int c = 0; c < C::kStep / 64; ++c) {
       load(c);
-      peak = fmaxf(peak, edge ? peak64<true>(v, f + 4 * c, 64 * c, mk)
-                              : peak64<false>(v, f + 4 * c, 64 * c, mk));
+      peak = fmaxf(peak, peak64(v, f + 4 * c));
     }
     if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
       // new references for the warp's rows, and their sums brought to them
@@ -655,10 +691,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
 #pragma unroll
     for (int c = 0; c < C::kStep / 64; ++c) {
       if (C::kStep > 64) load(c);  // (64 scores are still in registers)
-      l += edge ? weigh64<true>(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, 64 * c, log_up,
-                                down, m_base, mk)
-                : weigh64<false>(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, 64 * c, log_up,
-                                 down, m_base, mk);
+      l += weigh64(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, log_up, down, m_base);
     }
     tc::wait_st();
     tc::fence_before_sync();
@@ -778,7 +811,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (splits == 1) scale *= l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     bf16* to = out + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * out_stride +
                (w.h * a.g + row - tok * a.g) * D;
-    const size_t slot = (size_t)blockIdx.x * kAttnPromptRows + tile * 128 + row;
+    const size_t slot = (size_t)blockIdx.x * kAttnPromptRows + tile * 128;
 #pragma unroll 1
     for (int b = 0; b < D; b += 32) {
       uint32_t v[32];
@@ -802,13 +835,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       } else {
 #pragma unroll
         for (int k = 0; k < 32; k += 4)
-          __stcg(reinterpret_cast<float4*>(sp.o + slot * D + b + k),
+          __stcg(reinterpret_cast<float4*>(sp.o + slot * D + (b + k) * 128 + 4 * row),
                  make_float4(__uint_as_float(v[k]) * scale, __uint_as_float(v[k + 1]) * scale,
                              __uint_as_float(v[k + 2]) * scale,
                              __uint_as_float(v[k + 3]) * scale));
       }
     }
-    if (splits > 1 && valid) __stcg(sp.ml + slot, make_float2(m, l));
+    if (splits > 1 && valid) __stcg(sp.ml + slot + row, make_float2(m, l));
   }
   if (splits > 1 && tid == 0)  // parts, tokens, first row, key head
     sp.shared[blockIdx.x] =
@@ -829,105 +862,100 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 }
 
-// Joins the parts of a unit's rows, which CTAs of a launch that splits keys left: kRuns
-// warps take a row, each an interleaved share of the parts, and their sums are added in
-// order.  Bound by the latency of its loads: a row's references and sums are read at once,
-// a lane to a part, and kAhead parts' weighted sums with them.  One part after the other
-// made 128 rows over 50000 keys, 148 parts, 145 us; now 39.  Few parts get a warp to a
-// row: a chunk of 1024 rows over 4000 keys, in two parts, takes 58 us, with four warps 80.
-constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeFew = 16, kMergeRuns = 4;
+// Joins the parts of a unit's rows, which CTAs of a launch that splits keys left as
+// [row tile][4 columns][row] (a row for each thread that writes: 16 bytes of 32 rows side
+// by side; row after row the writes took 3 us of a 1024-row chunk's 67).  A thread has four
+// columns of a row; kRuns of them take interleaved shares of the parts and are added in
+// order.  Bound by the latency of its loads, so the sums of kAhead parts are on their way
+// at once: one part after the other made 128 rows over 50000 keys, 148 parts, 145 us; now
+// 39.
+constexpr int kMergeFew = 16;  // parts up to which a thread takes all
 
 template <int D, bool kFew>
-__global__ void __launch_bounds__(kMergeThreads)
+struct Merge {
+  static constexpr int kThreads = 2 * D, kRows = kFew ? 8 : 2, kRuns = kFew ? 1 : 4;
+  static constexpr int kMost = kFew ? kMergeFew : kAttnPromptCtas, kAhead = kFew ? 2 : 8;
+  static constexpr int kBlocks = Pr<D>::kTiles * 128 / kRows;
+};
+
+template <int D, bool kFew>
+__global__ void __launch_bounds__(2 * D)
     k_prompt_merge(AttnSplit sp, int g, int splits, bf16* out, int64_t out_stride) {
-  constexpr int kPer = D / 32;  // columns of a lane
-  constexpr int kMost = kFew ? kMergeFew : kAttnPromptCtas;
-  constexpr int kLoads = (kMost + 31) / 32;
-  constexpr int kAhead = kFew ? 2 : 8, kRuns = kFew ? 1 : kMergeRuns;
-  __shared__ float s_w[kMergeWarps][kMost];
-  __shared__ float s_x[kFew ? 1 : kMergeWarps][kPer][32];
+  using M = Merge<D, kFew>;
+  constexpr int kRowThreads = D / 4 * M::kRows;
+  __shared__ float2 s_ml[M::kMost][M::kRows];
+  __shared__ float4 s_x[M::kRuns][kRowThreads];
+  __shared__ float s_l[M::kRuns][kRowThreads];
   pdl_wait();
-  const int c0 = blockIdx.x * splits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * splits, tid = threadIdx.x;
   const int4 unit = __ldcg(sp.shared + c0);
-  const int parts = unit.x, tq = 128 / g, run = warp % kRuns;
-  const int row = blockIdx.y * (kMergeWarps / kRuns) + warp / kRuns;  // of the unit's row tiles
-  const int tile = row >> 7, r = row & 127, in = r / g;
-  const int tok = tile * tq + in;
-  const bool on = parts > 0 && in < tq && tok < unit.y;
-  const auto slot = [&](int p) { return (size_t)(c0 + p) * kAttnPromptRows + row; };
-  float y[kAhead][kPer];
+  const int parts = unit.x, tq = 128 / g;
+  const int row0 = blockIdx.y * M::kRows;  // of the unit's row tiles
+  const int tile = row0 >> 7;
+  // (the block's rows are one tile's: none counts where the first does not)
+  if (parts == 0 || (row0 & 127) / g >= tq || tile * tq + (row0 & 127) / g >= unit.y) return;
+  const int i = tid % kRowThreads, run = tid / kRowThreads;
+  const int row = row0 + i % M::kRows, col = i / M::kRows;
+  const int r = row & 127, in = r / g, tok = tile * tq + in;
+  const bool on = in < tq && tok < unit.y;
+  const float4* o = reinterpret_cast<const float4*>(sp.o) +
+                    ((size_t)c0 * kAttnPromptRows + tile * 128) * (D / 4) + col * 128 + r;
+  float4 y[M::kAhead];
   const auto load = [&](int p0) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int p = p0 + k * kRuns;
-      const float* o = sp.o + slot(p) * D + lane * kPer;
-#pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        float2 v = make_float2(0.0f, 0.0f);
-        if (p < parts) v = __ldcg(reinterpret_cast<const float2*>(o + i));
-        y[k][i] = v.x;
-        y[k][i + 1] = v.y;
-      }
+    for (int k = 0; k < M::kAhead; ++k) {
+      const int p = p0 + k * M::kRuns;
+      y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (on && p < parts) y[k] = __ldcg(o + (size_t)p * (kAttnPromptRows * (D / 4)));
     }
   };
-  float x[kPer], inv = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
-  if (on) {
-    float2 ml[kLoads];
-    float m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int p = k * 32 + lane;
-      ml[k] = make_float2(-INFINITY, 0.0f);
-      if (p < parts) ml[k] = __ldcg(sp.ml + slot(p));
-    }
-    load(run);
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) m = fmaxf(m, ml[k].x);
-    m = warp_max(m);
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int p = k * 32 + lane;
-      const float f = ml[k].x == -INFINITY ? 1.0f : exp2_approx(ml[k].x - m);
-      if (p < parts) s_w[warp][p] = f;
-      l = fmaf(ml[k].y, f, l);
-    }
-    l = warp_sum(l);
-    inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-    __syncwarp();
-    for (int p0 = run;;) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int p = p0 + k * kRuns;
-        if (p < parts) {
-          const float f = s_w[warp][p];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) x[i] = fmaf(y[k][i], f, x[i]);
-        }
-      }
-      p0 += kAhead * kRuns;
-      if (p0 >= parts) break;
-      load(p0);
-    }
+  load(run);
+  for (int e = tid; e < parts * M::kRows; e += M::kThreads) {
+    const int p = e / M::kRows, k = e % M::kRows;
+    s_ml[p][k] = __ldcg(sp.ml + (size_t)(c0 + p) * kAttnPromptRows + row0 + k);
   }
-  if constexpr (!kFew) {
+  __syncthreads();
+  float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, s_ml[p][i % M::kRows].x);
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p0 = run;;) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s_x[warp][i][lane] = x[i];
+    for (int k = 0; k < M::kAhead; ++k) {
+      const int p = p0 + k * M::kRuns;
+      if (p < parts) {
+        const float2 ml = s_ml[p][i % M::kRows];
+        const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
+        l = fmaf(ml.y, f, l);
+        x = make_float4(fmaf(y[k].x, f, x.x), fmaf(y[k].y, f, x.y), fmaf(y[k].z, f, x.z),
+                        fmaf(y[k].w, f, x.w));
+      }
+    }
+    p0 += M::kAhead * M::kRuns;
+    if (p0 >= parts) break;
+    load(p0);
+  }
+  if constexpr (M::kRuns > 1) {
+    s_x[run][i] = x;
+    s_l[run][i] = l;
     __syncthreads();
     if (run > 0) return;
 #pragma unroll
-    for (int w = 1; w < kRuns; ++w)
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] += s_x[warp + w][i][lane];
+    for (int k = 1; k < M::kRuns; ++k) {
+      const float4 z = s_x[k][i];
+      l += s_l[k][i];
+      x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+    }
   }
   if (!on) return;
-  bf16* to = out + (int64_t)(unit.z + tok) * out_stride + (unit.w * g + r - in * g) * D +
-             lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<__nv_bfloat162*>(to + i) = __floats2bfloat162_rn(x[i] * inv, x[i + 1] * inv);
+  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+  uint2 v;
+  v.x = *reinterpret_cast<const uint32_t*>(&lo);
+  v.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(out + (int64_t)(unit.z + tok) * out_stride +
+                            (unit.w * g + r - in * g) * D + 4 * col) = v;
 }
 
 template <int D>
@@ -939,12 +967,12 @@ cudaError_t launch_d(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64_
       launch_pdl(k_attn_prompt<D>, dim3(heads * splits), dim3(kPThreads), pr_smem_bytes<D>(), s,
                  pdl, m.k, m.v64, a, q, q_stride, out, out_stride, sp, units, splits);
   if (e != cudaSuccess || splits == 1) return e;
-  const int rows = Pr<D>::kTiles * 128;
-  if (splits <= kMergeFew)
-    return launch_pdl(k_prompt_merge<D, true>, dim3(heads, rows / kMergeWarps),
-                      dim3(kMergeThreads), 0, s, true, sp, a.g, splits, out, out_stride);
-  return launch_pdl(k_prompt_merge<D, false>, dim3(heads, rows * kMergeRuns / kMergeWarps),
-                    dim3(kMergeThreads), 0, s, true, sp, a.g, splits, out, out_stride);
+  const auto join = [&](auto* kernel, int blocks) {
+    return launch_pdl(kernel, dim3(heads, blocks), dim3(2 * D), 0, s, true, sp, a.g, splits, out,
+                      out_stride);
+  };
+  return splits <= kMergeFew ? join(k_prompt_merge<D, true>, Merge<D, true>::kBlocks)
+                             : join(k_prompt_merge<D, false>, Merge<D, false>::kBlocks);
 }
 
 }  // namespace
