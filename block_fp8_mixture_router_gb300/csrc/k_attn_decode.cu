@@ -600,9 +600,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
 template <int D, int R, bool kSplit>
 // (the bounds ask for 128 registers: with more, two CTAs' six warps do not fit an SM)
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
-    k_attn_decode(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const AttnArgs a, const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
-                  const AttnSplit sp) {
+    k_attn_decode(const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const bf16* q,
+                  int64_t q_stride, bf16* out, int64_t out_stride, const AttnSplit sp) {
   using C = Dec<D>;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
@@ -620,7 +620,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
     u.v = seq_view(a, u.s);
     if (!u.v.ok && tid == 0) atomicOr(a.status, kAttnBadBatch);
     u.t = unit - u0;
-    if (u.t < 0 || u.t * tq >= u.v.n) return;
+    if (u.t < 0 || u.t * tq >= u.v.n) {
+      pdl_wait();  // (what ends before the kernel in front does not wait for it)
+      return;
+    }
     unit_range<R>(a, u);
     // this unit alone: a run that is exactly its tiles
     begin = (long long)u.h * (u.kt1 - u.kt0);
@@ -655,6 +658,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
       total += sm.scan[w];
     }
     if (total == 0) {
+      pdl_wait();
       if (tid == 0) sp.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }
@@ -662,6 +666,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2)
     begin = per * blockIdx.x;
     end = min(begin + per, total);
     if (begin >= end) {
+      pdl_wait();
       if (tid == 0) sp.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }

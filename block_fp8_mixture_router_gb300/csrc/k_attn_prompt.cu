@@ -21,7 +21,7 @@
 //   tiles' buffers have room for 64 keys each, although an MMA with N = 64 takes as long
 //   as one with N = 128.
 //
-// Slower at 16384 rows, 16 heads of 128 (969 us as it is): one buffer of 128 keys per row
+// Slower at 16384 rows, 16 heads of 128, beside 969 us (now 915): one buffer of 128 keys per row
 // tile, 1048 us (the row tiles fall into step, and both work while the tensor cores
 // idle); the same with the row tiles' softmax warps taking turns, 1161 us (reads of
 // tensor memory take twice as long beside running MMAs); a row's scores held in 192
@@ -707,9 +707,10 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
 
 template <int D>
 __global__ void __launch_bounds__(kPThreads, 1)
-    k_attn_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const AttnArgs a, const bf16* q, int64_t q_stride, bf16* out, int64_t out_stride,
-                  const AttnSplit sp, int units, int splits) {
+    k_attn_prompt(const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const bf16* q,
+                  int64_t q_stride, bf16* out, int64_t out_stride, const AttnSplit sp, int units,
+                  int splits) {
   using C = Pr<D>;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* sq = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
@@ -734,6 +735,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   w.tok0 = (unit - u0) * per;
   const bool none = unit < u0 || w.tok0 >= w.v.n;
   if (none) {
+    pdl_wait();  // (what ends before the kernel in front does not wait for it)
     if (splits > 1 && tid == 0) sp.shared[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
@@ -868,18 +870,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
 // columns of a row; kRuns of them take interleaved shares of the parts and are added in
 // order.  Bound by the latency of its loads, so the sums of kAhead parts are on their way
 // at once: one part after the other made 128 rows over 50000 keys, 148 parts, 145 us; now
-// 39.
+// 30.
 constexpr int kMergeFew = 16;  // parts up to which a thread takes all
 
 template <int D, bool kFew>
 struct Merge {
-  static constexpr int kThreads = 2 * D, kRows = kFew ? 8 : 2, kRuns = kFew ? 1 : 4;
+  static constexpr int kRows = kFew ? 8 : 4, kRuns = kFew ? 1 : 4;
+  static constexpr int kThreads = D / 4 * kRows * kRuns;
   static constexpr int kMost = kFew ? kMergeFew : kAttnPromptCtas, kAhead = kFew ? 2 : 8;
   static constexpr int kBlocks = Pr<D>::kTiles * 128 / kRows;
 };
 
 template <int D, bool kFew>
-__global__ void __launch_bounds__(2 * D)
+__global__ void __launch_bounds__(kFew ? 2 * D : 4 * D)
     k_prompt_merge(AttnSplit sp, int g, int splits, bf16* out, int64_t out_stride) {
   using M = Merge<D, kFew>;
   constexpr int kRowThreads = D / 4 * M::kRows;
@@ -967,12 +970,12 @@ cudaError_t launch_d(const AttnArgs& a, const AttnMaps& m, const bf16* q, int64_
       launch_pdl(k_attn_prompt<D>, dim3(heads * splits), dim3(kPThreads), pr_smem_bytes<D>(), s,
                  pdl, m.k, m.v64, a, q, q_stride, out, out_stride, sp, units, splits);
   if (e != cudaSuccess || splits == 1) return e;
-  const auto join = [&](auto* kernel, int blocks) {
-    return launch_pdl(kernel, dim3(heads, blocks), dim3(2 * D), 0, s, true, sp, a.g, splits, out,
+  const auto join = [&](auto* kernel, int blocks, int threads) {
+    return launch_pdl(kernel, dim3(heads, blocks), dim3(threads), 0, s, true, sp, a.g, splits, out,
                       out_stride);
   };
-  return splits <= kMergeFew ? join(k_prompt_merge<D, true>, Merge<D, true>::kBlocks)
-                             : join(k_prompt_merge<D, false>, Merge<D, false>::kBlocks);
+  return splits <= kMergeFew ? join(k_prompt_merge<D, true>, Merge<D, true>::kBlocks, 2 * D)
+                             : join(k_prompt_merge<D, false>, Merge<D, false>::kBlocks, 4 * D);
 }
 
 }  // namespace
