@@ -23,6 +23,12 @@
 // A CTA has four softmax warps (a thread per key of the tile), a warp that issues
 // the MMAs and one that keeps a ring of key tiles (128 keys and their values, 32 KB
 // at head_dim 128) filled by TMA; two CTAs share an SM (one at head_dim 256).
+//
+// Measured: 64 rows of 32 heads over 590 MB of codes, 104 us (5.7 TB/s, where a plain
+// copy reaches 6.8); one row of 16 heads over 262143 tokens, 50 us (5.4 TB/s); one row
+// over 4096 tokens, 9.0 us: 5 us of dependent steps in a CTA (finding its tiles 1.2,
+// queries and first tile 1.6, softmax 1.2, products and the result 1.1), the rest launches
+// and the join.
 #include "attn_tc.cuh"
 
 namespace moe {

@@ -560,7 +560,8 @@ int moe_kv_append(moe_attn* ctx, const moe_kv_cache* cache, const void* k, int64
  * with row strides in values (multiples of 8), 16-byte aligned, not overlapping.
  * A row that sees a NaN key or value, or holds one itself, is NaN; unseen tokens
  * reach no row, whatever they hold.  The softmax and every sum run in fp32; the
- * queries are taken to 2^-17 of the head's largest value, the weights to 11 bits.  Results are bitwise identical from run to run.  Asynchronous.
+ * queries are taken to 2^-17 of the head's largest value, the weights to 11 bits.
+ * Results are bitwise identical from run to run.  Asynchronous.
  * Defined by: commit "the Drama 3 text backbone on CUDA" (full attention with
  * shared key heads, for prompts and single tokens); the cache held in 8 bits is
  * this library's. */

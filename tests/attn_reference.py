@@ -69,7 +69,7 @@ def rope(shape, x, positions, gamma=None, eps=1e-6):
     Tolerance: the rounding to bf16; the norm's fp32 sum and products (relative
     D + 8 half-steps of fp32, far below 2^-14 of the value for D <= 256); the
     angle (2^-25 of a turn, 2 pi times that in radians) and the two functions
-    (2^-21 each), relative to the pair's magnitudes."""
+    (2^-21 each at most), relative to the pair's magnitudes."""
     x = x.double().cpu()
     D = x.shape[-1]
     if gamma is not None:
