@@ -281,6 +281,37 @@ def test_attention_long(dev, seqs):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("D,rows", [(64, 12), (64, 20), (128, 21), (128, 31), (256, 45), (256, 60)])
+@pytest.mark.parametrize("window", [0, 130])
+def test_attention_few_row_tiles(dev, D, rows, window):
+    """Tiles of 16 rows (three tokens of five heads) up to the number at which the prompt
+    kernel takes over, and the one behind it, with keys shared out either way."""
+    shape = m.AttnShape(q_heads=5, kv_heads=1, head_dim=D, page_tokens=32, rotary_dim=0,
+                        window=window)
+    for ctx in (rows, rows + 1, 1000):
+        Case(dev, shape, [(rows, ctx)], seed=rows + ctx).check()
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [40, 150])
+def test_attention_long_other_widths(dev, D, rows):
+    """More parts of a row block than one thread joins, at the other head widths."""
+    shape = m.AttnShape(q_heads=14, kv_heads=2, head_dim=D, page_tokens=128, rotary_dim=0)
+    Case(dev, shape, [(rows, 7000)], seed=D + rows).check()
+
+
+@pytest.mark.parametrize("window", [300, 0x7FFEFFFF, 0x7FFFFFFF])
+def test_attention_windows_past_all_tokens(dev, window):
+    """A window wider than the cache sees what no window sees, bit for bit."""
+    kw = dict(q_heads=4, kv_heads=2, head_dim=128, page_tokens=64, rotary_dim=0)
+    for seqs in ([(1, 200), (3, 2)], [(200, 290)]):
+        a = Case(dev, m.AttnShape(**kw), seqs, seed=3)
+        b = Case(dev, m.AttnShape(window=window, **kw), seqs, seed=3)
+        q = a.q()
+        x, y = a.check(q), b.check(q)
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
 @pytest.mark.parametrize("hints", [dict(), dict(max_seq_rows=1, max_kv_len=1),
                                    dict(max_seq_rows=60000, max_kv_len=1 << 30)])
 def test_attention_hints_only_size_the_launch(dev, hints):
