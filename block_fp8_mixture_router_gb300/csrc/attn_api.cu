@@ -239,8 +239,9 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const int tq = tile_rows / a.g;
   const long long seq_tiles = (seq_rows + tq - 1) / tq;
   const long long units = (long long)b->rows / tq + b->n_seqs;  // per key head, at most
-  const bool prompt = (long long)seq_rows * a.g > kDecTileRows &&
-                      std::min(units, seq_tiles * b->n_seqs) * a.Hkv > D / kPromptTiles;
+  const long long row_tiles = std::min(units, seq_tiles * b->n_seqs) * a.Hkv;
+  const bool prompt =
+      (long long)seq_rows * a.g > kDecTileRows && row_tiles > D / kPromptTiles;
   AttnMaps maps;
   if (!make_attn_maps(&maps, a, D, prompt)) return MOE_ERR_CUDA;
   if (prompt) {
@@ -255,19 +256,25 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
                ? MOE_OK
                : MOE_ERR_CUDA;
   }
-  // Few row tiles: the key tiles of all of them in equal runs, at least two (256 keys) to
-  // a CTA (one row over 4096 keys: 8.9 us, with one tile to a CTA 9.5).  Many: a CTA per
-  // row tile.
-  const bool split = units <= 2048 && seq_tiles <= 64;
+  // The key tiles of all row tiles in equal runs, at least two (256 keys) to a CTA (one row
+  // over 4096 keys: 9.0 us, with one tile to a CTA 9.5): balanced whatever the lengths, but
+  // the CTAs find their runs and parts are joined.  So a CTA to a row tile where that fills
+  // the GPU about as well: short sequences, and no more than two for each place.
+  // Measured, sequences of one row x key heads of 128, in us, runs / a CTA each:
+  //   32 x 1 over 100 keys 8.9 / 7.4, 1000 keys 12.1 / 13.4;
+  //   32 x 4 over 100 12.8 / 7.9, 1000 15.7 / 15.7, ragged 14.9 / 13.4;
+  //   128 x 4 over 100 14.8 / 15.7, 1000 37.6 / 34.6, ragged 38.0 / 29.4;
+  //   1024 x 1 over 100 31 / 44, 1000 69 / 74; 4000 x 4 over 1000 678 / 1256.
+  long long span = keys;
+  if (a.window) span = std::min<long long>(span, (long long)a.window + tq + kAttnKeys);
+  const long long unit_tiles = (span + kAttnKeys - 1) / kAttnKeys, places = c->dec_slots;
+  const bool each = unit_tiles <= 8 && (row_tiles <= places
+                                            ? unit_tiles * (places - row_tiles) <= 5 * places
+                                            : unit_tiles > 1 && row_tiles <= 2 * places);
   long long grid = units * a.Hkv;
-  if (split) {
-    long long span = keys;
-    if (a.window) span = std::min<long long>(span, (long long)a.window + tq + kAttnKeys);
-    const long long tiles = units * a.Hkv * ((span + kAttnKeys - 1) / kAttnKeys);
-    grid = std::max<long long>(1, std::min<long long>((tiles + 1) / 2, c->dec_slots));
-  }
+  if (!each) grid = std::max<long long>(1, std::min((grid * unit_tiles + 1) / 2, places));
   return launch_attn_decode(D, tile_rows, a, maps, q, q_stride, out, out_stride, c->split,
-                            (int)grid, split, pdl, s) == cudaSuccess
+                            (int)grid, !each, pdl, s) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }

@@ -300,6 +300,16 @@ def test_attention_long_other_widths(dev, D, rows):
     Case(dev, shape, [(rows, 7000)], seed=D + rows).check()
 
 
+@pytest.mark.parametrize("n,most", [(40, 100), (130, 1000), (300, 30), (700, 900), (4000, 40)])
+def test_attention_many_sequences(dev, n, most):
+    """A row of each of many sequences, lengths from none to `most`: as runs of key tiles and
+    as a CTA to each, whichever the sizes call for."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, most + 1, (n,), generator=g).tolist()
+    shape = m.AttnShape(q_heads=4, kv_heads=2, head_dim=64, page_tokens=16, rotary_dim=0)
+    Case(dev, shape, [(1, k) for k in lens], seed=n).check()
+
+
 @pytest.mark.parametrize("window", [300, 0x7FFEFFFF, 0x7FFFFFFF])
 def test_attention_windows_past_all_tokens(dev, window):
     """A window wider than the cache sees what no window sees, bit for bit."""
