@@ -245,12 +245,17 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   AttnMaps maps;
   if (!make_attn_maps(&maps, a, D, prompt)) return MOE_ERR_CUDA;
   if (prompt) {
-    const long long units = b->rows / attn_prompt_tokens(D, a.g) + (long long)b->n_seqs;
-    const long long heads = units * a.Hkv, tiles = (keys + 127) / 128;
-    long long splits = 1;
-    if (heads < c->sm_count && heads <= kAttnPromptCtas)
-      splits = std::max<long long>(
-          1, std::min<long long>(std::min(c->sm_count, kAttnPromptCtas) / heads, tiles / 2));
+    // Row blocks fewer than the SMs share their keys out, at least two tiles to a CTA.  How
+    // many there are follows from the most rows of a sequence; the grid has room for more.
+    // (Three sequences of 64 rows over 20000 keys, 16 heads of 128 to 4: 67 us with shares
+    // after the grid's count, 47 after this one.)
+    const int per = attn_prompt_tokens(D, a.g);
+    const long long units = b->rows / per + (long long)b->n_seqs;
+    const long long heads = std::min(units, ((long long)seq_rows + per - 1) / per * b->n_seqs) *
+                            a.Hkv;
+    const long long splits = std::max<long long>(
+        1, std::min({std::min(c->sm_count, kAttnPromptParts) / heads,
+                     kAttnPromptCtas / (units * a.Hkv), (keys + 127) / 128 / 2}));
     return launch_attn_prompt(D, a, maps, q, q_stride, out, out_stride, c->split, (int)units,
                               (int)splits, pdl, s) == cudaSuccess
                ? MOE_OK

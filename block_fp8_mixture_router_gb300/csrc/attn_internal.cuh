@@ -56,7 +56,9 @@ struct AttnSplit {
 };
 constexpr int kAttnSlotRows = 16;
 constexpr int kAttnPromptRows = 256;  // rows of a slot of the prompt kernel
-constexpr int kAttnPromptCtas = 160;  // most CTAs of a launch of it that splits keys
+constexpr int kAttnPromptCtas = 320;  // most CTAs of a launch of it that splits keys, with
+                                      // those that find no rows
+constexpr int kAttnPromptParts = 160; // most parts of a row block's keys
 constexpr int kAttnMaxCtas = 512;  // CTAs of a launch that splits units
 
 cudaError_t launch_rope(int D, const bf16* x, int64_t x_stride, int heads, const int* positions,

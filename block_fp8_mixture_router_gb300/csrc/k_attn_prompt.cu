@@ -883,7 +883,7 @@ template <int D, bool kFew>
 struct Merge {
   static constexpr int kRows = kFew ? 8 : 4, kRuns = kFew ? 1 : 4;
   static constexpr int kThreads = D / 4 * kRows * kRuns;
-  static constexpr int kMost = kFew ? kMergeFew : kAttnPromptCtas, kAhead = kFew ? 2 : 8;
+  static constexpr int kMost = kFew ? kMergeFew : kAttnPromptParts, kAhead = kFew ? 2 : 8;
   static constexpr int kBlocks = Pr<D>::kTiles * 128 / kRows;
 };
 
