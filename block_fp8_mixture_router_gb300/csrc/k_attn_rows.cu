@@ -13,6 +13,8 @@
 // run in place.  Measured: 20 heads of 128 of 16384 rows rotated in 32.3 us (5.2 TB/s,
 // where a plain copy reaches 6.8), of one row in 3.2 us; 10600 rows of keys and values of
 // 4 heads in three prompts appended in 10.7 us, a row for each of 64 sequences in 5.7.
+#include <algorithm>
+
 #include "attn_device.cuh"
 
 namespace moe {
@@ -189,7 +191,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 // while the block agrees on the page's scale, so they are read once.
 template <int D, int kMost, bool kStep>
 __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs& p, int unit,
-                                            int h, bool is_v, float* swap) {
+                                            int h, bool is_v, float2* table, float* swap) {
   using L = Lanes<D>;
   __shared__ float s_max[kRowThreads / 32];
   const int P = 1 << a.page_shift;
@@ -239,11 +241,11 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
         const int pos = lo + min(k * L::kRows + sub, m - 1);
         if (p.k_gamma) norm_head<D>(x, p.k_gamma, p.eps, c);
         // a row's sines by its lanes, which are one warp's
-        __shared__ float2 s_cs[kRowThreads / L::kPer][D / 2];
+        float2* cs = table + sub * (D / 2);
         __syncwarp();
-        for (int i = c; i < p.rope.rot >> 1; i += L::kPer) s_cs[sub][i] = rope_cs(p.rope, i, pos);
+        for (int i = c; i < p.rope.rot >> 1; i += L::kPer) cs[i] = rope_cs(p.rope, i, pos);
         __syncwarp();
-        rotate_head<D>(x, p.rope, c, swap, [&](int i) { return s_cs[sub][i]; });
+        rotate_head<D>(x, p.rope, c, swap, [&](int i) { return cs[i]; });
         raw[k] = pack8(x);
         unpack8(raw[k], x);
       }
@@ -310,16 +312,16 @@ __device__ __forceinline__ void append_unit(const AttnArgs& a, const AppendArgs&
 template <int D, int kMost, bool kStep>
 __global__ void __launch_bounds__(kRowThreads, kMost <= 4 ? 4 : kMost <= 8 ? 3 : 2)
     k_append(AttnArgs a, AppendArgs p, int append_blocks, int block_rows) {
+  extern __shared__ float2 s_table[];  // sines of a block's rows, of queries or of keys
   __shared__ float s_swap[kStep ? kRowThreads * 8 : 1];
   pdl_trigger();
   if ((int)blockIdx.x < append_blocks) {
     const int b = blockIdx.x;
     const int uh = b >> 1;
-    append_unit<D, kMost, kStep>(a, p, uh / a.Hkv, uh % a.Hkv, b & 1, s_swap);
+    append_unit<D, kMost, kStep>(a, p, uh / a.Hkv, uh % a.Hkv, b & 1, s_table, s_swap);
     return;
   }
   if constexpr (kStep) {
-    extern __shared__ float2 s_table[];
     __shared__ int s_start[kSmemSeqs + 1];
     const int row0 = (blockIdx.x - append_blocks) * block_rows;
     const int nr = min(block_rows, a.rows - row0);
@@ -386,9 +388,9 @@ cudaError_t append_dm(const AttnArgs& a, const AppendArgs& p, cudaStream_t s) {
   } else {
     const int br = rope_block_rows<D>(a.Hq);
     const int q_blocks = (a.rows + br - 1) / br;
-    k_append<D, kMost, true><<<blocks + q_blocks, kRowThreads,
-                               (size_t)br * (p.rope.rot / 2) * sizeof(float2), s>>>(a, p, blocks,
-                                                                                    br);
+    const int table = std::max(br * (p.rope.rot / 2), Lanes<D>::kRows * (D / 2));
+    k_append<D, kMost, true><<<blocks + q_blocks, kRowThreads, table * sizeof(float2), s>>>(
+        a, p, blocks, br);
   }
   return cudaGetLastError();
 }

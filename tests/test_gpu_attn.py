@@ -475,6 +475,24 @@ def test_step_is_its_parts(dev, kw, seqs, norm):
     assert a.net.device_status() == m.MOE_OK
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_step_of_one_head_rotated_whole(dev, D, layout):
+    """One query head: a block of the prologue holds the sines of as many rows as it can."""
+    shape = m.AttnShape(q_heads=1, kv_heads=1, head_dim=D, page_tokens=32, rotary_dim=D,
+                        rope_layout=layout)
+    for seqs in ([(1, 40)], [(130, 150), (70, 400), (1, 1)]):
+        a, b = Case(dev, shape, seqs, seed=41), Case(dev, shape, seqs, seed=41)
+        qkv = a.randn(a.rows, 3, D)
+        out = a.net.step(qkv, a.cache, a.batch)
+        pos = torch.cat([torch.arange(k - n, k) for n, k in seqs]).to(torch.int32).to(dev)
+        q, k = b.net.rope(qkv[:, :1], pos), b.net.rope(qkv[:, 1:2], pos)
+        b.net.append(k, qkv[:, 2:], b.cache, b.batch)
+        assert torch.equal(a.codes["k"], b.codes["k"])
+        check_close(out, *b.expected(q))
+        assert a.net.device_status() == m.MOE_OK
+
+
 # ---- refusals ----------------------------------------------------------------------
 
 def test_refusals(dev):
