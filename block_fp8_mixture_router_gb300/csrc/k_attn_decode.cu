@@ -284,6 +284,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
         for (int g = sub * box_rows / 16; g < (sub + 1) * box_rows / 16; ++g)
           sm.meta[r.stage][g] = make_float2(ks, vs);
       const int top = __reduce_max_sync(0xffffffffu, mine && on ? ordered(vs) : 0);
+      __syncwarp();  // all lanes' scales before lane 0's arrival
       if (lane == 0) {
         sm.tile_top[r.stage] = from_ordered(top);
         tc::mbar_arrive_expect_tx(&sm.full[r.stage], boxes * box_rows * D * 2);
