@@ -89,8 +89,8 @@ bool supported(const moe_attn_config* c) {
 
 // Byte sizes of everything a context allocates, in order.
 struct Sizes {
-  size_t turns, q, part_o, part_ml, shared, status;
-  size_t total() const { return turns + q + part_o + part_ml + shared + status; }
+  size_t turns, q, part_o, part_sums, shared, status;
+  size_t total() const { return turns + q + part_o + part_sums + shared + status; }
 };
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -104,7 +104,7 @@ Sizes sizes_of(const moe_attn_config* c) {
   const size_t rows =
       std::max(slots * kAttnSlotRows, (size_t)kAttnPromptCtas * kAttnPromptRows);
   s.part_o = up256(rows * c->head_dim * 4);
-  s.part_ml = up256(rows * 8);
+  s.part_sums = up256(rows * 16);
   s.shared = up256((size_t)kAttnMaxCtas * 16);
   s.status = 256;
   return s;
@@ -324,7 +324,7 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out) {
   while ((1 << c->page_shift) < cfg->page_tokens) ++c->page_shift;
   bool ok = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, device) ==
             cudaSuccess;
-  const size_t bytes[6] = {z.turns, z.q, z.part_o, z.part_ml, z.shared, z.status};
+  const size_t bytes[6] = {z.turns, z.q, z.part_o, z.part_sums, z.shared, z.status};
   void* p[6] = {};
   try {
     c->allocs.reserve(6);
@@ -336,7 +336,7 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out) {
       c->turns = static_cast<unsigned long long*>(p[0]);
       c->q = static_cast<bf16*>(p[1]);
       c->split.o = static_cast<float*>(p[2]);
-      c->split.ml = static_cast<float2*>(p[3]);
+      c->split.sums = static_cast<float4*>(p[3]);
       c->split.shared = static_cast<int4*>(p[4]);
       c->status = static_cast<int*>(p[5]);
       const std::vector<unsigned long long> t = turn_table(*cfg);

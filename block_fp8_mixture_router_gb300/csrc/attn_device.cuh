@@ -121,6 +121,13 @@ __device__ __forceinline__ bool is_finite(float x) {
   return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
 
+// A value scale as a number between the append's smallest and largest, so that its logarithm
+// is one too.
+__device__ __forceinline__ float clamp_scale(float x) {
+  return fminf(fmaxf(x, __uint_as_float((uint32_t)(127 + kScaleMinExp) << 23)),
+               __uint_as_float((uint32_t)(127 + kScaleMaxExp) << 23));
+}
+
 // 0x80 in every byte of w that is an e4m3 NaN code (0x7F or 0xFF).
 __device__ __forceinline__ uint32_t e4m3_nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;

@@ -9,7 +9,8 @@ constexpr int kAttnMaxGroup = 16;     // query heads of one key head
 constexpr int kAttnMaxSeqs = 4096;
 constexpr int kAttnMaxTokens = 0x7FFF0000;  // positions and a tile behind them fit an int
 constexpr int kAttnKeys = 128;        // keys of a tile of the decode kernel
-constexpr int kScaleMinExp = -100;    // the smallest block scale is 2^-100
+constexpr int kScaleMinExp = -100;    // the smallest block scale is 2^-100, and 448 x the
+constexpr int kScaleMaxExp = 120;     // largest, 2^120, holds every bf16 value
 
 // Device status word bits.
 constexpr int kAttnTimeout = 1;
@@ -50,7 +51,8 @@ struct RopeArgs {
 struct AttnSplit {
   float* o;        // [slots][kAttnSlotRows][D]: weighted sums of the values (the prompt
                    // kernel's: [CTAs][row tiles][D / 4][128 rows][4])
-  float2* ml;      // [slots][kAttnSlotRows]: the rows' references (log2) and sums
+  float4* sums;    // [slots][kAttnSlotRows]: the rows' references (log2) for score + log2(value
+                   // scale) and for the score, and the sum of 2^(score - the latter)
   int4* shared;    // [CTAs]: the unit that begins in this CTA and goes on in others:
                    // its parts (0: none), rows, first row, key head
 };

@@ -7,6 +7,18 @@
 // in one pass over the keys with a running maximum m and sum.  A row tile is R
 // rows (8 or 16): the g query heads of a key head times R/g tokens.
 //
+// A value is code c x its page's scale 2^lambda, and what the tensor cores sum are codes,
+// weighted by 2^(s_j + lambda_j - r) against a reference r of their own, the running maximum
+// of s_j + lambda_j over the keys that the row sees:
+//
+//   out = 2^(r - m) sum_j 2^(s_j + lambda_j - r) c_j / sum_j 2^(s_j - m).
+//
+// Each row so has weights of its own range, whatever scales other rows' keys have and
+// however far apart its own are.  The lower sum takes its terms from the weights, times
+// 2^(r - m - lambda), so that a score costs one exponential; where that factor passes
+// 2^kSpread, keys that count could have weights below fp32's range, and the terms get
+// exponentials of their own.
+//
 // The cache's bytes bound it, so the codes go to the tensor cores as they are
 // stored, keys and values as the operand with M = 128 and the few rows as N:
 //
@@ -42,8 +54,14 @@ constexpr int kTmaWarp = 5;
 // A weight is stored as p x 2^12, and p taken against a reference that may lag the
 // row's maximum by kLag powers of two: sums are only scaled again when a score
 // outgrows that, and 2^(12 + kLag) is where e5m2's last binade begins.
-constexpr float kPShift = 4096.0f;
+constexpr float kShiftLog = 12.0f;
 constexpr float kLag = 3.0f;
+// The sum of 2^(s - m) is fp32 and takes a lag of kSumLag.  s + lambda is within kLag of r, so
+// s - m can only pass that for a page with r - m - lambda above kSpread, and only then
+// are the scores held against m at all.  A weight below 2^-126 then is a term below
+// 2^(kSpread - 126).  (What a row does depends on its own scores and scales alone.)
+constexpr float kSumLag = 64.0f;
+constexpr float kSpread = kSumLag - kLag - 1.0f;
 constexpr int kParts = 4;
 
 template <int D>
@@ -87,13 +105,17 @@ struct DecSmem {
   uint8_t q[32 * D];       // query parts: [2R rows][D] in panels of kRowBytes, swizzled
   alignas(32) float fac[16];  // a row's score factor, but for the key's scale
   int pos[16];             // a row's position
-  alignas(32) float m[16];    // a row's reference
-  alignas(32) float base[16]; // what a row's scores are reduced by: m, or 0 where it is -inf
-  alignas(32) float alpha[16];  // what a new reference multiplies the row's sums by
-  int top[4][16];          // the warps' row maxima, as ordered integers
+  alignas(32) float ref[16];  // a row's reference for score + log2(value scale), r above
+  alignas(32) float m[16];    // and for the score
+  // what is added to a row's scores, 12 - r or 12 where r is -inf, and 2^(r - m), or 0, over the
+  // weights' 2^12
+  alignas(16) float2 base[16];
+  alignas(16) float2 alpha[16];  // what new references multiply its two sums by
+  float gap[16];                 // r - m, or -inf
+  float spread;                  // the largest of them
+  int top[2][4][16];       // the warps' row maxima (r's and m's), as ordered integers
   float l[4][16];          // the warps' row sums
   float2 meta[Dec<D>::kStages][kAttnKeys / 16];  // scales of 16 keys and their values
-  float tile_top[Dec<D>::kStages];               // the largest value scale of a stage
   uint64_t full[Dec<D>::kStages], empty[Dec<D>::kStages];
   uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done;
   uint32_t tmem;
@@ -216,8 +238,8 @@ __device__ __forceinline__ void stage_queries(const AttnArgs& a, const Unit& u, 
       if (c == 0) {
         sm.fac[r] = f;
         sm.pos[r] = u.v.first + u.tok0 + tok;
-        sm.m[r] = -INFINITY;
-        sm.base[r] = 0.0f;
+        sm.ref[r] = sm.m[r] = sm.gap[r] = -INFINITY;
+        sm.base[r] = make_float2(kShiftLog, 0.0f);
       }
     }
   }
@@ -252,7 +274,7 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
     const int key = kt0 * kAttnKeys + lane * box_rows;
     bool on = lane < tiles * per_tile && key < u.hi && key + box_rows > u.lo;
     int page = 0;
-    float ks = -1.0f, vs = 0.0f;  // keys of a page that is not copied count as absent
+    float ks = -1.0f, vs = 1.0f;  // keys of a page that is not copied count as absent
     if (on) {
       page = page_at(a, u.s, key >> a.page_shift);
       if (page < 0) {
@@ -283,12 +305,8 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const Unit& u, int t0
       if (mine)
         for (int g = sub * box_rows / 16; g < (sub + 1) * box_rows / 16; ++g)
           sm.meta[r.stage][g] = make_float2(ks, vs);
-      const int top = __reduce_max_sync(0xffffffffu, mine && on ? ordered(vs) : 0);
       __syncwarp();  // all lanes' scales before lane 0's arrival
-      if (lane == 0) {
-        sm.tile_top[r.stage] = from_ordered(top);
-        tc::mbar_arrive_expect_tx(&sm.full[r.stage], boxes * box_rows * D * 2);
-      }
+      if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[r.stage], boxes * box_rows * D * 2);
       r.next(C::kStages);
     }
   }
@@ -384,7 +402,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
   float l[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) l[r] = 0.0f;
-  float vref = 0x1p-126f, up = 0.0f;  // values are held as multiples of vref; any page replaces it
+  float spread = -INFINITY;
   // where this thread's weight goes in a part's row n: row * 128 + the swizzled key
   uint8_t* const pw = sm.p + (tid & 15);
   const int col = (tid >> 4) << 4;
@@ -392,7 +410,8 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
   for (int kt = t0; kt < t1; ++kt) {
     tc::wait_bounded(&sm.full[ph.ring.stage], ph.ring.phase, abort, a.status);
     const float2 sc = sm.meta[ph.ring.stage][tid >> 4];
-    const float top = sm.tile_top[ph.ring.stage];
+    float lv;  // (a scale of a cache that other code filled may be anything)
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(lv) : "f"(clamp_scale(sc.y)));
     const int key = kt * kAttnKeys + tid;
     const bool live = key >= u.lo && key < u.hi && sc.x >= 0.0f;
     const bool edge = kt * kAttnKeys + kAttnKeys - 1 > pos0 || kt * kAttnKeys < u.lo ||
@@ -433,52 +452,67 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
     tc::wait_bounded(&sm.s_full[ph.s.stage], ph.s.phase, abort, a.status);
     tc::fence_after_sync();
     __syncwarp();
-    float s[R];
-    float peak = -INFINITY;  // largest of the scores over their rows' references
+    float s[R];              // s + lambda
+    float peak = -INFINITY;  // the largest of them over their rows' references
 #pragma unroll
     for (int h = 0; h < R; h += 8) {
       uint32_t hi[8], lo[8];
       tc::tmem_ld_async(tmem + ph.s.stage * 32 + h, hi);
       tc::tmem_ld_async(tmem + ph.s.stage * 32 + R + h, lo);
-      float fac[8], m[8];
+      float fac[8], ref[8];
       load8(sm.fac + h, fac);
-      load8(sm.m + h, m);
+      load8(sm.ref + h, ref);
       tc::wait_ld();
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        s[h + r] = (__uint_as_float(hi[r]) + __uint_as_float(lo[r])) * (fac[r] * sc.x);
-        if (seen & (1u << (h + r))) peak = fmaxf(peak, s[h + r] - m[r]);
+        s[h + r] = fmaf(__uint_as_float(hi[r]) + __uint_as_float(lo[r]), fac[r] * sc.x, lv);
+        if (seen & (1u << (h + r))) peak = fmaxf(peak, s[h + r] - ref[r]);
       }
     }
+    bool outgrown = peak > kLag;
+    if (spread - lv > kSpread)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (seen & (1u << r)) outgrown |= s[r] - lv - sm.m[r] > kSumLag;
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&sm.s_empty[ph.s.stage]);
     ph.s.next(2);
-    if (softmax_any(peak > kLag || top > vref)) {
-      // new references: the rows' running maxima, and the largest value scale so far
+    if (softmax_any(outgrown)) {
+      // new references, the running maxima, for the rows that have outgrown theirs
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         // (a NaN score raises nothing)
         const float x = (seen & (1u << r)) && s[r] == s[r] ? s[r] : -INFINITY;
         const int t = __reduce_max_sync(0xffffffffu, ordered(x));
-        if (lane == 0) sm.top[warp][r] = t;
+        const int u = __reduce_max_sync(0xffffffffu, ordered(x - lv));
+        if (lane == 0) sm.top[0][warp][r] = t, sm.top[1][warp][r] = u;
       }
       softmax_sync();
-      const float vf = top > vref ? __fdiv_rn(vref, top) : 1.0f;
-      vref = fmaxf(vref, top);
-      up = __fdiv_rn(kPShift, vref);
       if (tid < R) {
-        const float m = sm.m[tid];
-        const float t = from_ordered(max(max(sm.top[0][tid], sm.top[1][tid]),
-                                         max(sm.top[2][tid], sm.top[3][tid])));
-        const float m_new = fmaxf(m, t);
-        sm.alpha[tid] = m_new == -INFINITY ? 1.0f : exp2_approx(m - m_new);
-        sm.m[tid] = m_new;
-        sm.base[tid] = m_new == -INFINITY ? 0.0f : m_new;
+        const auto top = [&](int i) {
+          return from_ordered(max(max(sm.top[i][0][tid], sm.top[i][1][tid]),
+                                  max(sm.top[i][2][tid], sm.top[i][3][tid])));
+        };
+        float ref = sm.ref[tid], m = sm.m[tid];
+        float2 alpha = make_float2(1.0f, 1.0f);
+        const float ref_top = top(0), m_top = top(1);
+        if (ref_top - ref > kLag || m_top - m > kSumLag) {
+          const float ref_new = fmaxf(ref, ref_top), m_new = fmaxf(m, m_top);
+          alpha = make_float2(exp2_approx(ref - ref_new), exp2_approx(m - m_new));
+          sm.ref[tid] = ref = ref_new;
+          sm.m[tid] = m = m_new;
+          sm.base[tid] = make_float2(kShiftLog - ref, exp2_approx(ref - m - kShiftLog));
+          sm.gap[tid] = ref - m;
+        }
+        sm.alpha[tid] = alpha;
+        const int most = __reduce_max_sync((1u << R) - 1, ordered(sm.gap[tid]));
+        if (tid == 0) sm.spread = from_ordered(most);
       }
       softmax_sync();
+      spread = sm.spread;
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] *= sm.alpha[r];
+      for (int r = 0; r < R; ++r) l[r] *= sm.alpha[r].y;
       if (kt > t0) {
         tc::wait_bounded(&sm.pv_done, ph.pv ^ 1, abort, a.status);
         tc::fence_after_sync();
@@ -493,7 +527,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
             tc::wait_ld();
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              const float f = sm.alpha[r] * vf;
+              const float f = sm.alpha[r].x;
               x[r] = __float_as_uint(__uint_as_float(x[r]) * f);
               x[R + r] = __float_as_uint(__uint_as_float(x[R + r]) * f);
             }
@@ -504,27 +538,35 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
       }
     }
     // the weights carry the page's scale in their exponent, and the sum of them is
-    // freed of it again; a page below 2^-72 of the largest adds no value that counts
-    const float w = fmaxf(sc.y * up, 0x1p-60f);
-    float lw, w_inv;
-    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(lw) : "f"(w));
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(w_inv) : "f"(w));
-    if (!live) w_inv = 0.0f;
+    // freed of it again
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(clamp_scale(sc.y)));
+    if (spread - lv > kSpread) {  // of some row at least: the sums here, all rows' in its way
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (seen & (1u << r)) {
+          const float2 base = sm.base[r];
+          l[r] = sm.gap[r] - lv > kSpread
+                     ? l[r] + exp2_approx(s[r] - lv - sm.m[r])
+                     : fmaf(exp2_approx(s[r] + base.x), inv * base.y, l[r]);
+        }
+      inv = 0.0f;
+    }
     // the parts' rows are free once the last tile's values are done
     if (kt > t0) tc::wait_bounded(&sm.pv_done, ph.pv ^ 1, abort, a.status);
     ph.pv ^= 1;
 #pragma unroll
     for (int r = 0; r < R; r += 2) {
-      const float2 base = *reinterpret_cast<const float2*>(sm.base + r);
+      const float4 base = *reinterpret_cast<const float4*>(sm.base + r);
       float rest[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float p = exp2_approx(s[r + k] + (lw - (k ? base.y : base.x)));
+        float p = exp2_approx(s[r + k] + (k ? base.z : base.x));
         if (edge) {
           if (poison) p = __int_as_float(0x7FFFFFFF);
           if (!(seen & (1u << (r + k)))) p = 0.0f;
         }
-        l[r + k] = fmaf(p, w_inv, l[r + k]);
+        l[r + k] = fmaf(p, inv * (k ? base.w : base.y), l[r + k]);
         rest[k] = p;
       }
       // three bits from the top, then three of the rest each time; the first part leaves
@@ -578,16 +620,15 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
         if (r < u.rows) {
           const float o = (__uint_as_float(x[r]) + __uint_as_float(x[R + r]) * 0x1p-3f +
                            __uint_as_float(y[r]) * 0x1p-6f +
-                           __uint_as_float(y[R + r]) * 0x1p-9f) *
-                          (vref * (1.0f / kPShift));
+                           __uint_as_float(y[R + r]) * 0x1p-9f);
           if (whole) {
             const float sum = sm.l[0][r] + sm.l[1][r] + sm.l[2][r] + sm.l[3][r];
-            const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+            const float inv = sum == 0.0f ? 0.0f : __fdividef(sm.base[r].y, sum);
             const int tok = r / a.g;
             out[(int64_t)(u.v.row0 + u.tok0 + tok) * out_stride + (u.h * a.g + r - tok * a.g) * D +
                 d] = __float2bfloat16_rn(o * inv);
           } else {
-            __stcg(sp.o + ((size_t)slot * kAttnSlotRows + r) * D + d, o);
+            __stcg(sp.o + ((size_t)slot * kAttnSlotRows + r) * D + d, o * 0x1p-12f);
           }
         }
       }
@@ -595,8 +636,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
   }
   tc::fence_before_sync();
   if (!whole && tid < u.rows)
-    __stcg(sp.ml + (size_t)slot * kAttnSlotRows + tid,
-           make_float2(sm.m[tid], sm.l[0][tid] + sm.l[1][tid] + sm.l[2][tid] + sm.l[3][tid]));
+    __stcg(sp.sums + (size_t)slot * kAttnSlotRows + tid,
+           make_float4(sm.ref[tid], sm.m[tid],
+                       sm.l[0][tid] + sm.l[1][tid] + sm.l[2][tid] + sm.l[3][tid], 0.0f));
 }
 
 // kSplit: the key tiles of all units, in unit order, are dealt to the CTAs in
@@ -796,7 +838,7 @@ __global__ void __launch_bounds__(2 * D)
   constexpr int kThreadsM = 2 * D, kCols = D / 4, kRuns = 8, kWarps = kThreadsM / 32;
   constexpr int kAhead = 8;             // parts of a run that are loaded at once
   __shared__ float s_w[kAttnMaxCtas];   // the parts' weights
-  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float s_ref[kWarps], s_m[kWarps], s_l[kWarps];
   __shared__ float4 s_x[kRuns - 1][kCols];
   const int c0 = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   pdl_wait();
@@ -817,22 +859,25 @@ __global__ void __launch_bounds__(2 * D)
     }
   };
   // the first parts' references and sums; more parts than threads are read again
-  float2 ml = make_float2(-INFINITY, 0.0f);
-  if (tid < parts) ml = __ldcg(sp.ml + slot(tid));
+  float4 own = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+  if (tid < parts) own = __ldcg(sp.sums + slot(tid));
   load(0);
-  float m = ml.x;
-  for (int p = tid + kThreadsM; p < parts; p += kThreadsM) m = fmaxf(m, __ldcg(&sp.ml[slot(p)].x));
-  m = warp_max(m);
-  if ((tid & 31) == 0) s_m[tid >> 5] = m;
+  float ref = own.x, m = own.y;
+  for (int p = tid + kThreadsM; p < parts; p += kThreadsM) {
+    const float4 more = __ldcg(sp.sums + slot(p));
+    ref = fmaxf(ref, more.x), m = fmaxf(m, more.y);
+  }
+  ref = warp_max(ref), m = warp_max(m);
+  if ((tid & 31) == 0) s_ref[tid >> 5] = ref, s_m[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w]);
+  for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, s_ref[w]), m = fmaxf(m, s_m[w]);
   float l = 0.0f;
   for (int p = tid; p < parts; p += kThreadsM) {
-    if (p >= kThreadsM) ml = __ldcg(sp.ml + slot(p));
-    const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
-    s_w[p] = f;
-    l = fmaf(ml.y, f, l);
+    if (p >= kThreadsM) own = __ldcg(sp.sums + slot(p));
+    const bool none = own.y == -INFINITY;  // (of a row that saw no key its sums are 0, or NaN)
+    s_w[p] = none ? 1.0f : exp2_approx(own.x - ref);
+    l = fmaf(own.z, none ? 1.0f : exp2_approx(own.y - m), l);
   }
   l = warp_sum(l);
   if ((tid & 31) == 0) s_l[tid >> 5] = l;
@@ -863,7 +908,8 @@ __global__ void __launch_bounds__(2 * D)
     const float4 z = s_x[i][col];
     x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
   }
-  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+  const float up = m == -INFINITY ? 1.0f : exp2_approx(ref - m);
+  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l) * up;
   const int tok = row / g;
   const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.x * inv, x.y * inv);
   const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);

@@ -2,10 +2,11 @@
 // chunks of them): commit "the Drama 3 text backbone on CUDA" (full attention with
 // shared key heads); the cache's format is this library's.
 //
-//   S = Q K^T,  P = 2^(scale S - m),  O += P V,  out = O / sum P
+//   S = Q K^T,  P = 2^(scale S + lambda - r),  O += P C,  out = 2^(r - m) O / sum 2^(scale S - m)
 //
-// in one pass over the keys with a running reference m and sum for each row.  Bound
-// by the tensor cores and the shared memory that feeds them.  A CTA holds 256 rows
+// in one pass over the keys with V = C 2^lambda, C the codes and 2^lambda their pages' scales,
+// and for each row two running references, r of S + lambda and m of S, and a sum (see
+// k_attn_decode.cu for why two).  Bound by the tensor cores and the shared memory that feeds them.  A CTA holds 256 rows
 // (128 at head_dim 256): row tiles of 128, the g query heads of a key head times 128/g
 // tokens, and takes the keys 64 at a time (128 at head_dim 256).
 //
@@ -46,10 +47,20 @@ constexpr int kPThreads = 480;
 constexpr int kMmaWarp = 12, kTmaWarp = 14;
 constexpr int kKeys = 128;          // keys of a tile
 constexpr int kChunk = 64;          // keys of a piece of V
-// Weights as p x 2^10 in fp16, p against a reference that may lag the row's maximum
-// by kLag powers of two: sums are scaled again only when a score outgrows that.
-constexpr float kShiftLog = 10.0f;
-constexpr float kLag = 5.0f;
+// Weights as p x 2^5 in fp16, p against a reference that may lag the row's maximum by kLag
+// powers of two: sums are scaled again only when a score outgrows that, or the sum's
+// reference by kSumLag.  What is lost of a weight is 2^-12 of it, or 2^-30 of the row's
+// largest.  (Each row decides for itself, so that no token it does not see changes it; with
+// 2^7 and a lag of 8 a chunk's row tiles are scaled so often that 1024 rows at head_dim 256 take
+// 144 us and not 134.)
+constexpr float kShiftLog = 5.0f;
+constexpr float kLag = 10.0f;
+constexpr float kSumLag = 14.0f;
+// The row's sum takes its terms 2^(s - m) from the weights 2^(s + lambda - r + 5), so that a
+// score costs one exponential.  For a page far below the row's largest the weights are
+// taken no smaller than 2^(s - m - kLeast): as fp16 they are 0 all the same, s - m being at
+// most kSumLag, and the terms stay within fp32.
+constexpr float kLeast = kSumLag + 26.0f;
 
 template <int D>
 struct Pr {
@@ -80,7 +91,6 @@ struct alignas(16) Meta {
   float ks[kKeys / 16];       // key scales
   float log_vs[kKeys / 16];   // value scales: log2, and one over
   float inv_vs[kKeys / 16];
-  float top;                  // the largest value scale
   uint32_t absent;            // groups whose page does not exist (or is not needed)
 };
 
@@ -270,7 +280,7 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
   // keys of tile kt + 1 go out before the values of tile kt: they are needed first
   int page = 0, page_next = 0;
   bool on = false, on_next = false;
-  float ks = -1.0f, vs = 1.0f;
+  float ks = -1.0f, vs = 1.0f, log_vs = 0.0f;
   int base = w.t0;                 // first tile of the lanes' boxes
   const auto look_up = [&](int kt0) {
     const int tiles = min(batch, w.t1 - kt0);
@@ -286,9 +296,10 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
         on_next = false;
       } else {
         ks = a.ks[(size_t)page_next * a.Hkv + w.h];
-        vs = a.vs[(size_t)page_next * a.Hkv + w.h];
+        vs = clamp_scale(a.vs[(size_t)page_next * a.Hkv + w.h]);
       }
     }
+    log_vs = __log2f(vs);
   };
   int v_page = 0, v_sub = -1;
   bool v_on = false;
@@ -311,16 +322,12 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const Work& w,
         for (int g = sub * box / 16; g < (sub + 1) * box / 16; ++g)
         {
           sm.meta[slot].ks[g] = ks;
-          sm.meta[slot].log_vs[g] = __log2f(vs);
+          sm.meta[slot].log_vs[g] = log_vs;
           sm.meta[slot].inv_vs[g] = __fdiv_rn(1.0f, vs);
         }
-      const float top = warp_max(mine && on ? vs : 0.0f);
       const uint32_t absent = __reduce_or_sync(
           0xffffffffu, mine && !on ? ((1u << (box / 16)) - 1) << (sub * box / 16) : 0u);
-      if (lane == 0) {
-        sm.meta[slot].top = top;
-        sm.meta[slot].absent = absent;
-      }
+      if (lane == 0) sm.meta[slot].absent = absent;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.meta_full[slot]);
       wait(&sm.k_empty[rk.i], rk.phase ^ 1, &sm.abort, a.status);
@@ -547,9 +554,13 @@ __device__ __forceinline__ void hide64(uint32_t (&v)[2][32], const RowMask& mk) 
   }
 }
 
-// The largest of a row's 64 scores, in log2 units (NaN scores do not count).
-__device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float* f) {
-  float peak = -INFINITY;
+// The largest of a row's 64 scores, in log2 units, with their pages' scales (x) and without
+// (y); NaN scores do not count.
+__device__ __forceinline__ float2 peak64(const uint32_t (&v)[2][32], const float* f,
+                                         const float* lvs) {
+  float2 peak = make_float2(-INFINITY, -INFINITY);
+  const float4 lv = *reinterpret_cast<const float4*>(lvs);
+  const float log_vs[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float x[16];
@@ -558,18 +569,19 @@ __device__ __forceinline__ float peak64(const uint32_t (&v)[2][32], const float*
     float y[5];
 #pragma unroll
     for (int c = 0; c < 5; ++c) y[c] = max3(x[3 * c], x[3 * c + 1], x[3 * c + 2]);
-    const float m = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15]));
-    peak = fmaxf(peak, m * f[g]);
+    const float m = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], x[15])) * f[g];
+    peak.x = fmaxf(peak.x, m + log_vs[g]);
+    peak.y = fmaxf(peak.y, m);
   }
   return peak;
 }
 
 // Weights of a row's 64 keys (16-key groups group0 on of the tile),
-// 2^(s f + base) by groups of 16, as fp16 to tensor memory; returns their sum freed of
-// the pages' value scales.
+// 2^(s f + lambda - r_base) by groups of 16, as fp16 to tensor memory, and no group's with an
+// exponent below s f + least; returns their sum freed of the pages' value scales and times `up`.
 __device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_p, const float* f,
-                                         const Meta& me, int group0, float log_up, float down,
-                                         float m_base) {
+                                         const Meta& me, int group0, float r_base, float up,
+                                         float least) {
   float sum = 0.0f;
   const float4 lv = *reinterpret_cast<const float4*>(me.log_vs + group0);
   const float4 iv = *reinterpret_cast<const float4*>(me.inv_vs + group0);
@@ -580,9 +592,8 @@ __device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int g = 2 * h + q;
-      // a page below 2^-70 of the largest adds no value that counts
-      const float base = fmaxf(log_vs[g] + log_up, -60.0f) - m_base;
-      const float inv = fminf(inv_vs[g] * down, 0x1p60f);
+      const float base = fmaxf(log_vs[g] - r_base, least);
+      const float inv = fminf(inv_vs[g] * up, 0x1p40f);  // 2^kLeast
       const float2 ff = make_float2(f[g], f[g]), bb = make_float2(base, base);
       float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -605,8 +616,8 @@ __device__ __forceinline__ float weigh64(const uint32_t (&v)[2][32], uint32_t t_
 
 template <int D>
 __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int tile, uint32_t tmem,
-                                       const float* fac_of, PrSmem<D>& sm, float& m_out,
-                                       float& l_out, float& vref_out) {
+                                       const float* fac_of, PrSmem<D>& sm, float& r_out,
+                                       float& m_out, float& l_out) {
   using C = Pr<D>;
   const int row = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(row & 96) << 16;
@@ -619,14 +630,14 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
   // CTA's rows see: a row tile that sees all keys has to know of those values too
   const int pos0 = w.v.first + w.tok0, pos1 = pos0 + w.toks - 1;
   const float fac = fac_of[row];
-  float m = -INFINITY, l = 0.0f, vref = 0x1p-126f, log_up = 0.0f, down = 0.0f;
+  float r = -INFINITY, m = -INFINITY, l = 0.0f;
+  float up = 0.0f;  // 2^(r - m), over the weights' 2^5
   const int n = C::kPer * (w.t1 - w.t0);
   for (int j = 0; j < n; ++j) {
     const int i = j / C::kPer, kt = w.t0 + i, slot = i % C::kMeta, buf = 2 * tile + (j & 1);
     const int part = j % C::kPer, group0 = part * (C::kStep / 16);
     if (part == 0) wait(&sm.meta_full[slot], (i / C::kMeta) & 1, abort, a.status);
     const Meta& me = sm.meta[slot];
-    const float top = me.top;
     const bool edge = edge_tile(a, w, kt, pos0, pos1) || me.absent != 0;
     RowMask mk[C::kStep / 64];
     if (edge) {
@@ -661,43 +672,47 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
       tc::wait_ld();
       if (edge) hide64(v, mk[c]);
     };
-    float peak = -INFINITY;
+    float2 peak = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
     for (int c = 0; c < C::kStep / 64; ++c) {
       load(c);
-      peak = fmaxf(peak, peak64(v, f + 4 * c));
+      const float2 x = peak64(v, f + 4 * c, me.log_vs + group0 + 4 * c);
+      peak = make_float2(fmaxf(peak.x, x.x), fmaxf(peak.y, x.y));
     }
-    if (__any_sync(0xffffffffu, peak > m + kLag || top > vref)) {
-      // new references for the warp's rows, and their sums brought to them
-      const float m_new = fmaxf(m, peak);
-      const float alpha = m_new == -INFINITY ? 1.0f : exp2_approx(m - m_new);
-      const float vf = top > vref ? __fdiv_rn(vref, top) : 1.0f;
-      m = m_new;
-      l *= alpha;
-      vref = fmaxf(vref, top);
-      log_up = kShiftLog - __log2f(vref);
-      down = vref * 0x1p-10f;
+    const bool outgrown = peak.x > r + kLag || peak.y > m + kSumLag;
+    if (__any_sync(0xffffffffu, outgrown)) {
+      // new references for those of the warp's rows, and their sums brought to them (a row
+      // that has not outgrown its own stays as it is, whatever the others see)
+      float alpha = 1.0f;
+      if (outgrown) {
+        const float r_new = fmaxf(r, peak.x), m_new = fmaxf(m, peak.y);
+        alpha = exp2_approx(r - r_new);
+        l *= exp2_approx(m - m_new);
+        r = r_new;
+        m = m_new;
+        up = exp2_approx(r - m - kShiftLog);
+      }
       if (j > 0) {
         wait(&sm.pv_done[buf ^ 1], ((j - 1) >> 1) & 1, abort, a.status);
         tc::fence_after_sync();
         __syncwarp();
-        const float g = alpha * vf;
 #pragma unroll 1
         for (int b = 0; b < D; b += 16) {
           uint32_t o[16];
           tc::tmem_ld_async(t_o + b, o);
           tc::wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
           tc::tmem_st(t_o + b, o);
         }
       }
     }
-    const float m_base = m == -INFINITY ? 0.0f : m;
+    const float r_base = (r == -INFINITY ? 0.0f : r) - kShiftLog;
+    const float least = (m == -INFINITY ? 0.0f : -m) - kLeast;
 #pragma unroll
     for (int c = 0; c < C::kStep / 64; ++c) {
       if (C::kStep > 64) load(c);  // (64 scores are still in registers)
-      l += weigh64(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, log_up, down, m_base);
+      l += weigh64(v, t_s + 32 * c, f + 4 * c, me, group0 + 4 * c, r_base, up, least);
     }
     tc::wait_st();
     tc::fence_before_sync();
@@ -706,9 +721,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Work& w, int til
   wait(&sm.pv_done[2 * tile + ((n - 1) & 1)], ((n - 1) >> 1) & 1, abort, a.status);
   tc::fence_after_sync();
   __syncwarp();
+  r_out = r;
   m_out = m;
   l_out = l;
-  vref_out = vref;
 }
 
 template <int D>
@@ -810,13 +825,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc::fence_async_smem();
     tc::mbar_arrive(&sm.q_full[tile]);
     asm volatile("bar.sync %0, 128;\n" ::"r"(3 + tile) : "memory");  // fac is complete
-    float m = -INFINITY, l = 0.0f, vref = 0x1p-126f;
-    if (any) soften<D>(a, w, tile, tmem, fac, sm, m, l, vref);
+    float r = -INFINITY, m = -INFINITY, l = 0.0f;
+    if (any) soften<D>(a, w, tile, tmem, fac, sm, r, m, l);
     const int tok = row / a.g, toks = min(w.tq, w.toks - tile * w.tq);
     const bool valid = tok < toks;
     const uint32_t t_o = tmem + ((uint32_t)(row & 96) << 16) + 256 + tile * D;
-    float scale = vref * 0x1p-10f;
-    if (splits == 1) scale *= l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+    float scale = 0x1p-5f;
+    if (splits == 1)
+      scale = l == 0.0f ? 0.0f
+                        : __fdividef(m == -INFINITY ? 1.0f : exp2_approx(r - m - kShiftLog), l);
     bf16* to = out + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * out_stride +
                (w.h * a.g + row - tok * a.g) * D;
     const size_t slot = (size_t)blockIdx.x * kAttnPromptRows + tile * 128;
@@ -849,7 +866,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                              __uint_as_float(v[k + 3]) * scale));
       }
     }
-    if (splits > 1 && valid) __stcg(sp.ml + slot + row, make_float2(m, l));
+    if (splits > 1 && valid) __stcg(sp.sums + slot + row, make_float4(r, m, l, 0.0f));
   }
   if (splits > 1 && tid == 0)  // parts, tokens, first row, key head
     sp.shared[blockIdx.x] =
@@ -892,7 +909,7 @@ __global__ void __launch_bounds__(kFew ? 2 * D : 4 * D)
     k_prompt_merge(AttnSplit sp, int g, int splits, bf16* out, int64_t out_stride) {
   using M = Merge<D, kFew>;
   constexpr int kRowThreads = D / 4 * M::kRows;
-  __shared__ float2 s_ml[M::kMost][M::kRows];
+  __shared__ float4 s_sums[M::kMost][M::kRows];
   __shared__ float4 s_x[M::kRuns][kRowThreads];
   __shared__ float s_l[M::kRuns][kRowThreads];
   pdl_wait();
@@ -921,21 +938,25 @@ __global__ void __launch_bounds__(kFew ? 2 * D : 4 * D)
   load(run);
   for (int e = tid; e < parts * M::kRows; e += M::kThreads) {
     const int p = e / M::kRows, k = e % M::kRows;
-    s_ml[p][k] = __ldcg(sp.ml + (size_t)(c0 + p) * kAttnPromptRows + row0 + k);
+    s_sums[p][k] = __ldcg(sp.sums + (size_t)(c0 + p) * kAttnPromptRows + row0 + k);
   }
   __syncthreads();
-  float m = -INFINITY, l = 0.0f;
+  float ref = -INFINITY, m = -INFINITY, l = 0.0f;
 #pragma unroll 4
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, s_ml[p][i % M::kRows].x);
+  for (int p = 0; p < parts; ++p) {
+    const float4 x = s_sums[p][i % M::kRows];
+    ref = fmaxf(ref, x.x), m = fmaxf(m, x.y);
+  }
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int p0 = run;;) {
 #pragma unroll
     for (int k = 0; k < M::kAhead; ++k) {
       const int p = p0 + k * M::kRuns;
       if (p < parts) {
-        const float2 ml = s_ml[p][i % M::kRows];
-        const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - m);
-        l = fmaf(ml.y, f, l);
+        const float4 own = s_sums[p][i % M::kRows];
+        const bool none = own.y == -INFINITY;  // (of a row that saw no key its sums are 0, or NaN)
+        const float f = none ? 1.0f : exp2_approx(own.x - ref);
+        l = fmaf(own.z, none ? 1.0f : exp2_approx(own.y - m), l);
         x = make_float4(fmaf(y[k].x, f, x.x), fmaf(y[k].y, f, x.y), fmaf(y[k].z, f, x.z),
                         fmaf(y[k].w, f, x.w));
       }
@@ -957,7 +978,8 @@ __global__ void __launch_bounds__(kFew ? 2 * D : 4 * D)
     }
   }
   if (!on) return;
-  const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+  const float inv =
+      l == 0.0f ? 0.0f : __fdividef(m == -INFINITY ? 1.0f : exp2_approx(ref - m), l);
   const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv);
   const __nv_bfloat162 hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
   uint2 v;

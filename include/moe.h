@@ -470,8 +470,8 @@ typedef struct {
 /* The cache of one layer, device memory of the caller: n_pages pages, each
  * [kv_heads][page_tokens][head_dim] e4m3 codes (16-byte aligned), and one fp32
  * scale per page and head, [n_pages][kv_heads]; a value is code x scale.
- * moe_kv_append writes powers of two; a cache that other code filled may hold
- * any scales from 2^-100 to 2^100. */
+ * moe_kv_append writes powers of two from 2^-100 to 2^120; a cache that other
+ * code filled may hold any scales of that range, however far apart. */
 typedef struct {
   uint8_t* k_codes;
   uint8_t* v_codes;
@@ -559,8 +559,10 @@ int moe_kv_append(moe_attn* ctx, const moe_kv_cache* cache, const void* k, int64
  * position sees none and gets zeros.  q and out bf16 [rows][q_heads][head_dim]
  * with row strides in values (multiples of 8), 16-byte aligned, not overlapping.
  * A row that sees a NaN key or value, or holds one itself, is NaN; unseen tokens
- * reach no row, whatever they hold.  The softmax and every sum run in fp32; the
- * queries are taken to 2^-17 of the head's largest value, the weights to 11 bits.
+ * reach no row, whatever they hold or their pages' scales are (not a bit of it, in
+ * calls of the same sizes).  The softmax and every sum run in fp32; the queries are
+ * taken to 2^-17 of the head's largest value, the weights (times the page's value
+ * scale) to 11 bits, or 2^-30 of the row's largest where that is more.
  * Results are bitwise identical from run to run.  Asynchronous.
  * Defined by: commit "the Drama 3 text backbone on CUDA" (full attention with
  * shared key heads, for prompts and single tokens); the cache held in 8 bits is
