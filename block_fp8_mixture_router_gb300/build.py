@@ -36,7 +36,8 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(
+        CSRC, "*.h")) + [
         os.path.join(ROOT, "include", "moe.h"), os.path.abspath(__file__)]
 
 

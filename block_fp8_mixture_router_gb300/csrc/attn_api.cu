@@ -13,8 +13,12 @@
 #include <vector>
 
 #include "attn_internal.cuh"
+#include "rope_turns.h"
 
 using namespace moe;
+
+static_assert(MOE_ROPE_PLAIN == 0 && MOE_ROPE_LINEAR == 1 && MOE_ROPE_BY_PARTS == 2,
+              "RopeSpec's scalings");
 
 struct moe_attn {
   moe_attn_config cfg;
@@ -117,23 +121,10 @@ void release(moe_attn* c) {
 
 // Turns per position of every pair as 64-bit fractions of a turn.
 std::vector<unsigned long long> turn_table(const moe_attn_config& c) {
-  const double two_pi = 6.283185307179586476925286766559;
+  const RopeSpec spec{c.rotary_dim, c.rope_scaling, c.rope_base, c.rope_factor,
+                      c.rope_trained_positions, c.rope_turns_low, c.rope_turns_high};
   std::vector<unsigned long long> t(std::max(c.rotary_dim / 2, 1), 0);
-  for (int i = 0; i < c.rotary_dim / 2; ++i) {
-    double f = pow(c.rope_base, -2.0 * i / c.rotary_dim);
-    if (c.rope_scaling == MOE_ROPE_LINEAR) f /= c.rope_factor;
-    if (c.rope_scaling == MOE_ROPE_BY_PARTS) {
-      const double turns = c.rope_trained_positions * f / two_pi;
-      const double g = std::min(
-          1.0, std::max(0.0, (turns - c.rope_turns_low) / (c.rope_turns_high - c.rope_turns_low)));
-      f *= g + (1.0 - g) / c.rope_factor;
-    }
-    double frac = f / two_pi;
-    frac -= floor(frac);  // whole turns per position turn nothing
-    const double hi = floor(ldexp(frac, 32));
-    const double lo = nearbyint(ldexp(ldexp(frac, 32) - hi, 32));  // below 2^32 + 1
-    t[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;
-  }
+  for (int i = 0; i < c.rotary_dim / 2; ++i) t[i] = rope_turns(spec, i);
   return t;
 }
 

@@ -84,11 +84,12 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 }
 
 // Cosine and sine (times the amplitude) of pair i at a position.  The angle in turns is
-// the top 32 bits of position x turns[i] modulo 2^64, off by at most 2^-32 of a turn.  Its
-// nearest quarter turn is taken out in integers, and what is left, at most an eighth,
-// goes as x + y, y the part below x's last bit, into Taylor's series to x^9 and x^10, whose
-// next terms stay below 2^-29: in all good to 2^-23.  (With the fast functions, good to
-// 2^-21, one stored key in a million came out on the other side of a rounding.)
+// the top 32 bits of position x turns[i] modulo 2^64, off by at most 1.25 x 2^-32 of a turn
+// (the bits below them, and the entry's rounding).  Its nearest quarter turn is taken out in
+// integers, and what is left, at most an eighth, goes as x + y, y the part below x's last
+// bit, into Taylor's series to x^9 and x^10, whose next terms stay below 2^-29: in all good
+// to 2^-23.  (With the fast functions, good to 2^-21, one stored key in a million came out
+// on the other side of a rounding.)
 __device__ __forceinline__ float2 rope_cs(const RopeArgs& r, int i, int pos) {
   constexpr float kUnit = 0x1.921fb6p-30f;            // 2 pi / 2^32, and what it leaves
   constexpr float kUnitLow = -0x1.777a5cp-55f;

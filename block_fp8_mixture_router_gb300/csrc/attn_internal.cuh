@@ -36,9 +36,9 @@ struct AttnArgs {
   int* status;
 };
 
-// The rotation of a head: turns per position of each pair as 64-bit fractions
-// of a turn, so that position x entry, taken modulo 2^64, is the exact angle
-// modulo one turn to 2^-65 per position.
+// The rotation of a head: turns per position of each pair as 64-bit fractions of a turn,
+// good to 0.51 units (rope_turns.h), so that position x entry, taken modulo 2^64, is the
+// angle modulo one turn to 2^-65 of a turn per position: 2^-34 at the farthest.
 struct RopeArgs {
   const unsigned long long* turns;  // [rot / 2]
   int rot;

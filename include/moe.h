@@ -526,8 +526,10 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out);
  * any value; gamma bf16 [head_dim] or NULL for no norm; all device pointers,
  * x, y and gamma 16-byte aligned.  y may be x with the same stride (in place);
  * no other overlap (MOE_ERR_INVALID_ARG).  1 <= heads <= 1024; rows is not
- * bounded by max_rows; rows == 0 does nothing.  Angles are exact fractions of a
- * turn in 64-bit fixed point, so far positions lose nothing.  Asynchronous.
+ * bounded by max_rows; rows == 0 does nothing.  Angles are fractions of a turn in
+ * 64-bit fixed point, within 1.25 x 2^-32 of a turn of the definition's at every
+ * position, and their cosines and sines within 2^-23 of those of that angle.
+ * Asynchronous.
  * Defined by: commit "the Drama 3 text backbone on CUDA" (Q/K norm, partial
  * rotary positions in the half layout); the interleaved layout and the scaled
  * frequencies are this library's. */
