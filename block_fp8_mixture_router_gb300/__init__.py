@@ -561,11 +561,13 @@ class KVCache:
     (uint8) and fp32 scales [pages][kv_heads], for keys and for values."""
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        self.device = k_codes.get_device()
         for t, kind, dims in ((k_codes, torch.uint8, 4), (v_codes, torch.uint8, 4),
                               (k_scales, torch.float32, 2), (v_scales, torch.float32, 2)):
-            if t.dtype != kind or not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
+            if t.dtype != kind or not t.is_cuda or t.get_device() != self.device or \
+                    not t.is_contiguous() or t.dim() != dims:
                 raise ValueError("codes must be contiguous 4-D uint8 and scales contiguous 2-D "
-                                 "fp32 CUDA tensors")
+                                 "fp32 CUDA tensors of one device")
         if k_codes.shape != v_codes.shape or k_scales.shape != v_scales.shape or \
                 k_scales.shape != k_codes.shape[:2]:
             raise ValueError("keys and values, codes and scales must agree in shape")
@@ -596,11 +598,12 @@ class AttnBatch:
 
     def __init__(self, row_start, kv_len, pages, rows: int, max_seq_rows: int = 0,
                  max_kv_len: int = 0):
+        self.device = row_start.get_device()
         for t, dims in ((row_start, 1), (kv_len, 1), (pages, 2)):
-            if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims or \
-                    not t.is_contiguous():
+            if t.dtype != torch.int32 or not t.is_cuda or t.get_device() != self.device or \
+                    t.dim() != dims or not t.is_contiguous():
                 raise ValueError("row_start, kv_len and pages must be contiguous int32 CUDA "
-                                 "tensors of 1, 1 and 2 dimensions")
+                                 "tensors of 1, 1 and 2 dimensions, of one device")
         n = kv_len.shape[0]
         if row_start.shape[0] != n + 1 or pages.shape[0] != n:
             raise ValueError("row_start has one entry more than kv_len, pages one row for each")
@@ -610,10 +613,12 @@ class AttnBatch:
         self._ref = ctypes.byref(self._c)
 
 
-def _rows3(t: torch.Tensor, rows: int, heads: int, dim: int, what: str) -> int:
-    """Row stride of a [rows, heads, dim] bf16 CUDA tensor whose heads lie side by side."""
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.shape != (rows, heads, dim):
-        raise ValueError(f"{what} must be a bf16 CUDA tensor [{rows}, {heads}, {dim}]")
+def _rows3(t: torch.Tensor, rows: int, heads: int, dim: int, what: str, device: int) -> int:
+    """Row stride of a [rows, heads, dim] bf16 tensor of a GPU whose heads lie side by side.
+    (A host tensor's device number is -1.)"""
+    if t.dtype is not torch.bfloat16 or t.get_device() != device or t.shape != (rows, heads, dim):
+        raise ValueError(f"{what} must be a bf16 tensor [{rows}, {heads}, {dim}] of CUDA device "
+                         f"{device}")
     sr, sh, sd = t.stride()
     if (sd != 1 and rows) or (sh != dim and heads > 1 and rows):
         raise ValueError(f"{what}: the heads of a row must lie side by side")
@@ -651,16 +656,19 @@ class Attention:
             return torch._C._cuda_getCurrentRawStream(self.device)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
-    def _cache_ok(self, cache: KVCache):
+    def _cache_ok(self, cache: KVCache, batch: AttnBatch):
         if cache._pages != self._pages:
             raise ValueError("the cache's pages are not of this shape")
+        if cache.device != self.device or batch.device != self.device:
+            raise ValueError(f"the cache and the batch must be of CUDA device {self.device}")
 
     def _gamma(self, g):
         if g is None:
             return None
-        if g.dtype is not torch.bfloat16 or not g.is_cuda or g.shape != self._gamma_shape or \
-                not g.is_contiguous():
-            raise ValueError("a gamma must be a contiguous bf16 CUDA tensor [head_dim]")
+        if g.dtype is not torch.bfloat16 or g.get_device() != self.device or \
+                g.shape != self._gamma_shape or not g.is_contiguous():
+            raise ValueError(f"a gamma must be a contiguous bf16 tensor [head_dim] of CUDA device "
+                             f"{self.device}")
         return g.data_ptr()
 
     def _out(self, like, rows):
@@ -674,15 +682,16 @@ class Attention:
         if x.dim() != 3:
             raise ValueError("x must be [rows, heads, head_dim]")
         rows, heads, dim = x.shape[0], x.shape[1], self.shape.head_dim
-        xs = _rows3(x, rows, heads, dim, "x")
-        if positions.dtype is not torch.int32 or not positions.is_cuda or \
+        xs = _rows3(x, rows, heads, dim, "x", self.device)
+        if positions.dtype is not torch.int32 or positions.get_device() != self.device or \
                 positions.shape != (rows,) or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int32 CUDA tensor [rows]")
+            raise ValueError(f"positions must be a contiguous int32 tensor [rows] of CUDA device "
+                             f"{self.device}")
         if out is None:
             out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=x.device)
         rc = self._lib.moe_rope(self.ctx, x.data_ptr(), xs, heads, positions.data_ptr(),
                                 self._gamma(gamma), eps, rows, out.data_ptr(),
-                                _rows3(out, rows, heads, dim, "out"), self._at(stream))
+                                _rows3(out, rows, heads, dim, "out", self.device), self._at(stream))
         if rc:
             raise MoEError(rc, "moe_rope")
         return out
@@ -691,9 +700,9 @@ class Attention:
                stream=None):
         """Rows of keys and values [rows, kv_heads, head_dim] into the cache."""
         s, n = self.shape, batch.rows
-        ks = _rows3(k, n, s.kv_heads, s.head_dim, "k")
-        vs = _rows3(v, n, s.kv_heads, s.head_dim, "v")
-        self._cache_ok(cache)
+        ks = _rows3(k, n, s.kv_heads, s.head_dim, "k", self.device)
+        vs = _rows3(v, n, s.kv_heads, s.head_dim, "v", self.device)
+        self._cache_ok(cache, batch)
         rc = self._lib.moe_kv_append(self.ctx, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
                                      batch._ref, self._at(stream))
         if rc:
@@ -704,13 +713,13 @@ class Attention:
         """Attention of q [rows, q_heads, head_dim] over the cache, which already
         holds the batch's rows."""
         s, n = self.shape, batch.rows
-        qs = _rows3(q, n, s.q_heads, s.head_dim, "q")
+        qs = _rows3(q, n, s.q_heads, s.head_dim, "q", self.device)
         if out is None:
             out = self._out(q, n)
-        self._cache_ok(cache)
+        self._cache_ok(cache, batch)
         rc = self._lib.moe_attn_forward(self.ctx, cache._ref, q.data_ptr(), qs, batch._ref,
                                         out.data_ptr(),
-                                        _rows3(out, n, s.q_heads, s.head_dim, "out"),
+                                        _rows3(out, n, s.q_heads, s.head_dim, "out", self.device),
                                         self._at(stream))
         if rc:
             raise MoEError(rc, "moe_attn_forward")
@@ -722,14 +731,14 @@ class Attention:
         """The whole attention step from a projection's rows [rows, q_heads + 2 kv_heads,
         head_dim]: norms and rotates, appends, attends."""
         s, n = self.shape, batch.rows
-        xs = _rows3(qkv, n, s.q_heads + 2 * s.kv_heads, s.head_dim, "qkv")
+        xs = _rows3(qkv, n, s.q_heads + 2 * s.kv_heads, s.head_dim, "qkv", self.device)
         if out is None:
             out = self._out(qkv, n)
-        self._cache_ok(cache)
+        self._cache_ok(cache, batch)
         rc = self._lib.moe_attn_step(self.ctx, cache._ref, qkv.data_ptr(), xs,
                                      self._gamma(q_gamma), self._gamma(k_gamma), eps, batch._ref,
                                      out.data_ptr(),
-                                     _rows3(out, n, s.q_heads, s.head_dim, "out"),
+                                     _rows3(out, n, s.q_heads, s.head_dim, "out", self.device),
                                      self._at(stream))
         if rc:
             raise MoEError(rc, "moe_attn_step")
