@@ -14,6 +14,7 @@
 
 #include "attn_internal.cuh"
 #include "rope_turns.h"
+#include "row_overlap.h"
 
 using namespace moe;
 
@@ -139,13 +140,11 @@ bool rows_ok(const void* p, int64_t stride, int64_t width) {
   return p && aligned16(p) && stride >= width && stride % 8 == 0;
 }
 
-// Whether two arrays of rows (row stride and width in bf16 values) share a byte
-// of the ranges that they span.
+// Whether two arrays of rows (row stride and width in bf16 values) share a byte.
 bool overlap_rows(const void* a, int64_t as, int64_t aw, const void* b, int64_t bs, int64_t bw,
                   int rows) {
-  const char* pa = static_cast<const char*>(a);
-  const char* pb = static_cast<const char*>(b);
-  return pa < pb + 2 * (bs * (rows - 1) + bw) && pb < pa + 2 * (as * (rows - 1) + aw);
+  return rows_overlap(reinterpret_cast<uintptr_t>(a), 2 * as, 2 * aw,
+                      reinterpret_cast<uintptr_t>(b), 2 * bs, 2 * bw, rows);
 }
 
 int check_batch(const moe_attn* c, const moe_kv_cache* k, const moe_attn_batch* b) {

@@ -524,8 +524,9 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn** out);
  * x, y bf16 [rows][heads][head_dim] with row strides of x_stride and y_stride
  * values (multiples of 8, at least heads * head_dim); positions int32 [rows],
  * any value; gamma bf16 [head_dim] or NULL for no norm; all device pointers,
- * x, y and gamma 16-byte aligned.  y may be x with the same stride (in place);
- * no other overlap (MOE_ERR_INVALID_ARG).  1 <= heads <= 1024; rows is not
+ * x, y and gamma 16-byte aligned.  y may be x with the same stride (in place), or
+ * lie beside x in the same rows; no byte may be shared otherwise
+ * (MOE_ERR_INVALID_ARG).  1 <= heads <= 1024; rows is not
  * bounded by max_rows; rows == 0 does nothing.  Angles are fractions of a turn in
  * 64-bit fixed point, within 1.25 x 2^-32 of a turn of the definition's at every
  * position, and their cosines and sines within 2^-23 of those of that angle.
@@ -559,7 +560,8 @@ int moe_kv_append(moe_attn* ctx, const moe_kv_cache* cache, const void* k, int64
  * out[r][h] = sum_j softmax_j(softmax_scale q[r][h] . k_j) v_j over the keys j
  * that the row sees (see moe_attn_batch and window); a row at a negative
  * position sees none and gets zeros.  q and out bf16 [rows][q_heads][head_dim]
- * with row strides in values (multiples of 8), 16-byte aligned, not overlapping.
+ * with row strides in values (multiples of 8), 16-byte aligned, without a shared
+ * byte (they may be column ranges of one buffer).
  * A row that sees a NaN key or value, or holds one itself, is NaN; unseen tokens
  * reach no row, whatever they hold or their pages' scales are (not a bit of it, in
  * calls of the same sizes).  The softmax and every sum run in fp32; the queries are
