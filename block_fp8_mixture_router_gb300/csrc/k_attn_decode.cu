@@ -115,6 +115,7 @@ struct DecSmem {
   float spread;                  // the largest of them
   int top[2][4][16];       // the warps' row maxima (r's and m's), as ordered integers
   float l[4][16];          // the warps' row sums
+  uint32_t odd[4];         // rows of which a warp's columns hold a NaN
   float2 meta[Dec<D>::kStages][kAttnKeys / 16];  // scales of 16 keys and their values
   uint64_t full[Dec<D>::kStages], empty[Dec<D>::kStages];
   uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done;
@@ -606,6 +607,15 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
   tc::wait_bounded(&sm.pv_done, ph.pv ^ 1, abort, a.status);
   tc::fence_after_sync();
   __syncwarp();
+  const auto out_at = [&](int r, int d) {
+    const int tok = r / a.g;
+    return out + (int64_t)(u.v.row0 + u.tok0 + tok) * out_stride +
+           (u.h * a.g + r - tok * a.g) * D + d;
+  };
+  const auto part_at = [&](int r, int d) {
+    return sp.o + ((size_t)slot * kAttnSlotRows + r) * D + d;
+  };
+  uint32_t odd = 0;  // rows of which this thread's columns hold a NaN
 #pragma unroll
   for (int panel = 0; panel < C::kPanels; ++panel) {
     const uint32_t dt = tmem + 64 + panel * 64;
@@ -621,20 +631,33 @@ __device__ __forceinline__ void soften(const AttnArgs& a, const Unit& u, int t0,
           const float o = (__uint_as_float(x[r]) + __uint_as_float(x[R + r]) * 0x1p-3f +
                            __uint_as_float(y[r]) * 0x1p-6f +
                            __uint_as_float(y[R + r]) * 0x1p-9f);
+          if (o != o) odd |= 1u << r;
           if (whole) {
             const float sum = sm.l[0][r] + sm.l[1][r] + sm.l[2][r] + sm.l[3][r];
             const float inv = sum == 0.0f ? 0.0f : __fdividef(sm.base[r].y, sum);
-            const int tok = r / a.g;
-            out[(int64_t)(u.v.row0 + u.tok0 + tok) * out_stride + (u.h * a.g + r - tok * a.g) * D +
-                d] = __float2bfloat16_rn(o * inv);
+            *out_at(r, d) = __float2bfloat16_rn(o * inv);
           } else {
-            __stcg(sp.o + ((size_t)slot * kAttnSlotRows + r) * D + d, o * 0x1p-12f);
+            __stcg(part_at(r, d), o * 0x1p-12f);
           }
         }
       }
     }
   }
   tc::fence_before_sync();
+  // A NaN value of a tile that all rows see reaches its own column only: the row is NaN all
+  // the same, as where the rows' masks made its weight NaN.
+  if (softmax_any(odd != 0)) {
+    odd = __reduce_or_sync(0xffffffffu, odd);
+    if (lane == 0) sm.odd[warp] = odd;
+    softmax_sync();
+    odd = sm.odd[0] | sm.odd[1] | sm.odd[2] | sm.odd[3];
+    for (int d = tid; d < D; d += kSoftmax)
+      for (int r = 0; r < u.rows; ++r)
+        if ((odd >> r) & 1) {
+          if (whole) *out_at(r, d) = __float2bfloat16_rn(__int_as_float(0x7FFFFFFF));
+          else __stcg(part_at(r, d), __int_as_float(0x7FFFFFFF));
+        }
+  }
   if (!whole && tid < u.rows)
     __stcg(sp.sums + (size_t)slot * kAttnSlotRows + tid,
            make_float4(sm.ref[tid], sm.m[tid],

@@ -837,6 +837,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     bf16* to = out + (int64_t)(w.v.row0 + w.tok0 + tile * w.tq + tok) * out_stride +
                (w.h * a.g + row - tok * a.g) * D;
     const size_t slot = (size_t)blockIdx.x * kAttnPromptRows + tile * 128;
+    bool odd = false;  // the row holds a NaN
 #pragma unroll 1
     for (int b = 0; b < D; b += 32) {
       uint32_t v[32];
@@ -849,6 +850,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int k = 0; k < 32; ++k) v[k] = 0;
       }
       if (!valid) continue;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) odd |= __uint_as_float(v[k]) != __uint_as_float(v[k]);
       if (splits == 1) {
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
@@ -865,6 +868,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
                              __uint_as_float(v[k + 2]) * scale,
                              __uint_as_float(v[k + 3]) * scale));
       }
+    }
+    if (odd) {
+      // a NaN value of a tile that all rows see reaches its own column only: the row is NaN
+      // all the same, as where its mask made the weight NaN
+      const float nan = __int_as_float(0x7FFFFFFF);
+      for (int b = 0; b < D; b += 4)
+        if (splits == 1)
+          *reinterpret_cast<uint2*>(to + b) = make_uint2(0x7FFF7FFFu, 0x7FFF7FFFu);
+        else
+          __stcg(reinterpret_cast<float4*>(sp.o + slot * D + b * 128 + 4 * row),
+                 make_float4(nan, nan, nan, nan));
     }
     if (splits > 1 && valid) __stcg(sp.sums + slot + row, make_float4(r, m, l, 0.0f));
   }
