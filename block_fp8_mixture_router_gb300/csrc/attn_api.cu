@@ -42,14 +42,14 @@ constexpr int kDecTileRows = kAttnSlotRows;
 // The decode kernel takes a sequence whose rows (tokens x query heads of a key head) fit
 // one of its tiles, or few tiles in all: it reads the keys once for every tile.  The
 // prompt kernel takes the others, with 128 rows to a tile.  Tiles = sequences x key heads
-// x tiles of a sequence; measured over 300 to 200000 keys, prompt kernel's time over
-// decode kernel's, geometric means:
-//   head_dim    4 tiles     8     16     24     64
-//         64       0.91   0.85   0.78   0.67   0.63
-//        128       1.03   0.94   0.86   0.75   0.66
-//        256       1.31   1.15   1.12   0.95   0.78
-// hence more than head_dim / 16 tiles.
-constexpr int kPromptTiles = 16;
+// x tiles of a sequence; measured over 300 to 200000 keys, 1 to 8 query heads to a key
+// head, prompt kernel's time over decode kernel's, geometric means:
+//   head_dim   2 tiles     3      4      6      8     12     16     24     32
+//         64      1.01   0.92   0.89   0.80   0.80   0.70   0.69   0.57   0.55
+//        128      1.08   1.00   0.94   0.87   0.86   0.75   0.72   0.62   0.60
+//        256      1.13   1.07   1.01   0.90   0.91   0.75   0.76   0.66   0.63
+// hence from 3, 4 and 6 tiles on.
+constexpr bool prompt_tiles(int head_dim, long long tiles) { return tiles > 1 + head_dim / 64; }
 
 struct Device {
   int prev = -1;
@@ -231,7 +231,7 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   const long long units = (long long)b->rows / tq + b->n_seqs;  // per key head, at most
   const long long row_tiles = std::min(units, seq_tiles * b->n_seqs) * a.Hkv;
   const bool prompt =
-      (long long)seq_rows * a.g > kDecTileRows && row_tiles > D / kPromptTiles;
+      (long long)seq_rows * a.g > kDecTileRows && prompt_tiles(D, row_tiles);
   AttnMaps maps;
   if (!make_attn_maps(&maps, a, D, prompt)) return MOE_ERR_CUDA;
   if (prompt) {
@@ -260,6 +260,9 @@ int run_attention(moe_attn* c, const AttnArgs& a, const moe_attn_batch* b, const
   //   32 x 4 over 100 12.8 / 7.9, 1000 15.7 / 15.7, ragged 14.9 / 13.4;
   //   128 x 4 over 100 14.8 / 15.7, 1000 37.6 / 34.6, ragged 38.0 / 29.4;
   //   1024 x 1 over 100 31 / 44, 1000 69 / 74; 4000 x 4 over 1000 678 / 1256.
+  // Over some 150 such sizes each (1 to 4000 sequences, 100 to 1000 keys, equal and ragged) the
+  // rule's choice takes 1.0 % longer than the better one at head_dim 64, 1.2 % at 128 and
+  // 3.0 % at 256 (geometric means); the worst are ragged batches of 128 to 256 sequences.
   long long span = keys;
   if (a.window) span = std::min<long long>(span, (long long)a.window + tq + kAttnKeys);
   const long long unit_tiles = (span + kAttnKeys - 1) / kAttnKeys, places = c->dec_slots;
