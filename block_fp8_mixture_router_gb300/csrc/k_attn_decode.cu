@@ -14,7 +14,8 @@
 //   out = 2^(r - m) sum_j 2^(s_j + lambda_j - r) c_j / sum_j 2^(s_j - m).
 //
 // Each row so has weights of its own range, whatever scales other rows' keys have and
-// however far apart its own are.  The lower sum takes its terms from the weights, times
+// however far apart its own are (2 us of the 107 below, against one scale reference for
+// all rows of a tile).  The lower sum takes its terms from the weights, times
 // 2^(r - m - lambda), so that a score costs one exponential; where that factor passes
 // 2^kSpread, keys that count could have weights below fp32's range, and the terms get
 // exponentials of their own.
@@ -36,9 +37,9 @@
 // the MMAs and one that keeps a ring of key tiles (128 keys and their values, 32 KB
 // at head_dim 128) filled by TMA; two CTAs share an SM (one at head_dim 256).
 //
-// Measured: 64 rows of 32 heads over 590 MB of codes, 104 us (5.7 TB/s, where a plain
-// copy reaches 6.8); one row of 16 heads over 262143 tokens, 50 us (5.4 TB/s); one row
-// over 4096 tokens, 9.0 us: 5 us of dependent steps in a CTA (finding its tiles 1.2,
+// Measured: 64 rows of 32 heads over 590 MB of codes, 107 us (5.6 TB/s, where a plain
+// copy reaches 6.8); one row of 16 heads over 262143 tokens, 51 us (5.3 TB/s); one row
+// over 4096 tokens, 9.2 us: 5 us of dependent steps in a CTA (finding its tiles 1.2,
 // queries and first tile 1.6, softmax 1.2, products and the result 1.1), the rest launches
 // and the join.
 #include "attn_tc.cuh"
@@ -982,7 +983,7 @@ cudaError_t setup_attn_decode(int D) {
 
 // Two CTAs of up to 113 KB, 128 registers and 128 TMEM columns share an SM (the
 // occupancy query counts one for a kernel that allocates tensor memory; measured, 64 rows
-// over 590 MB of keys and values take 133 us with one and 104 with two).
+// over 590 MB of keys and values take 142 us with one and 107 with two).
 int attn_decode_slots(int D, int sm_count) { return D == 256 ? sm_count : 2 * sm_count; }
 
 cudaError_t launch_attn_decode(int D, int tile_rows, const AttnArgs& a, const AttnMaps& m,

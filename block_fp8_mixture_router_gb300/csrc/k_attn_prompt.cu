@@ -22,13 +22,13 @@
 //   tiles' buffers have room for 64 keys each, although an MMA with N = 64 takes as long
 //   as one with N = 128.
 //
-// Measured: a prompt of 16384 rows, 16 heads of 128, 907 us (1213 TFLOP/s of two products,
-// 63 % of what a plain 16-bit matrix product reaches); 1024 rows over 8192 keys at head_dim
-// 256, 136 us (950); frames of 11 rows, 8 sequences over 1500 keys, 20 us, by their
-// latency.  A step of 64 keys and 256 rows takes 1770 clocks, of which the MMAs take 1660:
+// Measured: a prompt of 16384 rows, 16 heads of 128, 914 us (1203 TFLOP/s of two products,
+// 62 % of what a plain 16-bit matrix product reaches); 1024 rows over 8192 keys at head_dim
+// 256, 133 us (970); frames of 11 rows, 8 sequences over 1500 keys, 19 us, by their
+// latency.  A step of 64 keys and 256 rows takes 1780 clocks, of which the MMAs take 1660:
 // those of the scores, with N = 64, twice their share.
 //
-// Slower at 16384 rows, 16 heads of 128, beside 969 us (now 915): one buffer of 128 keys per row
+// Slower at 16384 rows, 16 heads of 128, beside 969 us at the time: one buffer of 128 keys per row
 // tile, 1048 us (the row tiles fall into step, and both work while the tensor cores
 // idle); the same with the row tiles' softmax warps taking turns, 1161 us (reads of
 // tensor memory take twice as long beside running MMAs); a row's scores held in 192

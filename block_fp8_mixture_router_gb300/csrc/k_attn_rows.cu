@@ -10,9 +10,9 @@
 // row belongs to D/8 neighbouring lanes, 16 bytes each: loads and stores are
 // whole 16-byte pieces, the norm's sum and the half layout's partner values
 // travel by shuffles, and since no lane reads another's memory the rotation can
-// run in place.  Measured: 20 heads of 128 of 16384 rows rotated in 32.3 us (5.2 TB/s,
+// run in place.  Measured: 20 heads of 128 of 16384 rows rotated in 32.5 us (5.2 TB/s,
 // where a plain copy reaches 6.8), of one row in 3.2 us; 10600 rows of keys and values of
-// 4 heads in three prompts appended in 10.7 us, a row for each of 64 sequences in 5.7.
+// 4 heads in three prompts appended in 10.9 us, a row for each of 64 sequences in 5.7.
 #include <algorithm>
 
 #include "attn_device.cuh"

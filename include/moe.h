@@ -486,8 +486,12 @@ typedef struct {
  * cache once this call's rows are in it: its i-th row of n stands at position
  * kv_len[s] - n + i.  pages[s * pages_stride + j] is the page that holds tokens
  * j * page_tokens and on; entries behind the last token are not read.
- * max_seq_rows and max_kv_len: no sequence has more rows or tokens.  They size
- * the launch only: larger values in the arrays are handled, more slowly.
+ * max_seq_rows and max_kv_len: no sequence has more rows or tokens (0: not
+ * known, taken as rows and as pages_stride * page_tokens).  They choose the kernel
+ * and size the launch: larger values in the arrays are handled, more slowly.  One
+ * kernel takes the whole batch, the prompts' where max_seq_rows calls for it, and
+ * single tokens over long caches beside a prompt's rows are slow there: they want a
+ * call of their own, and so does max_seq_rows = 1 in a batch of single tokens.
  * A page number outside the cache, a length outside 0..pages_stride *
  * page_tokens or a descending row_start touches no memory outside the buffers;
  * results of that sequence are then undefined, and
@@ -580,7 +584,8 @@ int moe_attn_forward(moe_attn* ctx, const moe_kv_cache* cache, const void* q, in
  * rotated at the batch's positions and rounded to bf16; keys and values go to the
  * cache; out as in moe_attn_forward.  Bit for bit moe_rope on the queries and on
  * the keys, moe_kv_append and moe_attn_forward, with the first three in one
- * launch.  Asynchronous.
+ * launch.  The gate by which that backbone multiplies the output is the caller's.
+ * Asynchronous.
  * Defined by: commit "the Drama 3 text backbone on CUDA" and PR #925 "drama: load
  * the checkpoint with direct I/O in file order and build the codec on its own
  * thread", commit list (one prologue launch norms, rotates and caches a row). */
