@@ -152,7 +152,7 @@ def test_scales_of_the_whole_range(dev, kw, rows, tokens):  # noqa: F811
 
 
 @pytest.mark.parametrize("rows,tokens", [(1, 100), (3, 700), (150, 400), (1, 6000), (150, 5000)])
-@pytest.mark.parametrize("size", [1.0, 2.0 ** 20, 2.0 ** 100])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 20, 2.0 ** 100, 2.0 ** 124])
 def test_zero_tokens_keep_their_weight(dev, rows, tokens, size):  # noqa: F811
     """Pages of zeros, which the append gives the smallest scale there is, beside pages of
     ordinary and of large values: their keys count in the softmax all the same."""
