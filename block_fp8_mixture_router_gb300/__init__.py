@@ -46,7 +46,10 @@ EXPORTED = ("moe_create", "moe_load_weights", "moe_forward", "moe_forward_host",
             "moe_chain_forward", "moe_chain_destroy", "moe_debug_poison_workspace",
             "moe_attn_required_bytes", "moe_attn_create", "moe_rope", "moe_kv_append",
             "moe_attn_forward", "moe_attn_step", "moe_attn_last_device_status",
-            "moe_attn_destroy")
+            "moe_attn_destroy",
+            "moe_ops_required_bytes", "moe_ops_create", "moe_dispatch", "moe_dispatch_grad",
+            "moe_combine", "moe_combine_grad", "moe_linear", "moe_linear_grad", "moe_swiglu",
+            "moe_swiglu_grad", "moe_ops_last_device_status", "moe_ops_destroy")
 
 MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
 MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BY_PARTS = 0, 1, 2
@@ -88,6 +91,26 @@ class moe_attn_batch(ctypes.Structure):
                 ("pages", ctypes.c_void_p)] + [
                     (n, ctypes.c_int) for n in
                     ("n_seqs", "pages_stride", "rows", "max_seq_rows", "max_kv_len")]
+
+
+class moe_ops_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_experts", "top_k", "max_rows", "max_width")] + [
+        ("workspace_cap_bytes", ctypes.c_size_t)]
+
+
+class moe_rows(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class moe_block_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("groups", "out", "in_")]
+
+
+class moe_order(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("starts", "pair_of_slot", "slot_of_pair")] + [
+        ("tokens", ctypes.c_int)]
 
 
 class MoEError(RuntimeError):
@@ -146,9 +169,25 @@ def load_library(path: str = LIB_PATH):
     L.moe_attn_last_device_status.argtypes = [vp]
     L.moe_attn_destroy.argtypes = [vp]
     L.moe_attn_destroy.restype = None
+    rp, wp = ctypes.POINTER(moe_rows), ctypes.POINTER(moe_block_weights)
+    op = ctypes.POINTER(moe_order)
+    L.moe_ops_required_bytes.argtypes = [ctypes.POINTER(moe_ops_config),
+                                         ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_ops_create.argtypes = [ctypes.POINTER(moe_ops_config), i, ip]
+    L.moe_dispatch.argtypes = [vp, vp, vp, i64, i, op, rp, vp]
+    L.moe_dispatch_grad.argtypes = [vp, vp, i64, op, i, vp, i64, vp]
+    L.moe_combine.argtypes = [vp, vp, i64, op, vp, i, vp, i64, vp]
+    L.moe_combine_grad.argtypes = [vp, vp, i64, vp, i64, op, vp, i, rp, vp, vp]
+    L.moe_linear.argtypes = [vp, rp, wp, vp, i, vp, i64, vp]
+    L.moe_linear_grad.argtypes = [vp, rp, wp, vp, i, vp, i64, vp]
+    L.moe_swiglu.argtypes = [vp, vp, i64, i, i, rp, vp]
+    L.moe_swiglu_grad.argtypes = [vp, vp, i64, vp, i64, i, i, rp, vp]
+    L.moe_ops_last_device_status.argtypes = [vp]
+    L.moe_ops_destroy.argtypes = [vp]
+    L.moe_ops_destroy.restype = None
     for n in EXPORTED:
         if n not in ("moe_destroy", "moe_status_string", "moe_chain_destroy",
-                     "moe_attn_destroy"):
+                     "moe_attn_destroy", "moe_ops_destroy"):
             getattr(L, n).restype = ctypes.c_int
     _lib = L
     return L
@@ -311,6 +350,73 @@ def moe_attn_last_device_status(ctx) -> int:
 
 def moe_attn_destroy(ctx) -> None:
     load_library().moe_attn_destroy(ctx)
+
+
+def moe_ops_required_bytes(cfg: moe_ops_config):
+    n = ctypes.c_size_t()
+    rc = load_library().moe_ops_required_bytes(ctypes.byref(cfg), ctypes.byref(n))
+    return rc, n.value
+
+
+def moe_ops_create(cfg: moe_ops_config, device: int = 0):
+    h = ctypes.c_void_p()
+    rc = load_library().moe_ops_create(ctypes.byref(cfg), device, ctypes.byref(h))
+    return rc, h
+
+
+def moe_dispatch(ctx, idx, x, x_stride: int, width: int, order, rows, stream=None) -> int:
+    """order: a moe_order, rows: a moe_rows (each may be None)."""
+    return load_library().moe_dispatch(ctx, _ptr(idx), _ptr(x), x_stride, width, order, rows,
+                                       _stream(stream))
+
+
+def moe_dispatch_grad(ctx, drows, drows_stride: int, order, width: int, dx, dx_stride: int,
+                      stream=None) -> int:
+    return load_library().moe_dispatch_grad(ctx, _ptr(drows), drows_stride, order, width,
+                                            _ptr(dx), dx_stride, _stream(stream))
+
+
+def moe_combine(ctx, rows, rows_stride: int, order, weights, width: int, y, y_stride: int,
+                stream=None) -> int:
+    return load_library().moe_combine(ctx, _ptr(rows), rows_stride, order, _ptr(weights), width,
+                                      _ptr(y), y_stride, _stream(stream))
+
+
+def moe_combine_grad(ctx, dy, dy_stride: int, rows, rows_stride: int, order, weights, width: int,
+                     drows, dweights, stream=None) -> int:
+    return load_library().moe_combine_grad(ctx, _ptr(dy), dy_stride, _ptr(rows), rows_stride,
+                                           order, _ptr(weights), width, drows, _ptr(dweights),
+                                           _stream(stream))
+
+
+def moe_linear(ctx, x, w, starts, rows: int, y, y_stride: int, stream=None) -> int:
+    """x: a moe_rows, w: a moe_block_weights (each may be None)."""
+    return load_library().moe_linear(ctx, x, w, _ptr(starts), rows, _ptr(y), y_stride,
+                                     _stream(stream))
+
+
+def moe_linear_grad(ctx, dy, w, starts, rows: int, dx, dx_stride: int, stream=None) -> int:
+    return load_library().moe_linear_grad(ctx, dy, w, _ptr(starts), rows, _ptr(dx), dx_stride,
+                                          _stream(stream))
+
+
+def moe_swiglu(ctx, gate_up, gate_up_stride: int, rows: int, width: int, h, stream=None) -> int:
+    return load_library().moe_swiglu(ctx, _ptr(gate_up), gate_up_stride, rows, width, h,
+                                     _stream(stream))
+
+
+def moe_swiglu_grad(ctx, dh, dh_stride: int, gate_up, gate_up_stride: int, rows: int, width: int,
+                    dgate_up, stream=None) -> int:
+    return load_library().moe_swiglu_grad(ctx, _ptr(dh), dh_stride, _ptr(gate_up), gate_up_stride,
+                                          rows, width, dgate_up, _stream(stream))
+
+
+def moe_ops_last_device_status(ctx) -> int:
+    return load_library().moe_ops_last_device_status(ctx)
+
+
+def moe_ops_destroy(ctx) -> None:
+    load_library().moe_ops_destroy(ctx)
 
 
 def moe_set_option(ctx, option: int, value: int) -> int:
@@ -746,3 +852,300 @@ class Attention:
 
     def device_status(self) -> int:
         return moe_attn_last_device_status(self.ctx)
+
+
+# ---- the layer's parts as operators of their own ---------------------------
+
+def _groups(width: int) -> int:
+    return -(-width // 128)
+
+
+class QuantRows:
+    """Rows in 8 bits: e4m3 codes [rows, width] (uint8) and a fp32 scale for each 128 values
+    of a row [rows, ceil(width / 128)], as MoELayer.quantize and add_rmsnorm_quantize return
+    them."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.device = codes.get_device()
+        if codes.dtype != torch.uint8 or scales.dtype != torch.float32 or not codes.is_cuda or \
+                scales.get_device() != self.device or codes.dim() != 2 or \
+                not codes.is_contiguous() or not scales.is_contiguous() or \
+                tuple(scales.shape) != (codes.shape[0], _groups(codes.shape[1])):
+            raise ValueError("codes must be contiguous uint8 [rows, width] and scales contiguous "
+                             "fp32 [rows, ceil(width / 128)] CUDA tensors of one device")
+        self.codes, self.scales = codes, scales
+        self.shape = tuple(codes.shape)
+        self._c = moe_rows(None, 0, codes.data_ptr(), scales.data_ptr())
+
+    @classmethod
+    def empty(cls, rows: int, width: int, device="cuda"):
+        return cls(torch.empty((rows, width), dtype=torch.uint8, device=device),
+                   torch.empty((rows, _groups(width)), dtype=torch.float32, device=device))
+
+
+class BlockWeights:
+    """W [groups, out, in] (or [out, in]) as a block-FP8 checkpoint stores it: e4m3 codes
+    (uint8) and a fp32 scale per 128 x 128 block."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() == 2 and scales.dim() == 2:
+            codes, scales = codes[None], scales[None]
+        self.device = codes.get_device()
+        if codes.dtype != torch.uint8 or scales.dtype != torch.float32 or not codes.is_cuda or \
+                scales.get_device() != self.device or codes.dim() != 3 or \
+                not codes.is_contiguous() or not scales.is_contiguous() or \
+                tuple(scales.shape) != (codes.shape[0], _groups(codes.shape[1]),
+                                        _groups(codes.shape[2])):
+            raise ValueError("codes must be contiguous uint8 [groups, out, in] and scales "
+                             "contiguous fp32 [groups, ceil(out / 128), ceil(in / 128)] CUDA "
+                             "tensors of one device")
+        self.codes, self.scales = codes, scales
+        self.groups, self.out, self.inner = codes.shape
+        self._c = moe_block_weights(codes.data_ptr(), scales.data_ptr(), *codes.shape)
+        self._ref = ctypes.byref(self._c)
+
+
+class ExpertOrder:
+    """Rows sorted by expert (moe_order in include/moe.h): int32 starts [n_experts + 1],
+    pair_of_slot [tokens x top_k] and slot_of_pair [tokens, top_k]."""
+
+    def __init__(self, starts: torch.Tensor, pair_of_slot: torch.Tensor,
+                 slot_of_pair: torch.Tensor):
+        self.device = starts.get_device()
+        for t, dims in ((starts, 1), (pair_of_slot, 1), (slot_of_pair, 2)):
+            if t.dtype != torch.int32 or not t.is_cuda or t.get_device() != self.device or \
+                    t.dim() != dims or not t.is_contiguous():
+                raise ValueError("starts, pair_of_slot and slot_of_pair must be contiguous int32 "
+                                 "CUDA tensors of 1, 1 and 2 dimensions, of one device")
+        if pair_of_slot.numel() != slot_of_pair.numel():
+            raise ValueError("pair_of_slot has one entry for each of slot_of_pair's")
+        self.starts, self.pair_of_slot, self.slot_of_pair = starts, pair_of_slot, slot_of_pair
+        self.tokens = slot_of_pair.shape[0]
+        self._shape = (starts.shape[0] - 1, slot_of_pair.shape[1])
+        self._c = moe_order(starts.data_ptr(), pair_of_slot.data_ptr(), slot_of_pair.data_ptr(),
+                            self.tokens)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_experts: int, tokens: int, top_k: int, device="cuda"):
+        def ints(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=device)
+        return cls(ints(n_experts + 1), ints(tokens * top_k), ints(tokens, top_k))
+
+
+class ExpertOps:
+    """The layer's parts as operators, with their gradients, on one GPU: owns a context and
+    its workspace (moe_ops_config in include/moe.h).  Rows are bf16 tensors [rows, width], or
+    QuantRows; `out` may be given in either form, `quantize` asks for new QuantRows."""
+
+    def __init__(self, n_experts: int = 256, top_k: int = 8, max_rows: int = 1024,
+                 max_width: int = 2048, device: int = 0, workspace_cap_bytes: int = 0):
+        self.n_experts, self.top_k, self.max_rows = n_experts, top_k, max_rows
+        self.device = device
+        rc, h = moe_ops_create(moe_ops_config(n_experts, top_k, max_rows, max_width,
+                                              workspace_cap_bytes), device)
+        _check(rc, "moe_ops_create")
+        self.ctx = h
+        self._lib = load_library()
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            moe_ops_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _at(self, stream) -> int:
+        """The stream's handle; None: PyTorch's current stream of the device."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+    def _rows2(self, t, what: str, rows=None, width=None) -> int:
+        """Row stride of a bf16 tensor [rows, width] of this device."""
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or \
+                t.get_device() != self.device or t.dim() != 2 or \
+                (rows is not None and t.shape[0] != rows) or \
+                (width is not None and t.shape[1] != width):
+            raise ValueError(f"{what} must be a bf16 tensor "
+                             f"[{'rows' if rows is None else rows}, "
+                             f"{'width' if width is None else width}] of CUDA device "
+                             f"{self.device}")
+        if t.stride(1) != 1 and t.numel() and t.shape[1] > 1:
+            raise ValueError(f"{what}: the values of a row must lie side by side")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+    def _form(self, t, what: str, rows=None, width=None):
+        """A moe_rows of either form, by reference."""
+        if isinstance(t, QuantRows):
+            if t.device != self.device or (rows is not None and t.shape[0] != rows) or \
+                    (width is not None and t.shape[1] != width):
+                raise ValueError(f"{what} must be QuantRows [{rows}, {width}] of CUDA device "
+                                 f"{self.device}")
+            return ctypes.byref(t._c)
+        stride = self._rows2(t, what, rows, width)
+        return ctypes.byref(moe_rows(t.data_ptr(), stride, None, None))
+
+    def _new(self, rows: int, width: int, quantize: bool = False):
+        dev = torch.device("cuda", self.device)
+        if quantize:
+            return QuantRows.empty(rows, width, dev)
+        return torch.empty((rows, width), dtype=torch.bfloat16, device=dev)
+
+    def _order(self, order: ExpertOrder):
+        if not isinstance(order, ExpertOrder) or order.device != self.device or \
+                order._shape != (self.n_experts, self.top_k):
+            raise ValueError(f"the order must be of {self.n_experts} experts, top {self.top_k}, "
+                             f"on CUDA device {self.device}")
+        return order._ref
+
+    def _floats(self, t, what: str, tokens: int) -> int:
+        if t.dtype is not torch.float32 or t.get_device() != self.device or \
+                t.shape != (tokens, self.top_k) or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous fp32 tensor [{tokens}, {self.top_k}] "
+                             f"of CUDA device {self.device}")
+        return t.data_ptr()
+
+    def sort(self, idx: torch.Tensor, order: ExpertOrder | None = None, stream=None):
+        """The order of idx (int32 [tokens, top_k], as MoELayer.route returns it)."""
+        return self._dispatch(None, idx, False, None, order, stream)[0]
+
+    def dispatch(self, x: torch.Tensor, idx: torch.Tensor, quantize: bool = False, out=None,
+                 order: ExpertOrder | None = None, stream=None):
+        """Token rows x [tokens, width] to their experts: (order, rows [tokens x top_k, width]).
+        Rows behind order.starts[-1] are left as they were."""
+        return self._dispatch(x, idx, quantize, out, order, stream)
+
+    def _dispatch(self, x, idx, quantize, out, order, stream):
+        if idx.dtype is not torch.int32 or idx.get_device() != self.device or idx.dim() != 2 or \
+                idx.shape[1] != self.top_k or not idx.is_contiguous():
+            raise ValueError(f"idx must be a contiguous int32 tensor [tokens, {self.top_k}] of "
+                             f"CUDA device {self.device}")
+        tokens = idx.shape[0]
+        if order is None:
+            order = ExpertOrder.empty(self.n_experts, tokens, self.top_k, idx.device)
+            if tokens == 0:
+                order.starts.zero_()
+        ref = self._order(order)
+        if order.tokens != tokens:
+            raise ValueError("the order is of another number of tokens")
+        ptr, stride, width, form = None, 0, 0, None
+        if x is not None:
+            stride, width = self._rows2(x, "x", tokens), x.shape[1]
+            out = self._new(tokens * self.top_k, width, quantize) if out is None else out
+            ptr, form = x.data_ptr(), self._form(out, "out", tokens * self.top_k, width)
+        rc = self._lib.moe_dispatch(self.ctx, idx.data_ptr(), ptr, stride, width, ref, form,
+                                    self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_dispatch")
+        return order, out
+
+    def dispatch_grad(self, drows: torch.Tensor, order: ExpertOrder,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gradient of dispatch's x: each token's rows added up."""
+        ref, width = self._order(order), drows.shape[-1]
+        stride = self._rows2(drows, "drows", order.tokens * self.top_k)
+        out = self._new(order.tokens, width) if out is None else out
+        rc = self._lib.moe_dispatch_grad(self.ctx, drows.data_ptr(), stride, ref, width,
+                                         out.data_ptr(),
+                                         self._rows2(out, "out", order.tokens, width),
+                                         self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_dispatch_grad")
+        return out
+
+    def combine(self, rows: torch.Tensor, order: ExpertOrder, weights: torch.Tensor,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The experts' rows [tokens x top_k, width] back to tokens, by weights [tokens, top_k]."""
+        ref, width = self._order(order), rows.shape[-1]
+        stride = self._rows2(rows, "rows", order.tokens * self.top_k)
+        out = self._new(order.tokens, width) if out is None else out
+        rc = self._lib.moe_combine(self.ctx, rows.data_ptr(), stride, ref,
+                                   self._floats(weights, "weights", order.tokens), width,
+                                   out.data_ptr(), self._rows2(out, "out", order.tokens, width),
+                                   self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_combine")
+        return out
+
+    def combine_grad(self, dy: torch.Tensor, rows: torch.Tensor, order: ExpertOrder,
+                     weights: torch.Tensor, quantize: bool = False, out=None,
+                     dweights: torch.Tensor | None = None, stream=None):
+        """The gradients of combine: (drows, dweights)."""
+        ref, width, pairs = self._order(order), rows.shape[-1], order.tokens * self.top_k
+        stride = self._rows2(rows, "rows", pairs)
+        out = self._new(pairs, width, quantize) if out is None else out
+        if dweights is None:
+            dweights = torch.empty_like(weights)
+        rc = self._lib.moe_combine_grad(
+            self.ctx, dy.data_ptr(), self._rows2(dy, "dy", order.tokens, width), rows.data_ptr(),
+            stride, ref, self._floats(weights, "weights", order.tokens), width,
+            self._form(out, "out", pairs, width),
+            self._floats(dweights, "dweights", order.tokens), self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_combine_grad")
+        return out, dweights
+
+    def _product(self, call, what, x, w, starts, out, transposed, stream):
+        if not isinstance(w, BlockWeights) or w.device != self.device:
+            raise ValueError(f"w must be BlockWeights of CUDA device {self.device}")
+        inner, outer = (w.out, w.inner) if transposed else (w.inner, w.out)
+        if starts is not None and (
+                starts.dtype is not torch.int32 or starts.get_device() != self.device or
+                starts.shape != (w.groups + 1,) or not starts.is_contiguous()):
+            raise ValueError(f"starts must be a contiguous int32 tensor [{w.groups + 1}] of CUDA "
+                             f"device {self.device}")
+        rows = x.shape[0]
+        form = self._form(x, "the rows", rows, inner)
+        out = self._new(rows, outer) if out is None else out
+        rc = call(self.ctx, form, w._ref, None if starts is None else starts.data_ptr(), rows,
+                  out.data_ptr(), self._rows2(out, "out", rows, outer), self._at(stream))
+        if rc:
+            raise MoEError(rc, what)
+        return out
+
+    def linear(self, x, w: BlockWeights, starts: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x [rows, in] (bf16 or QuantRows) times W^T: [rows, out] in bf16.  Several groups of
+        weights take the rows starts[g] .. starts[g + 1] - 1 each (an order's starts)."""
+        return self._product(self._lib.moe_linear, "moe_linear", x, w, starts, out, False, stream)
+
+    def linear_grad(self, dy, w: BlockWeights, starts: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gradient of linear's x: dy [rows, out] (bf16 or QuantRows) times W."""
+        return self._product(self._lib.moe_linear_grad, "moe_linear_grad", dy, w, starts, out,
+                             True, stream)
+
+    def swiglu(self, gate_up: torch.Tensor, quantize: bool = False, out=None, stream=None):
+        """silu(gate) x up of gate_up [rows, 2 width]: [rows, width]."""
+        stride = self._rows2(gate_up, "gate_up")
+        rows, width = gate_up.shape[0], gate_up.shape[1] // 2
+        if gate_up.shape[1] % 2:
+            raise ValueError("gate_up holds as many gates as ups")
+        out = self._new(rows, width, quantize) if out is None else out
+        rc = self._lib.moe_swiglu(self.ctx, gate_up.data_ptr(), stride, rows, width,
+                                  self._form(out, "out", rows, width), self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_swiglu")
+        return out
+
+    def swiglu_grad(self, dh: torch.Tensor, gate_up: torch.Tensor, quantize: bool = False,
+                    out=None, stream=None):
+        """The gradient of swiglu's gate_up."""
+        stride = self._rows2(dh, "dh")
+        rows, width = dh.shape
+        out = self._new(rows, 2 * width, quantize) if out is None else out
+        rc = self._lib.moe_swiglu_grad(self.ctx, dh.data_ptr(), stride, gate_up.data_ptr(),
+                                       self._rows2(gate_up, "gate_up", rows, 2 * width), rows,
+                                       width, self._form(out, "out", rows, 2 * width),
+                                       self._at(stream))
+        if rc:
+            raise MoEError(rc, "moe_swiglu_grad")
+        return out
+
+    def device_status(self) -> int:
+        return moe_ops_last_device_status(self.ctx)

@@ -3,18 +3,15 @@
 // Conventions as in moe_api.cu: unsupported shapes are refused when the context
 // is created, sizes are checked against the cap before anything is allocated,
 // and every refusal is a status code.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 #include <new>
 #include <vector>
 
+#include "api_host.h"
 #include "attn_internal.cuh"
 #include "rope_turns.h"
-#include "row_overlap.h"
 
 using namespace moe;
 
@@ -51,18 +48,6 @@ constexpr int kDecTileRows = kAttnSlotRows;
 // hence from 3, 4 and 6 tiles on.
 constexpr bool prompt_tiles(int head_dim, long long tiles) { return tiles > 1 + head_dim / 64; }
 
-struct Device {
-  int prev = -1;
-  bool ok = false;
-  explicit Device(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~Device() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
 bool supported(const moe_attn_config* c) {
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return false;
   if (c->kv_heads < 1 || c->kv_heads > 64) return false;
@@ -98,8 +83,6 @@ struct Sizes {
   size_t total() const { return turns + q + part_o + part_sums + shared + status; }
 };
 
-size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
-
 Sizes sizes_of(const moe_attn_config* c) {
   Sizes s;
   const size_t slots = 2 * (size_t)kAttnMaxCtas;
@@ -132,19 +115,6 @@ std::vector<unsigned long long> turn_table(const moe_attn_config& c) {
 RopeArgs rope_args(const moe_attn* c) {
   return RopeArgs{c->turns, c->cfg.rotary_dim, c->cfg.rope_layout == MOE_ROPE_INTERLEAVED,
                   (float)c->cfg.rope_amplitude};
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-bool rows_ok(const void* p, int64_t stride, int64_t width) {
-  return p && aligned16(p) && stride >= width && stride % 8 == 0;
-}
-
-// Whether two arrays of rows (row stride and width in bf16 values) share a byte.
-bool overlap_rows(const void* a, int64_t as, int64_t aw, const void* b, int64_t bs, int64_t bw,
-                  int rows) {
-  return rows_overlap(reinterpret_cast<uintptr_t>(a), 2 * as, 2 * aw,
-                      reinterpret_cast<uintptr_t>(b), 2 * bs, 2 * bw, rows);
 }
 
 int check_batch(const moe_attn* c, const moe_kv_cache* k, const moe_attn_batch* b) {
@@ -184,21 +154,6 @@ AttnArgs attn_args(const moe_attn* c, const moe_kv_cache* k, const moe_attn_batc
   a.rows = b->rows;
   a.status = c->status;
   return a;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    cudaGetLastError();
-  });
-  return fn;
 }
 
 bool encode_pool(CUtensorMap* m, const void* pool, const AttnArgs& a, int D, int most) {

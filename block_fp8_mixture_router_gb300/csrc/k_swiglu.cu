@@ -1,0 +1,148 @@
+// Element-wise kernels on rows: the gated activation and its gradient, and the rows'
+// quantisation in front of a product.
+//
+//   h = silu(g) u,  dg = dh u s (1 + g (1 - s)),  du = dh silu(g),  s = 1 / (1 + e^-g)
+//
+// Every value is read and written once, so HBM bounds them.  Eight lanes take a group of
+// 128 columns, 16 values each: the group's largest is then three shuffles away and a lane's
+// loads and stores are 16-byte vectors.
+#include "rows_device.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Unit u = (row, group of 128 columns) of the eight lanes that a thread belongs to.
+struct Unit {
+  int row, c;
+  bool on;
+};
+
+__device__ __forceinline__ Unit unit_of(unsigned u, int rows, int groups) {
+  Unit r;
+  r.row = (int)(u / (unsigned)groups);
+  r.c = (int)(u - (unsigned)r.row * groups) * kGroup + 16 * (int)(threadIdx.x & 7);
+  r.on = r.row < rows;
+  return r;
+}
+
+template <bool kCodes>
+__global__ void __launch_bounds__(kThreads) k_swiglu(const bf16* gu, int64_t gu_stride, int rows,
+                                                     int width, RowsOut out) {
+  const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(width));
+  const bf16* row = gu + (int64_t)u.row * gu_stride;
+  const Vec16 rg = load16(row, u.c, width, u.on), ru = load16(row + width, u.c, width, u.on);
+  float g[16], v[16];
+  unpack16(rg, g);
+  unpack16(ru, v);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= silu_f32(g[i]);
+  put16<kCodes>(out, u.row, u.c, width, u.on, v);
+}
+
+// Gradients of 16 gates and of 16 ups.
+__device__ __forceinline__ void swiglu_back(const Vec16& rd, const Vec16& rg, const Vec16& ru,
+                                            float (&dg)[16], float (&du)[16]) {
+  float d[16], g[16], u[16];
+  unpack16(rd, d);
+  unpack16(rg, g);
+  unpack16(ru, u);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float s = sigmoid_f32(g[i]), z = g[i] * s;
+    dg[i] = d[i] * u[i] * (s + z * (1.0f - s));
+    du[i] = d[i] * z;
+  }
+}
+
+// One group of the width at a time, both halves of the output.  In codes the width is a
+// multiple of 128, so that groups of the output lie in one half.
+template <bool kCodes>
+__global__ void __launch_bounds__(kThreads) k_swiglu_grad(const bf16* dh, int64_t dh_stride,
+                                                          const bf16* gu, int64_t gu_stride,
+                                                          int rows, int width, RowsOut out) {
+  const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(width));
+  const bf16* row = gu + (int64_t)u.row * gu_stride;
+  const Vec16 rd = load16(dh + (int64_t)u.row * dh_stride, u.c, width, u.on);
+  const Vec16 rg = load16(row, u.c, width, u.on), ru = load16(row + width, u.c, width, u.on);
+  float dg[16], du[16];
+  swiglu_back(rd, rg, ru, dg, du);
+  if constexpr (kCodes) {
+    put16<true>(out, u.row, u.c, 2 * width, u.on, dg);
+    put16<true>(out, u.row, width + u.c, 2 * width, u.on, du);
+  } else {
+    RowsOut half = out;
+    put16<false>(half, u.row, u.c, width, u.on, dg);
+    half.v += width;
+    put16<false>(half, u.row, u.c, width, u.on, du);
+  }
+}
+
+// Codes at other widths (multiples of 16): one group of the output's 2 x width columns at a
+// time; the group on the border holds gradients of gates and of ups.
+__global__ void __launch_bounds__(kThreads) k_swiglu_grad_mixed(const bf16* dh, int64_t dh_stride,
+                                                                const bf16* gu, int64_t gu_stride,
+                                                                int rows, int width, RowsOut out) {
+  const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(2 * width));
+  const bool up = u.c >= width, on = u.on && u.c < 2 * width;
+  const int c = up ? u.c - width : u.c;
+  const bf16* row = gu + (int64_t)u.row * gu_stride;
+  const Vec16 rd = load16(dh + (int64_t)u.row * dh_stride, c, width, on);
+  const Vec16 rg = load16(row, c, width, on), ru = load16(row + width, c, width, on);
+  float dg[16], du[16];
+  swiglu_back(rd, rg, ru, dg, du);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dg[i] = up ? du[i] : dg[i];
+  put16<true>(out, u.row, u.c, 2 * width, u.on, dg);
+}
+
+__global__ void __launch_bounds__(kThreads) k_quant_rows(const bf16* x, int64_t x_stride, int rows,
+                                                         int width, RowsOut out) {
+  const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(width));
+  float v[16];
+  unpack16(load16(x + (int64_t)u.row * x_stride, u.c, width, u.on), v);
+  put16<true>(out, u.row, u.c, width, u.on, v);
+  pdl_trigger();
+}
+
+unsigned grid_of(int rows, int width) {
+  constexpr size_t per = kThreads / 8;
+  return (unsigned)(((size_t)rows * groups_of(width) + per - 1) / per);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(const bf16* gu, int64_t gu_stride, int rows, int width,
+                          const RowsOut& out, cudaStream_t s) {
+  const unsigned grid = grid_of(rows, width);
+  if (out.v)
+    k_swiglu<false><<<grid, kThreads, 0, s>>>(gu, gu_stride, rows, width, out);
+  else
+    k_swiglu<true><<<grid, kThreads, 0, s>>>(gu, gu_stride, rows, width, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_grad(const bf16* dh, int64_t dh_stride, const bf16* gu,
+                               int64_t gu_stride, int rows, int width, const RowsOut& out,
+                               cudaStream_t s) {
+  const unsigned grid = grid_of(rows, width);
+  if (out.v)
+    k_swiglu_grad<false><<<grid, kThreads, 0, s>>>(dh, dh_stride, gu, gu_stride, rows, width, out);
+  else if (width % kGroup == 0)
+    k_swiglu_grad<true><<<grid, kThreads, 0, s>>>(dh, dh_stride, gu, gu_stride, rows, width, out);
+  else
+    k_swiglu_grad_mixed<<<grid_of(rows, 2 * width), kThreads, 0, s>>>(dh, dh_stride, gu, gu_stride,
+                                                                      rows, width, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quant_rows(const bf16* x, int64_t x_stride, int rows, int width,
+                              uint8_t* codes, float* scales, cudaStream_t s) {
+  k_quant_rows<<<grid_of(rows, width), kThreads, 0, s>>>(x, x_stride, rows, width,
+                                                         RowsOut{nullptr, 0, codes, scales});
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,85 @@
+// Device helpers of kernels that work through rows of bf16 values 16 to a lane: loads,
+// stores, and the quantisation of a group of 128 by eight lanes.
+#pragma once
+
+#include "moe_device.cuh"
+#include "ops_internal.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ void unpack8(const uint4& r, float* v) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Columns c .. c + 15 of a row of `width` values (a multiple of 8) as two vectors; zeros
+// behind its end.
+struct Vec16 {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ Vec16 load16(const bf16* row, int c, int width, bool on) {
+  Vec16 v = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (on && c < width) v.a = *reinterpret_cast<const uint4*>(row + c);
+  if (on && c + 8 < width) v.b = *reinterpret_cast<const uint4*>(row + c + 8);
+  return v;
+}
+
+__device__ __forceinline__ void unpack16(const Vec16& r, float (&v)[16]) {
+  unpack8(r.a, v);
+  unpack8(r.b, v + 8);
+}
+
+__device__ __forceinline__ void store16(bf16* row, int c, int width, const Vec16& v) {
+  if (c < width) *reinterpret_cast<uint4*>(row + c) = v.a;
+  if (c + 8 < width) *reinterpret_cast<uint4*>(row + c + 8) = v.b;
+}
+
+__device__ __forceinline__ Vec16 pack16(const float (&v)[16]) { return {pack8(v), pack8(v + 8)}; }
+
+// Codes and scale of a group of 128 values, 16 in each of eight neighbouring lanes (the
+// whole warp calls).
+__device__ __forceinline__ uint4 quant16(const float (&v)[16], float* scale) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = group_scale(m);
+  *scale = s;
+  return make_uint4(quant4(v[0], v[1], v[2], v[3], s), quant4(v[4], v[5], v[6], v[7], s),
+                    quant4(v[8], v[9], v[10], v[11], s), quant4(v[12], v[13], v[14], v[15], s));
+}
+
+// Columns c .. c + 15 of row r of the output, whole groups of eight lanes at a time (the
+// whole warp calls; `on` is the same for the lanes of a group).
+template <bool kCodes>
+__device__ __forceinline__ void put16(const RowsOut& out, size_t r, int c, int width, bool on,
+                                      const float (&v)[16]) {
+  if constexpr (kCodes) {
+    float s;
+    const uint4 q = quant16(v, &s);
+    if (on && c < width) {
+      *reinterpret_cast<uint4*>(out.codes + r * width + c) = q;
+      if ((threadIdx.x & 7) == 0) out.scales[r * groups_of(width) + c / kGroup] = s;
+    }
+  } else if (on) {
+    store16(out.v + (int64_t)r * out.stride, c, width, pack16(v));
+  }
+}
+
+}  // namespace moe

@@ -607,6 +607,174 @@ int moe_attn_last_device_status(moe_attn* ctx);
  * thread that owns the modules releases them). */
 void moe_attn_destroy(moe_attn* ctx);
 
+/* ---- the layer's parts as operators of their own ------------------------------
+ *
+ * For experts and projections that the layer's own calls do not cover, and for their
+ * gradients: rows to their experts and back (moe_dispatch, moe_combine), the block-FP8
+ * product, dense or each row by its expert's weights (moe_linear), and the gated activation
+ * between two of them (moe_swiglu).  moe_route gives the experts and weights,
+ * moe_add_rmsnorm_quantize and moe_quantize write codes and scales that moe_linear takes.
+ * Weights in 8 bits are constants: no call has a gradient for them.
+ *
+ * Rows come in one of two forms: bf16, or e4m3 codes with one fp32 scale for each 128
+ * values of a row (the last group of a row may be shorter), a value being code x scale.
+ * Quantising, as moe_quantize: scale = amax / 448 of the group (1 where all are zero),
+ * codes = e4m3(value / scale), both quotients rounded to fp32.  A group that holds an
+ * infinity or NaN makes every result that takes it NaN.  In a gradient, quantising counts as
+ * the identity.
+ *
+ * A call reads and writes the rows it names and no others.  Arrays of one call share no
+ * byte (MOE_ERR_INVALID_ARG where the library sees it: rows read and rows written). */
+typedef struct {
+  int n_experts;  /* 1..256 */
+  int top_k;      /* 1..16: pairs of a token; need not be distinct experts */
+  int max_rows;   /* 1..65536: most tokens of one call; products take max_rows x top_k rows */
+  int max_width;  /* widest contraction of a product from bf16 rows, a multiple of 16, at most
+                     65536 (0: products from codes only); sizes the workspace */
+  size_t workspace_cap_bytes; /* 0 = no cap */
+} moe_ops_config;
+
+/* Rows in one of the two forms, device memory of the caller: `values` (codes and scales
+ * NULL), bf16, 16-byte aligned, row stride in values a multiple of 8 and at least the width,
+ * the width a multiple of 8; or `codes` [rows][width], 16-byte aligned, and `scales`
+ * [rows][ceil(width / 128)] (values NULL), the width a multiple of 16. */
+typedef struct {
+  void* values;
+  int64_t stride;
+  uint8_t* codes;
+  float* scales;
+} moe_rows;
+
+/* W [groups][out][in] in e4m3, 16-byte aligned, with one fp32 scale per 128 x 128 block,
+ * [groups][ceil(out / 128)][ceil(in / 128)], as a block-FP8 checkpoint stores it.
+ * Supported: 1..256 groups; out and in multiples of 16, at most 65536. */
+typedef struct {
+  const uint8_t* codes;
+  const float* scales;
+  int groups;
+  int out;
+  int in;
+} moe_block_weights;
+
+/* Which row belongs to which (token, rank) pair t * top_k + j, device arrays of the caller:
+ * rows are sorted by expert, and within an expert by pair.  Expert e has rows starts[e] ..
+ * starts[e + 1] - 1 (starts[n_experts + 1]); pair_of_slot[row] is the row's pair, -1 behind
+ * the last row; slot_of_pair[pair] the pair's row, -1 where the pair has no expert in
+ * 0..n_experts - 1 (a padding token, or another rank's expert).  Both [tokens x top_k]. */
+typedef struct {
+  int32_t* starts;
+  int32_t* pair_of_slot;
+  int32_t* slot_of_pair;
+  int tokens;
+} moe_order;
+
+/* Bytes moe_ops_create would allocate for `cfg`.
+ * Defined by: PR #925 "drama: load the checkpoint with direct I/O in file
+ * order and build the codec on its own thread", conversation, the
+ * allocation-cap commit (an engine admits a model against a memory budget). */
+int moe_ops_required_bytes(const moe_ops_config* cfg, size_t* bytes);
+
+/* Validate `cfg`, allocate the workspace.  Refusals and ownership as in moe_create.
+ * Synchronous.  A context is used by one stream at a time; it holds no weights, so layers
+ * that run one after the other can share it.
+ * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA GPU", section
+ * "What it adds" (the router and the experts' products as kernels of their own). */
+typedef struct moe_ops moe_ops;
+int moe_ops_create(const moe_ops_config* cfg, int device, moe_ops** out);
+
+/* Sort the pairs of idx int32 [tokens][top_k] by expert into `order` (written), and copy
+ * token rows x bf16 [tokens][width] (row stride in values) to their pairs' rows:
+ * rows[slot_of_pair[t * top_k + j]] = x[t], in bf16 or quantised.  Any idx is allowed: one
+ * outside 0..n_experts - 1 has no row.  Rows behind starts[n_experts] are left as they
+ * were; `rows` has room for tokens x top_k.  x NULL: the order only (rows and width are
+ * not looked at).  tokens == 0 does nothing (starts is then not written).  Asynchronous.
+ * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA GPU", section
+ * "What it adds" (fp8_experts.cu on FP8 rows); the commit "the Drama 3 text backbone on
+ * CUDA" (dynamic 1 x 128 FP8 activation quantization). */
+int moe_dispatch(moe_ops* ctx, const int32_t* idx, const void* x, int64_t x_stride, int width,
+                 const moe_order* order, const moe_rows* rows, void* stream);
+
+/* Its gradient: dx[t] = sum_j drows[slot_of_pair[t * top_k + j]] over the pairs with a row
+ * (zeros where a token has none), added in rank order in fp32 and rounded to bf16 once.
+ * drows bf16 [tokens x top_k][width], dx bf16 [tokens][width], row strides in values.
+ * Asynchronous.
+ * Defined by: the operation of moe_dispatch (commit "the Drama 3 text backbone on CUDA");
+ * gradients are this library's. */
+int moe_dispatch_grad(moe_ops* ctx, const void* drows, int64_t drows_stride,
+                      const moe_order* order, int width, void* dx, int64_t dx_stride,
+                      void* stream);
+
+/* The experts' rows back to their tokens: y[t] = sum_j weights[t][j] rows[slot_of_pair[t *
+ * top_k + j]], as moe_dispatch_grad, weights fp32 [tokens][top_k].  The weight of a pair
+ * without a row is not looked at.  Asynchronous.
+ * Defined by: commit "MoE combine on 8-wide vectors" (every sum keeps its order). */
+int moe_combine(moe_ops* ctx, const void* rows, int64_t rows_stride, const moe_order* order,
+                const float* weights, int width, void* y, int64_t y_stride, void* stream);
+
+/* Its gradients: drows[slot] = weights[t][j] dy[t] (bf16, or quantised from the fp32
+ * product; rows without a pair are left as they were) and dweights[t][j] = dy[t] . rows[slot]
+ * (fp32 sums; 0 where the pair has no row).  dy bf16 [tokens][width], rows bf16
+ * [tokens x top_k][width], dweights fp32 [tokens][top_k].  Asynchronous.
+ * Defined by: the operation of moe_combine (commit "MoE combine on 8-wide vectors");
+ * gradients are this library's. */
+int moe_combine_grad(moe_ops* ctx, const void* dy, int64_t dy_stride, const void* rows,
+                     int64_t rows_stride, const moe_order* order, const float* weights, int width,
+                     const moe_rows* drows, float* dweights, void* stream);
+
+/* y[r] = x[r] W_g^T for the rows r of group g, starts[g] .. starts[g + 1] - 1:
+ *   y[r][n] = sum_b sx[r][b] sw[g][n / 128][b] sum_{c in block b} xc[r][c] wc[g][n][c]
+ * over the blocks b of 128 along `in`; fp32 sums, one rounding to bf16.  x [rows][in] in
+ * either form (bf16 rows are quantised on the way, into the workspace); y bf16 [rows][out],
+ * row stride in values.  starts int32 [groups + 1] on the device, ascending, as moe_order
+ * holds it; NULL with one group: every row.  Rows of no group are left as they were.  A
+ * start outside 0..rows or a descending one touches no memory outside the buffers, and
+ * moe_ops_last_device_status returns MOE_ERR_INVALID_ARG.  0 <= rows <= max_rows x top_k.
+ * Results are bitwise identical from run to run.  Asynchronous.
+ * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA GPU", section
+ * "Precision" (e4m3 per row and per 128 inputs, amax / 448); the commit "the Drama 3 text
+ * backbone on CUDA" (block-FP8 weights, used as stored). */
+int moe_linear(moe_ops* ctx, const moe_rows* x, const moe_block_weights* w, const int32_t* starts,
+               int rows, void* y, int64_t y_stride, void* stream);
+
+/* The gradient for its rows: dx[r] = dy[r] W_g, with dy [rows][out] in either form (bf16 is
+ * quantised along `out`) and the same weights, read as they are stored; dx bf16 [rows][in].
+ * Otherwise as moe_linear.
+ * Defined by: the operation of moe_linear (commit "the Drama 3 text backbone on CUDA");
+ * gradients are this library's. */
+int moe_linear_grad(moe_ops* ctx, const moe_rows* dy, const moe_block_weights* w,
+                    const int32_t* starts, int rows, void* dx, int64_t dx_stride, void* stream);
+
+/* h = silu(gate) x up in fp32: gate_up bf16 [rows][2 width], the gates in front of the ups
+ * as a product with moe_weights' w13 leaves them; h [rows][width], rounded to bf16 or
+ * quantised once.  rows <= max_rows x top_k, width <= 65536.  Asynchronous.
+ * Defined by: commit "one SwiGLU launch for the routed and shared experts" (routed rows are
+ * stored as their FP8 quantization). */
+int moe_swiglu(moe_ops* ctx, const void* gate_up, int64_t gate_up_stride, int rows, int width,
+               const moe_rows* h, void* stream);
+
+/* Its gradient: with s = 1 / (1 + e^-gate), dgate = dh up s (1 + gate (1 - s)) and
+ * dup = dh gate s, side by side as [rows][2 width] in either form (128 columns of the 2 width
+ * share a scale); dh bf16 [rows][width].  Asynchronous.
+ * Defined by: the operation of moe_swiglu (commit "one SwiGLU launch for the routed and
+ * shared experts"); gradients are this library's. */
+int moe_swiglu_grad(moe_ops* ctx, const void* dh, int64_t dh_stride, const void* gate_up,
+                    int64_t gate_up_stride, int rows, int width, const moe_rows* dgate_up,
+                    void* stream);
+
+/* Device-side status of the context: MOE_OK; MOE_ERR_INVALID_ARG if a call's starts were not
+ * ascending within its rows or a slot lay outside them; MOE_ERR_DEVICE_TIMEOUT if a bounded
+ * wait gave up.  Synchronises the context's last stream and clears the flag.
+ * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA
+ * GPU", conversation, the follow-up fixes (a bad value is refused by name with
+ * an error, not trapped on). */
+int moe_ops_last_device_status(moe_ops* ctx);
+
+/* Release everything the context owns.  NULL is accepted.
+ * Defined by: PR #925 "drama: load the checkpoint with direct I/O in file
+ * order and build the codec on its own thread", conversation (the worker
+ * thread that owns the modules releases them). */
+void moe_ops_destroy(moe_ops* ctx);
+
 /* Static text for a status code.
  * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA
  * GPU", conversation, the follow-up fixes (errors refused by name). */
