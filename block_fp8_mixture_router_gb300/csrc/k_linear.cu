@@ -14,7 +14,7 @@
 // them, want a scale from shared memory for every column.)
 //
 // Warps: 0-7 the sums and the store (warp w: lanes 32 (w % 4) and on, columns 128 (w / 4)
-// and on), 8 the TMA loads, 9 the MMAs.  Persistent: a CTA takes tiles blockIdx.x,
+// and on), 8 the TMA loads, 9 and 10 the MMAs, 11 the scales.  Persistent: a CTA takes tiles blockIdx.x,
 // + gridDim.x, ..; the tiles of a group's 128 rows lie next to each other.
 #include "attn_tc.cuh"
 #include "ops_internal.cuh"
@@ -25,19 +25,29 @@ namespace {
 
 constexpr int kBM = 128, kBN = 256, kKB = 128;
 constexpr int kSumWarps = 8;
-constexpr int kThreads = 32 * (kSumWarps + 2);
-constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1;
+constexpr int kThreads = 32 * (kSumWarps + 4);
+constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1, kWarpScale = kSumWarps + 3;
+// Registers of a thread: twelve warps start with 168 (65536 / 384, by eights); the two
+// warpgroups that hold 128 sums and 64 products on their way give and take with the third.
+constexpr int kSumRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "no more registers than at launch");
 constexpr int kABytes = kBM * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kSmallBox = 32;                  // rows of a small box of x
-constexpr int kOutBytes = 32 * 32 * 2;         // a warp's piece of the output: 32 x 32
+constexpr int kOutBytes = 32 * 128 * 2;        // a warp's piece of the output: 32 x 128
 constexpr uint32_t kIdescBMajorN = 1u << 16;
+
+struct Tile {
+  int g, f, row0, n;  // group, column tile, first row, rows
+};
 
 struct LinSmem {
   uint64_t full[kStages], empty[kStages];
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
   int abort;
+  Tile tile[4];                // tiles j, j + 1, .. of this CTA, by j % 4
+  float scale[2][2][kBM];      // of a buffer's products, by column half and row
   int pre[kMaxExperts + 1];    // row tiles in front of each group
   int start[kMaxExperts + 1];  // the group's first row
   int count[kMaxExperts];
@@ -45,10 +55,6 @@ struct LinSmem {
 constexpr size_t kSmemBytes =
     1024 + (size_t)kStages * kStageBytes + kSumWarps * kOutBytes + sizeof(LinSmem);
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-
-struct Tile {
-  int g, f, row0, n;  // group, column tile, first row, rows
-};
 
 __device__ __forceinline__ Tile tile_of(const LinSmem& sm, int groups, int cols, int w) {
   const int t = w / cols;
@@ -109,31 +115,82 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, LinSmem
   return !__any_sync(0xffffffffu, !ok);
 }
 
-// A warp's 32 x 32 outputs (lane: row) through its piece of shared memory, so that stores
-// cover 64 bytes of each of eight rows.  16-byte units of a row are permuted by its number.
-__device__ __forceinline__ void store_piece(uint8_t* piece, const float* v, bf16* y,
-                                            int64_t y_stride, int rows, int cols) {
+template <int kRegs>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+
+// Waits for this warp's TMEM loads.  The registers are operands so that no use of them
+// moves in front of the wait.
+__device__ __forceinline__ void wait_ld_of(uint32_t (&v)[32]) {
+#define MOE_IO8(o)                                                                       \
+  "+r"(v[o + 0]), "+r"(v[o + 1]), "+r"(v[o + 2]), "+r"(v[o + 3]), "+r"(v[o + 4]),        \
+      "+r"(v[o + 5]), "+r"(v[o + 6]), "+r"(v[o + 7])
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : MOE_IO8(0), MOE_IO8(8), MOE_IO8(16), MOE_IO8(24)::"memory");
+#undef MOE_IO8
+}
+
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float s) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(v[j]), s, acc[j]);
+}
+
+// A warp's 32 x 128 outputs (lane: row) to its piece of shared memory, as two boxes of 64
+// columns under the 128-byte swizzle.
+__device__ __forceinline__ void stage_piece(uint8_t* piece, const float (&v)[128]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 16; ++c) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 p = __floats2bfloat162_rn(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    *reinterpret_cast<uint4*>(piece + 64 * lane + 16 * ((c ^ (lane >> 1)) & 3)) =
+    *reinterpret_cast<uint4*>(piece + (c >> 3) * 4096 + 128 * lane + 16 * ((c ^ lane) & 7)) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __syncwarp();
-  const int c = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    const uint4 q = *reinterpret_cast<const uint4*>(piece + 64 * r + 16 * ((c ^ (r >> 1)) & 3));
-    if (r < rows && 8 * c < cols) *reinterpret_cast<uint4*>(y + (int64_t)r * y_stride + 8 * c) = q;
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x,
+                                             int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n" ::
+                   "l"(reinterpret_cast<uint64_t>(map)),
+               "r"(tc::smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+
+// The staged piece to rows row .. row + 31 of y (the first `rows` of them) from column c0 on.
+// Whole pieces go by TMA, which cuts off columns behind the last one; a piece that ends
+// inside has its rows copied, since the rows behind are another group's.
+__device__ __forceinline__ void send_piece(const LinArgs& a, const uint8_t* piece, int row,
+                                           int rows, int c0) {
+  const int lane = threadIdx.x & 31, cols = a.outer - c0;
+  if (rows >= 32) {
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&a.out, piece, c0, row);
+      if (cols > 64) tma_store_2d(&a.out, piece + 4096, c0 + 64, row);
+      asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+    }
+    return;
   }
   __syncwarp();
+  bf16* y = a.y + (int64_t)row * a.y_stride + c0;
+  const int c = lane & 7;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = 4 * (i & 7) + (lane >> 3), h = i >> 3;
+    if (r < rows && 64 * h + 8 * c < cols)
+      *reinterpret_cast<uint4*>(y + (int64_t)r * a.y_stride + 64 * h + 8 * c) =
+          *reinterpret_cast<const uint4*>(piece + 4096 * h + 128 * r + 16 * ((c ^ r) & 7));
+  }
 }
 
 template <bool kTrans>
@@ -150,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
       tc::mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.tfull[i], 1);
+      tc::mbar_init(&sm.tfull[i], 2);  // the MMAs' commit and the scale warp
       tc::mbar_init(&sm.tempty[i], kSumWarps);
     }
     sm.abort = 0;
@@ -158,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
     tc::tma_prefetch_map(&a.x);
     tc::tma_prefetch_map(&a.xs);
     tc::tma_prefetch_map(&a.w);
+    tc::tma_prefetch_map(&a.out);
   }
   if (warp == kWarpMma) {
     __syncwarp();
@@ -172,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
   const int cols = (a.outer + kBN - 1) / kBN, blocks = (a.inner + kKB - 1) / kKB;
   const int tiles = sm.pre[a.groups] * cols;
 
+  if (warp >= kSumWarps) fewer_regs<kOtherRegs>();
   if (warp == kWarpTma) {
     uint32_t st = 0, ph = 0;
     int issued = 0;
@@ -221,18 +280,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
         }
       }
     }
-  } else if (warp == kWarpMma) {
-    const uint32_t leader = lane == 0;
+  } else if (warp < kWarpScale && warp >= kWarpMma) {
+    // Two warps take the blocks in turn, one for each buffer: an issuing warp waits for the
+    // tensor cores to take its MMAs, then pays for two commits and two barrier waits, and
+    // the other's MMAs run meanwhile.
+    const uint32_t leader = lane == 0, tb = warp - kWarpMma;
     const tc::Desc da = tc::desc_of(tc::smem_u32(stages), true);
     const tc::Desc db = tc::desc_of(tc::smem_u32(stages + kABytes), true,
                                     kTrans ? kBBytes / 2 : 16);
-    uint32_t st = 0, ph = 0, tb = 0, tph = 0;
+    uint32_t st = tb % kStages, ph = 0, tph = 0, turn = 0;
     bool ok = true;
     for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x) {
       const int left = a.outer - (w % cols) * kBN;
       const uint32_t idesc = tc::idesc_f8(kBM, left > kBN / 2 ? kBN : kBN / 2) |
                              (kTrans ? kIdescBMajorN : 0u);
-      for (int b = 0; b < blocks; ++b) {
+      for (int b = 0; b < blocks; ++b, turn ^= 1u) {
+        if (turn != tb) continue;
         ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status) &&
              wait_all(&sm.full[st], ph, sm, a.status);
         if (!ok) break;
@@ -243,60 +306,126 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
           // 32 values along a row of 128 bytes; 32 rows of them where the rows run along N
           tc::mma_ss<true>(tmem + tb * kBN, xa + 32 * k, xb + (kTrans ? 32 * kKB : 32) * k, idesc,
                            k > 0, leader);
-        tc::commit_by(&sm.empty[st], leader);
         tc::commit_by(&sm.tfull[tb], leader);
-        if (++st == kStages) { st = 0; ph ^= 1u; }
-        if ((tb ^= 1u) == 0) tph ^= 1u;
+        tc::commit_by(&sm.empty[st], leader);
+        tph ^= 1u;
+        st += 2;
+        if (st >= kStages) { st -= kStages; ph ^= 1u; }
+      }
+    }
+  } else if (warp == kWarpScale) {
+    // Scales: a lane has rows lane, + 32, + 64 and + 96 of every tile.  Those of two blocks
+    // are loaded while the two in front of them are written.
+    constexpr int kAhead = 2;
+    const int nb_out = (a.outer + kGroup - 1) / kGroup;
+    const int sw_step = kTrans ? nb_out : 1;
+    uint32_t tb = 0, tph = 0;
+    bool ok = true;
+    int j = 0;
+    for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x, ++j) {
+      const Tile t = tile_of(sm, a.groups, cols, w);
+      if (lane == 0) sm.tile[j & 3] = t;
+      const float* sx[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        sx[r] = a.sx + (size_t)(t.row0 + min(lane + 32 * r, t.n - 1)) * blocks;
+      const int cb = 2 * t.f, cb1 = min(cb + 1, nb_out - 1);
+      const float* sw = a.sw + (size_t)t.g * nb_out * blocks;
+      const float* sw0 = sw + (kTrans ? cb : cb * blocks);
+      const float* sw1 = sw + (kTrans ? cb1 : cb1 * blocks);
+      float nx[kAhead][4], nw[kAhead][2];
+      const auto load = [&](int b0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int b = min(b0 + k, blocks - 1);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) nx[k][r] = __ldg(sx[r] + b);
+          nw[k][0] = __ldg(sw0 + (size_t)b * sw_step);
+          nw[k][1] = __ldg(sw1 + (size_t)b * sw_step);
+        }
+      };
+      load(0);
+      for (int b0 = 0; b0 < blocks && ok; b0 += kAhead) {
+        float p[kAhead][2][4];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            p[k][0][r] = nx[k][r] * nw[k][0];
+            p[k][1][r] = nx[k][r] * nw[k][1];
+          }
+        if (b0 + kAhead < blocks) load(b0 + kAhead);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (b0 + k >= blocks || !ok) break;
+          ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sm.scale[tb][0][lane + 32 * r] = p[k][0][r];
+            sm.scale[tb][1][lane + 32 * r] = p[k][1][r];
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.tfull[tb]);
+          if ((tb ^= 1u) == 0) tph ^= 1u;
+        }
       }
     }
   } else {
+    more_regs<kSumRegs>();
     const int q = warp & 3, half = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * (kBN / 2);
     uint8_t* piece = pieces + warp * kOutBytes;
-    const int nb_out = (a.outer + kGroup - 1) / kGroup;
     uint32_t tb = 0, tph = 0;
-    for (int w = blockIdx.x; w < tiles; w += gridDim.x) {
-      const Tile t = tile_of(sm, a.groups, cols, w);
-      const int r = 32 * q + lane;               // this thread's row of the tile
-      const int c0 = t.f * kBN + half * (kBN / 2);  // this warp's first column
-      const bool live = 32 * q < t.n && c0 < a.outer;  // any output in this warp
-      const float* sx = a.sx + (size_t)(t.row0 + min(r, t.n - 1)) * blocks;
-      const float* sw = a.sw + (size_t)t.g * nb_out * blocks;
-      const int cb = min(c0 / kGroup, nb_out - 1);
-      sw += kTrans ? cb : cb * blocks;
-      const int sw_step = kTrans ? nb_out : 1;
+    int j = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x, ++j) {
       float acc[kBN / 2];
 #pragma unroll
       for (int i = 0; i < kBN / 2; ++i) acc[i] = 0.0f;
-      float next = __ldg(sx) * __ldg(sw);
+      Tile t = {0, 0, 0, 0};
       for (int b = 0; b < blocks; ++b) {
-        const float s = next;
-        if (b + 1 < blocks) next = __ldg(sx + b + 1) * __ldg(sw + (size_t)(b + 1) * sw_step);
-        // (a wait that gave up leaves the sums undefined; the loop still ends)
-        tc::wait_bounded(&sm.tfull[tb], tph, &sm.abort, a.status);
-        __syncwarp();
-        tc::fence_after_sync();
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < kBN / 2; i += 32) {
-            uint32_t v[32];
-            tc::tmem_ld_async(lanes + tb * kBN + i, v);
-            tc::wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[i + j] = fmaf(__uint_as_float(v[j]), s, acc[i + j]);
-          }
+        if (!wait_all(&sm.tfull[tb], tph, sm, a.status)) {
+          ok = false;
+          break;
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
+        tc::fence_after_sync();
+        if (b == 0) t = sm.tile[j & 3];
+        const float s = sm.scale[tb][half][32 * q + lane];
+        if (32 * q < t.n && t.f * kBN + half * (kBN / 2) < a.outer) {  // any output here
+          const uint32_t from = lanes + tb * kBN;
+          uint32_t v0[32], v1[32];
+          tc::tmem_ld_async(from, v0);
+          wait_ld_of(v0);
+          tc::tmem_ld_async(from + 32, v1);
+          add_scaled(acc, v0, s);
+          wait_ld_of(v1);
+          tc::tmem_ld_async(from + 64, v0);
+          add_scaled(acc + 32, v1, s);
+          wait_ld_of(v0);
+          tc::tmem_ld_async(from + 96, v1);
+          add_scaled(acc + 64, v0, s);
+          wait_ld_of(v1);
+          // the buffer is free: the last products are in registers
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
+          add_scaled(acc + 96, v1, s);
+        } else {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
+        }
         if ((tb ^= 1u) == 0) tph ^= 1u;
       }
-      if (!live || sm.abort) continue;
-      bf16* y = a.y + (int64_t)(t.row0 + 32 * q) * a.y_stride + c0;
-#pragma unroll
-      for (int i = 0; i < kBN / 2; i += 32)
-        store_piece(piece, acc + i, y + i, a.y_stride, t.n - 32 * q, a.outer - c0 - i);
+      const int c0 = t.f * kBN + half * (kBN / 2), rows = t.n - 32 * q;
+      if (!ok || rows <= 0 || c0 >= a.outer) continue;
+      // the piece is free once the TMA has read the tile before
+      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      __syncwarp();
+      stage_piece(piece, acc);
+      send_piece(a, piece, t.row0 + 32 * q, rows, c0);
     }
+    asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
   __syncthreads();
   if (warp == kWarpMma) {

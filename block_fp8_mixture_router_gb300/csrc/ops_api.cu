@@ -127,12 +127,14 @@ int combine(moe_ops* c, const void* rows, int64_t rows_stride, const moe_order* 
                                        c->status, s));
 }
 
-bool encode(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims,
+// Boxes of 128 bytes x box_rows rows under the 128-byte swizzle.
+bool encode(CUtensorMap* m, const void* p, bool in_bf16, int rank, const cuuint64_t* dims,
             const cuuint64_t* strides, cuuint32_t box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
   if (!fn) return false;
-  const cuuint32_t box[3] = {128, box_rows, 1}, unit[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(p), dims, strides, box, unit,
+  const cuuint32_t box[3] = {in_bf16 ? 64u : 128u, box_rows, 1}, unit[3] = {1, 1, 1};
+  return fn(m, in_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
+            const_cast<void*>(p), dims, strides, box, unit,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -170,8 +172,10 @@ int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int3
   const cuuint64_t dx[2] = {(cuuint64_t)inner, (cuuint64_t)rows}, sx[1] = {(cuuint64_t)inner};
   const cuuint64_t dw[3] = {(cuuint64_t)w->in, (cuuint64_t)w->out, (cuuint64_t)w->groups};
   const cuuint64_t sw[2] = {(cuuint64_t)w->in, (cuuint64_t)w->in * w->out};
-  if (!encode(&a.x, codes, 2, dx, sx, 128) || !encode(&a.xs, codes, 2, dx, sx, 32) ||
-      !encode(&a.w, w->codes, 3, dw, sw, 128))
+  const cuuint64_t dy[2] = {(cuuint64_t)outer, (cuuint64_t)rows};
+  const cuuint64_t sy[1] = {(cuuint64_t)(rows > 1 ? y_stride : outer) * 2};
+  if (!encode(&a.x, codes, false, 2, dx, sx, 128) || !encode(&a.xs, codes, false, 2, dx, sx, 32) ||
+      !encode(&a.w, w->codes, false, 3, dw, sw, 128) || !encode(&a.out, y, true, 2, dy, sy, 32))
     return MOE_ERR_CUDA;
   if (x->values &&
       launch_quant_rows(static_cast<const bf16*>(x->values), x->stride, rows, inner, c->codes,

@@ -55,6 +55,7 @@ struct LinArgs {
   CUtensorMap x;       // codes [rows][inner], boxes of 128 rows x 128 bytes
   CUtensorMap xs;      // the same in boxes of 32 rows
   CUtensorMap w;       // codes [groups][out][in], boxes of 128 x 128
+  CUtensorMap out;     // y, boxes of 32 rows x 64 values
   const float* sx;     // [rows][ceil(inner / 128)]
   const float* sw;     // [groups][ceil(out / 128)][ceil(in / 128)]
   const int* starts;   // [groups + 1] on the device, or nullptr: one group of all rows
