@@ -5,17 +5,28 @@
 //   y[r][n] = sum_b  sx[r][b] sw[n / 128][b]  sum_{c in block b} x[r][c] W[n][c]
 //   trans:    sx[r][b] sw[b][n / 128]  sum_{c in block b} x[r][c] W[c][n]
 //
-// A tile is 128 rows by 256 outputs.  The scales change with every block of 128 along the
-// contraction, so the MMAs of a block (four of K = 32) write a fresh product into one of two
-// TMEM buffers, and eight warps add it, times its scale, to fp32 sums in registers while the
-// tensor cores fill the other.  With the rows along the TMEM lanes a thread has one row and
-// the columns of one weight block: one scale to a thread and block of the contraction, and
-// one FMA to a product.  (The weights along the lanes, as the layer's own products have
-// them, want a scale from shared memory for every column.)
+// The scales change with every block of 128 along the contraction, so the MMAs of a block
+// (four of K = 32) write fresh products into TMEM, and eight warps add them, times their
+// scale, to fp32 sums in registers.  With the rows along the TMEM lanes a thread has one row
+// and columns of one weight block at a time: one scale to a thread, and one FMA to a product.
+// (The weights along the lanes, as the layer's own products have them, want a scale from
+// shared memory for every column.)
 //
-// Warps: 0-7 the sums and the store (warp w: lanes 32 (w % 4) and on, columns 128 (w / 4)
-// and on), 8 the TMA loads, 9 and 10 the MMAs, 11 the scales.  Persistent: a CTA takes tiles blockIdx.x,
-// + gridDim.x, ..; the tiles of a group's 128 rows lie next to each other.
+// A CTA has 128 rows by 256 columns, a pair of CTAs 256 by 256: each loads its rows and half
+// of the columns' weights, and the first issues the MMAs of both.  The pair halves the
+// weights' way into shared memory, which binds a CTA alone (48 KB of a block at the 64 bytes a
+// clock that an SM takes from L2 are 768 cycles; the block's MMAs take 512).
+// A block's products go to TMEM by column halves, in turn through four buffers of 128
+// columns: the warps copy a buffer to registers, give it back, and multiply while the tensor
+// cores are three halves ahead.  (Two buffers of 256 columns, given back after the FMAs, left
+// either side waiting for the other: 16384 rows x 2048 x 4096 139 us.)
+//
+// Warps: 0-7 the sums and the store (warp w: lanes 32 (w % 4) and on, columns 64 (w / 4) and
+// on of each half), 8 the TMA loads, 9 and 10 the MMAs of the two halves, 11 the scales.
+// Persistent: a CTA, or pair, takes tiles first, first + step, ..; the tiles of a group's rows
+// lie next to each other.
+#include <stdlib.h>
+
 #include "attn_tc.cuh"
 #include "ops_internal.cuh"
 
@@ -23,74 +34,102 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kKB = 128;
+constexpr int kBM = 128, kBN = 256, kKB = 128;   // rows, columns and depth of a CTA's tile
 constexpr int kSumWarps = 8;
-constexpr int kThreads = 32 * (kSumWarps + 4);
 constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1, kWarpScale = kSumWarps + 3;
-// Registers of a thread: twelve warps start with 168 (65536 / 384, by eights); the two
-// warpgroups that hold 128 sums and 64 products on their way give and take with the third.
-constexpr int kSumRegs = 208, kOtherRegs = 88;
-static_assert(2 * kSumRegs + kOtherRegs <= 3 * 168, "no more registers than at launch");
-constexpr int kABytes = kBM * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 3;
+constexpr int kWarpStore = kSumWarps + 4, kStoreWarps = 4;
+constexpr int kThreads = 32 * (kWarpStore + kStoreWarps);
+// Registers of a thread: sixteen warps start with 128; the two warpgroups that hold 128 sums
+// and 64 products on their way take what the others give.
+constexpr int kSumRegs = 216, kFeedRegs = 40, kStoreRegs = 40;
+static_assert(2 * kSumRegs + kFeedRegs + kStoreRegs <= 4 * 128, "no more registers than at launch");
+constexpr int kABytes = kBM * kKB;
+constexpr int kHalf = kBN / 2;                   // columns of a box of weights
+constexpr int kBufs = 512 / kBN;                 // TMEM buffers of a block's products: 2
 constexpr int kSmallBox = 32;                  // rows of a small box of x
 constexpr int kOutBytes = 32 * 128 * 2;        // a warp's piece of the output: 32 x 128
 constexpr uint32_t kIdescBMajorN = 1u << 16;
+
+// A CTA alone, or a pair of CTAs that shares its columns.
+template <bool kPair>
+struct Cfg {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kBRows = kBN / kCtas;      // columns whose weights a CTA loads
+  static constexpr int kBBytes = kBRows * kKB, kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = kPair ? 5 : 3;
+};
 
 struct Tile {
   int g, f, row0, n;  // group, column tile, first row, rows
 };
 
+constexpr int kMaxStages = 5;
+constexpr int kTiles = 8;  // the scales' warp is at most kBufs + 1 tiles ahead of the sums, and they two
+                             // ahead of the stores
 struct LinSmem {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t tfull[2], tempty[2];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[kBufs], tempty[kBufs];
+  uint64_t ofull[kSumWarps], ofree[kSumWarps];  // a warp's piece of the output
+  uint64_t peer_empty[kBufs];  // a pair's first CTA: the second's warps have read the buffer
   uint32_t tmem;
   int abort;
-  Tile tile[4];                // tiles j, j + 1, .. of this CTA, by j % 4
-  float scale[2][2][kBM];      // of a buffer's products, by column half and row
-  int pre[kMaxExperts + 1];    // row tiles in front of each group
-  int start[kMaxExperts + 1];  // the group's first row
-  int count[kMaxExperts];
+  Tile tile[kTiles];           // tiles j, j + 1, .. of this CTA, by j % kTiles
+  float scale[kBufs][2][kBM];  // of a buffer's products, by column half and row
+  unsigned short pre[kMaxExperts + 1];  // row tiles in front of each group
 };
-constexpr size_t kSmemBytes =
-    1024 + (size_t)kStages * kStageBytes + kSumWarps * kOutBytes + sizeof(LinSmem);
-static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+// (The dynamic shared memory of a kernel without any static begins at a multiple of 1024
+// bytes, which the swizzled tiles need; the kernel checks it.)
+template <bool kPair>
+constexpr size_t smem_bytes() {
+  return (size_t)Cfg<kPair>::kStages * Cfg<kPair>::kStageBytes + kSumWarps * kOutBytes +
+         sizeof(LinSmem);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448,
+              "shared memory of a CTA");
 
-__device__ __forceinline__ Tile tile_of(const LinSmem& sm, int groups, int cols, int w) {
+// First row and rows of a group, clamped to the rows there are.
+__device__ __forceinline__ int2 group_rows(const LinArgs& a, int g, bool* bad = nullptr) {
+  if (!a.starts) return make_int2(0, a.rows);
+  const int s0 = __ldg(a.starts + g), s1 = __ldg(a.starts + g + 1);
+  const int r0 = min(max(s0, 0), a.rows), r1 = min(max(s1, r0), a.rows);
+  if (bad) *bad |= r0 != s0 || r1 != s1;
+  return make_int2(r0, r1 - r0);
+}
+
+// Tile w; a pair's tile is its two CTAs' row tiles, this CTA's the one of its rank (n <= 0: it
+// has no rows).
+template <bool kPair>
+__device__ __forceinline__ Tile tile_of(const LinArgs& a, const LinSmem& sm, int cols, int w,
+                                        int rank) {
   const int t = w / cols;
-  int lo = 0, hi = groups;  // the last group with pre <= t
+  int lo = 0, hi = a.groups;  // the last group with pre <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (sm.pre[mid] <= t) lo = mid; else hi = mid;
   }
-  const int j = t - sm.pre[lo];
-  return Tile{lo, w - t * cols, sm.start[lo] + kBM * j, min(kBM, sm.count[lo] - kBM * j)};
+  const int skip = kBM * ((t - sm.pre[lo]) * Cfg<kPair>::kCtas + rank);
+  const int2 r = group_rows(a, lo);
+  return Tile{lo, w - t * cols, r.x + skip, min(kBM, r.y - skip)};
 }
 
-// Clamped bounds of every group's rows and the prefix of their row tiles, by the block.
-__device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm) {
-  for (int g = threadIdx.x; g < a.groups; g += kThreads) {
-    int r0 = 0, r1 = a.rows;
-    if (a.starts) {
-      const int s0 = __ldg(a.starts + g), s1 = __ldg(a.starts + g + 1);
-      r0 = min(max(s0, 0), a.rows);
-      r1 = min(max(s1, r0), a.rows);
-      if ((r0 != s0 || r1 != s1) && blockIdx.x == 0) atomicOr(a.status, kOpsBadOrder);
-    }
-    sm.start[g] = r0;
-    sm.count[g] = r1 - r0;
-  }
-  __syncthreads();
+// The prefix of the groups' row tiles of `per` rows, by the block.
+__device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm, int per) {
   if (threadIdx.x < 32) {
     constexpr int kPer = kMaxExperts / 32;
     const int lane = threadIdx.x;
     int loc[kPer], sum = 0;
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = kPer * lane + i;
-      loc[i] = g < a.groups ? (sm.count[g] + kBM - 1) / kBM : 0;
-      sum += loc[i];
+      loc[i] = 0;
+      if (g < a.groups) {
+        loc[i] = (group_rows(a, g, &bad).y + per - 1) / per;
+        sum += loc[i];
+      }
     }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && blockIdx.x == 0 && lane == 0) atomicOr(a.status, kOpsBadOrder);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -101,12 +140,80 @@ __device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = kPer * lane + i;
-      if (g < a.groups) sm.pre[g] = run;
+      if (g < a.groups) sm.pre[g] = (unsigned short)run;
       run += loc[i];
     }
-    if (lane == 31) sm.pre[a.groups] = incl;
+    // groups that overlap may have any number of tiles: such a call does nothing
+    if (lane == 31) sm.pre[a.groups] = (unsigned short)(bad ? 0 : incl);
   }
   __syncthreads();
+}
+
+// ---- pairs of CTAs -----------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+
+// The address of a shared-memory object of this CTA in the CTA of the given rank.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar)
+               : "memory");
+}
+
+// A load of a pair's CTA, counted on the first CTA's barrier.
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, int x, int y,
+                                             int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// The pair's MMA: 256 rows, the first 128 from this CTA's shared memory and into its TMEM.
+__device__ __forceinline__ void pair_mma(uint32_t d, tc::Desc a, tc::Desc b, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+      " mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+// Arrives on the barrier in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b16 m;\n setp.ne.b32 e, %1, 0;\n mov.b16 m, 3;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+      ".b64 [%0], m;\n}\n" ::"r"(tc::smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t ncols) {
+  asm volatile(
+      "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n"
+      "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::"r"(tc::smem_u32(dst)),
+      "r"(ncols)
+      : "memory");
+}
+
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols)
+               : "memory");
 }
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, LinSmem& sm,
@@ -135,24 +242,32 @@ __device__ __forceinline__ void wait_ld_of(uint32_t (&v)[32]) {
 #undef MOE_IO8
 }
 
-__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float s) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(v[j]), s, acc[j]);
+// Two FMAs in one instruction.
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, float s) {
+  asm volatile("{\n .reg .b64 a, v, t;\n mov.b64 a, {%0, %1};\n mov.b64 v, {%2, %3};\n"
+      " mov.b64 t, {%4, %4};\n fma.rn.f32x2 a, v, t, a;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "r"(v0), "r"(v1), "f"(s));
 }
 
-// A warp's 32 x 128 outputs (lane: row) to its piece of shared memory, as two boxes of 64
-// columns under the 128-byte swizzle.
-__device__ __forceinline__ void stage_piece(uint8_t* piece, const float (&v)[128]) {
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float s) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) fma2(acc[j], acc[j + 1], v[j], v[j + 1], s);
+}
+
+// A warp's 32 x 64 outputs of a half (lane: row) to shared memory, as a box under the
+// 128-byte swizzle.
+__device__ __forceinline__ void stage_piece(uint8_t* piece, const float* v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < 8; ++c) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 p = __floats2bfloat162_rn(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    *reinterpret_cast<uint4*>(piece + (c >> 3) * 4096 + 128 * lane + 16 * ((c ^ lane) & 7)) =
+    *reinterpret_cast<uint4*>(piece + 128 * lane + 16 * ((c ^ lane) & 7)) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
@@ -171,44 +286,48 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 __device__ __forceinline__ void send_piece(const LinArgs& a, const uint8_t* piece, int row,
                                            int rows, int c0) {
   const int lane = threadIdx.x & 31, cols = a.outer - c0;
+  if (rows <= 0 || cols <= 0) return;
   if (rows >= 32) {
-    tc::fence_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(&a.out, piece, c0, row);
-      if (cols > 64) tma_store_2d(&a.out, piece + 4096, c0 + 64, row);
-      asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
-    }
+    if (lane == 0) tma_store_2d(&a.out, piece, c0, row);
     return;
   }
-  __syncwarp();
   bf16* y = a.y + (int64_t)row * a.y_stride + c0;
   const int c = lane & 7;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int r = 4 * (i & 7) + (lane >> 3), h = i >> 3;
-    if (r < rows && 64 * h + 8 * c < cols)
-      *reinterpret_cast<uint4*>(y + (int64_t)r * a.y_stride + 64 * h + 8 * c) =
-          *reinterpret_cast<const uint4*>(piece + 4096 * h + 128 * r + 16 * ((c ^ r) & 7));
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (r < rows && 8 * c < cols)
+      *reinterpret_cast<uint4*>(y + (int64_t)r * a.y_stride + 8 * c) =
+          *reinterpret_cast<const uint4*>(piece + 128 * r + 16 * ((c ^ r) & 7));
   }
 }
 
-template <bool kTrans>
+template <bool kTrans, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ LinArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  using C = Cfg<kPair>;
+  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes;
+  extern __shared__ __align__(1024) uint8_t stages[];
   uint8_t* pieces = stages + kStages * kStageBytes;
   LinSmem& sm = *reinterpret_cast<LinSmem*>(pieces + kSumWarps * kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? (int)cluster_rank() : 0;
+  if (tc::smem_u32(stages) & 1023u) {  // the same for every CTA
+    if (threadIdx.x == 0) atomicOr(a.status, kOpsTimeout);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(&sm.full[i], 1);
       tc::mbar_init(&sm.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       tc::mbar_init(&sm.tfull[i], 2);  // the MMAs' commit and the scale warp
       tc::mbar_init(&sm.tempty[i], kSumWarps);
+      tc::mbar_init(&sm.peer_empty[i], 1);
+    }
+    for (int i = 0; i < kSumWarps; ++i) {
+      tc::mbar_init(&sm.ofull[i], 1);
+      tc::mbar_init(&sm.ofree[i], 1);
     }
     sm.abort = 0;
     tc::fence_barrier_init();
@@ -219,240 +338,354 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
   }
   if (warp == kWarpMma) {
     __syncwarp();
-    tc::tmem_alloc(&sm.tmem, 512);
-    tc::tmem_relinquish();
+    if constexpr (kPair) {
+      pair_tmem_alloc(&sm.tmem, 512);
+    } else {
+      tc::tmem_alloc(&sm.tmem, 512);
+      tc::tmem_relinquish();
+    }
   }
   pdl_wait();
   tc::fence_before_sync();
-  group_tiles(a, sm);
+  group_tiles(a, sm, kBM * C::kCtas);
+  if constexpr (kPair) cluster_sync();  // the other CTA's barriers are there
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   const int cols = (a.outer + kBN - 1) / kBN, blocks = (a.inner + kKB - 1) / kKB;
   const int tiles = sm.pre[a.groups] * cols;
+  const int first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
+  const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;  // this CTA's tiles
 
-  if (warp >= kSumWarps) fewer_regs<kOtherRegs>();
+  if (warp >= kWarpStore) fewer_regs<kStoreRegs>();
+  else if (warp >= kSumWarps) fewer_regs<kFeedRegs>();
   if (warp == kWarpTma) {
     uint32_t st = 0, ph = 0;
     int issued = 0;
     bool ok = true;
-    for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x) {
-      const Tile t = tile_of(sm, a.groups, cols, w);
-      // more than half a tile of rows in one box (rows behind the group's do no harm: each
-      // row's products are its own), fewer in small boxes
-      const int boxes = 2 * t.n > kBM ? 0 : (t.n + kSmallBox - 1) / kSmallBox;
-      // the second half of the tile's columns, where there are any
-      const int halves = a.outer - t.f * kBN > kBN / 2 ? 2 : 1;
-      const uint32_t bytes =
-          (boxes ? boxes * kSmallBox * kKB : kABytes) + halves * (kBBytes / 2);
+    // a CTA's x rows of a block: more than half a tile of rows in one box (rows behind the
+    // group's do no harm: each row's products are its own), fewer in small boxes
+    const auto boxes = [](int n) { return (min(n, kBM / 2) + kSmallBox - 1) / kSmallBox; };
+    const auto x_bytes = [&](int n) {
+      return n <= 0 ? 0 : 2 * n > kBM ? kABytes : boxes(n) * kSmallBox * kKB;
+    };
+    // boxes of the weights' columns that there are for the CTA of this rank
+    const auto w_boxes = [&](int f, int r) {
+      const int left = a.outer - f * kBN - r * C::kBRows;
+      return left <= 0 ? 0 : kPair || left <= kHalf ? 1 : 2;
+    };
+    for (int w = first; w < tiles && ok; w += step) {
+      const Tile t = tile_of<kPair>(a, sm, cols, w, rank);
+      const int n0 = t.f * kBN + rank * C::kBRows, n_boxes = w_boxes(t.f, rank);
+      uint32_t bytes = x_bytes(t.n) + n_boxes * (kHalf * kKB);
+      if constexpr (kPair)  // the second CTA's, too
+        bytes += x_bytes(tile_of<kPair>(a, sm, cols, w, 1).n) + w_boxes(t.f, 1) * (kHalf * kKB);
+      // this lane's copy: lanes 0-3 the rows, 4 and 5 the weights
+      const CUtensorMap* map = nullptr;
+      int place = 0, x0 = 0, y0 = 0, g = 0;
+      bool along = true;  // the contraction runs along the box's rows of 128 bytes
+      if (lane < 4) {
+        if (lane == 0 && 2 * t.n > kBM) map = &a.x;
+        else if (2 * t.n <= kBM && lane < boxes(t.n)) map = &a.xs;
+        place = lane * kSmallBox * kKB;
+        y0 = t.row0 + lane * kSmallBox;
+      } else if (lane < 4 + n_boxes) {
+        map = &a.w;
+        place = kABytes + (lane - 4) * (kHalf * kKB);
+        x0 = y0 = n0 + (lane - 4) * kHalf;
+        g = t.g;
+        along = !kTrans;
+      }
       for (int b = 0; b < blocks; ++b) {
         if (!wait_all(&sm.empty[st], ph ^ 1u, sm, a.status)) {
           ok = false;
           break;
         }
-        uint8_t* sa = stages + st * kStageBytes;
-        uint8_t* sb = sa + kABytes;
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(&sm.full[st], bytes);
-          if (boxes == 0)
-            tc::tma_load_2d(sa, &a.x, b * kKB, t.row0, &sm.full[st]);
+        // every lane with a copy issues it at once: one lane after the other's takes the warp
+        // 150 cycles each
+        if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sm.full[st], bytes);
+        __syncwarp();
+        if (map) {
+          uint8_t* to = stages + st * kStageBytes + place;
+          const int at = b * kKB;
+          if constexpr (kPair)
+            pair_load_3d(to, map, along ? at : x0, along ? y0 : at, g, in_cta(&sm.full[st], 0));
           else
-            for (int i = 0; i < boxes; ++i)
-              tc::tma_load_2d(sa + i * kSmallBox * kKB, &a.xs, b * kKB, t.row0 + i * kSmallBox,
-                              &sm.full[st]);
-          for (int h = 0; h < halves; ++h) {
-            const int n0 = t.f * kBN + h * (kBN / 2);
-            tc::tma_load_3d(sb + h * (kBBytes / 2), &a.w, kTrans ? n0 : b * kKB,
-                            kTrans ? b * kKB : n0, t.g, &sm.full[st]);
-          }
+            tc::tma_load_3d(to, map, along ? at : x0, along ? y0 : at, g, &sm.full[st]);
         }
         __syncwarp();
         ++issued;
         if (++st == kStages) { st = 0; ph ^= 1u; }
       }
     }
+    // every stage's last commits have arrived before the CTA leaves
+    for (int i = 0; i < kStages && ok; ++i) {
+      ok = wait_all(&sm.empty[st], ph ^ 1u, sm, a.status);
+      if (++st == kStages) { st = 0; ph ^= 1u; }
+    }
     if (!ok && lane == 0) {
-      // copies in flight land before the CTA leaves
+      // and after a wait that gave up, copies in flight have landed; a pair's second CTA,
+      // whose copies count on the first's barriers, allows them 10 ms
       const unsigned long long t0 = tc::global_ns();
       for (int i = 1; i <= kStages && i <= issued; ++i) {
         const int k = issued - i;
-        while (!tc::mbar_try_wait(&sm.full[k % kStages], (uint32_t)((k / kStages) & 1)) &&
-               tc::global_ns() - t0 < tc::kWaitLimitNs) {
+        const unsigned long long limit = rank == 0 ? tc::kWaitLimitNs : 10000000ull;
+        while ((rank > 0 || !tc::mbar_try_wait(&sm.full[k % kStages],
+                                               (uint32_t)((k / kStages) & 1))) &&
+               tc::global_ns() - t0 < limit) {
         }
       }
     }
   } else if (warp < kWarpScale && warp >= kWarpMma) {
     // Two warps take the blocks in turn, one for each buffer: an issuing warp waits for the
     // tensor cores to take its MMAs, then pays for two commits and two barrier waits, and
-    // the other's MMAs run meanwhile.
+    // the other's MMAs run meanwhile.  A pair's first CTA issues for both; the second's warps
+    // pass on that their buffer is empty.
     const uint32_t leader = lane == 0, tb = warp - kWarpMma;
     const tc::Desc da = tc::desc_of(tc::smem_u32(stages), true);
     const tc::Desc db = tc::desc_of(tc::smem_u32(stages + kABytes), true,
-                                    kTrans ? kBBytes / 2 : 16);
-    uint32_t st = tb % kStages, ph = 0, tph = 0, turn = 0;
+                                    kTrans && !kPair ? kHalf * kKB : 16);
+    uint32_t st = tb, ph = 0, tph = 0, turn = 0;
     bool ok = true;
-    for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x) {
+    if (kPair && rank == 1) {
+      const uint32_t bar = in_cta(&sm.peer_empty[tb], 0);
+      for (int n = tb; n < mine * blocks && ok; n += 2, tph ^= 1u) {
+        ok = wait_all(&sm.tempty[tb], tph, sm, a.status);
+        tc::fence_after_sync();
+        tc::fence_before_sync();
+        if (lane == 0 && ok) arrive_at(bar);
+        __syncwarp();
+      }
+    }
+    for (int w = first; w < tiles && ok && rank == 0; w += step) {
       const int left = a.outer - (w % cols) * kBN;
-      const uint32_t idesc = tc::idesc_f8(kBM, left > kBN / 2 ? kBN : kBN / 2) |
+      const uint32_t idesc = tc::idesc_f8(kBM * C::kCtas, kPair || left > kHalf ? kBN : kHalf) |
                              (kTrans ? kIdescBMajorN : 0u);
       for (int b = 0; b < blocks; ++b, turn ^= 1u) {
         if (turn != tb) continue;
         ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status) &&
+             (!kPair || wait_all(&sm.peer_empty[tb], tph ^ 1u, sm, a.status)) &&
              wait_all(&sm.full[st], ph, sm, a.status);
         if (!ok) break;
         tc::fence_after_sync();
         const tc::Desc xa = da + st * kStageBytes, xb = db + st * kStageBytes;
 #pragma unroll
-        for (int k = 0; k < kKB / 32; ++k)
+        for (int k = 0; k < kKB / 32; ++k) {
           // 32 values along a row of 128 bytes; 32 rows of them where the rows run along N
-          tc::mma_ss<true>(tmem + tb * kBN, xa + 32 * k, xb + (kTrans ? 32 * kKB : 32) * k, idesc,
-                           k > 0, leader);
-        tc::commit_by(&sm.tfull[tb], leader);
-        tc::commit_by(&sm.empty[st], leader);
+          const tc::Desc ka = xa + 32 * k, kb = xb + (kTrans ? 32 * kKB : 32) * k;
+          if constexpr (kPair)
+            pair_mma(tmem + tb * kBN, ka, kb, idesc, k > 0, leader);
+          else
+            tc::mma_ss<true>(tmem + tb * kBN, ka, kb, idesc, k > 0, leader);
+        }
+        if constexpr (kPair) {
+          pair_commit(&sm.tfull[tb], leader);
+          pair_commit(&sm.empty[st], leader);
+        } else {
+          tc::commit_by(&sm.tfull[tb], leader);
+          tc::commit_by(&sm.empty[st], leader);
+        }
         tph ^= 1u;
         st += 2;
         if (st >= kStages) { st -= kStages; ph ^= 1u; }
       }
     }
   } else if (warp == kWarpScale) {
-    // Scales: a lane has rows lane, + 32, + 64 and + 96 of every tile.  Those of two blocks
-    // are loaded while the two in front of them are written.
-    constexpr int kAhead = 2;
+    // Scales: a lane has rows lane, + 32, + 64 and + 96 of every tile.  Those of the next
+    // block, of the next tile's first after a tile's last, are loaded while one is written: a
+    // tile that began with its loads would hold the sums up for their latency.
     const int nb_out = (a.outer + kGroup - 1) / kGroup;
     const int sw_step = kTrans ? nb_out : 1;
     uint32_t tb = 0, tph = 0;
     bool ok = true;
-    int j = 0;
-    for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x, ++j) {
-      const Tile t = tile_of(sm, a.groups, cols, w);
-      if (lane == 0) sm.tile[j & 3] = t;
-      const float* sx[4];
+    unsigned sx[4], sw0 = 0, sw1 = 0;  // where the tile's scales begin
+    float nx[4], nw0 = 0.0f, nw1 = 0.0f;
+    const auto begin = [&](int w, int j) {
+      const Tile t = tile_of<kPair>(a, sm, cols, w, rank);
+      if (lane == 0) sm.tile[j % kTiles] = t;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        sx[r] = a.sx + (size_t)(t.row0 + min(lane + 32 * r, t.n - 1)) * blocks;
+        sx[r] = (unsigned)min(t.row0 + max(min(lane + 32 * r, t.n - 1), 0), a.rows - 1) * blocks;
       const int cb = 2 * t.f, cb1 = min(cb + 1, nb_out - 1);
-      const float* sw = a.sw + (size_t)t.g * nb_out * blocks;
-      const float* sw0 = sw + (kTrans ? cb : cb * blocks);
-      const float* sw1 = sw + (kTrans ? cb1 : cb1 * blocks);
-      float nx[kAhead][4], nw[kAhead][2];
-      const auto load = [&](int b0) {
+      const unsigned sw = (unsigned)t.g * nb_out * blocks;
+      sw0 = sw + (kTrans ? cb : cb * blocks);
+      sw1 = sw + (kTrans ? cb1 : cb1 * blocks);
+    };
+    const auto load = [&](int b) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int b = min(b0 + k, blocks - 1);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) nx[k][r] = __ldg(sx[r] + b);
-          nw[k][0] = __ldg(sw0 + (size_t)b * sw_step);
-          nw[k][1] = __ldg(sw1 + (size_t)b * sw_step);
-        }
-      };
+      for (int r = 0; r < 4; ++r) nx[r] = __ldg(a.sx + (sx[r] + b));
+      nw0 = __ldg(a.sw + (sw0 + b * sw_step));
+      nw1 = __ldg(a.sw + (sw1 + b * sw_step));
+    };
+    int w = first, j = 0, b = 0;
+    if (w < tiles) {
+      begin(w, 0);
       load(0);
-      for (int b0 = 0; b0 < blocks && ok; b0 += kAhead) {
-        float p[kAhead][2][4];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            p[k][0][r] = nx[k][r] * nw[k][0];
-            p[k][1][r] = nx[k][r] * nw[k][1];
-          }
-        if (b0 + kAhead < blocks) load(b0 + kAhead);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (b0 + k >= blocks || !ok) break;
-          ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sm.scale[tb][0][lane + 32 * r] = p[k][0][r];
-            sm.scale[tb][1][lane + 32 * r] = p[k][1][r];
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.tfull[tb]);
-          if ((tb ^= 1u) == 0) tph ^= 1u;
-        }
-      }
     }
-  } else {
-    more_regs<kSumRegs>();
-    const int q = warp & 3, half = warp >> 2;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * (kBN / 2);
-    uint8_t* piece = pieces + warp * kOutBytes;
-    uint32_t tb = 0, tph = 0;
-    int j = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; w < tiles && ok; w += gridDim.x, ++j) {
-      float acc[kBN / 2];
+    while (w < tiles && ok) {
+      float p[2][4];
 #pragma unroll
-      for (int i = 0; i < kBN / 2; ++i) acc[i] = 0.0f;
-      Tile t = {0, 0, 0, 0};
-      for (int b = 0; b < blocks; ++b) {
-        if (!wait_all(&sm.tfull[tb], tph, sm, a.status)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        if (b == 0) t = sm.tile[j & 3];
-        const float s = sm.scale[tb][half][32 * q + lane];
-        if (32 * q < t.n && t.f * kBN + half * (kBN / 2) < a.outer) {  // any output here
-          const uint32_t from = lanes + tb * kBN;
-          uint32_t v0[32], v1[32];
-          tc::tmem_ld_async(from, v0);
-          wait_ld_of(v0);
-          tc::tmem_ld_async(from + 32, v1);
-          add_scaled(acc, v0, s);
-          wait_ld_of(v1);
-          tc::tmem_ld_async(from + 64, v0);
-          add_scaled(acc + 32, v1, s);
-          wait_ld_of(v0);
-          tc::tmem_ld_async(from + 96, v1);
-          add_scaled(acc + 64, v0, s);
-          wait_ld_of(v1);
-          // the buffer is free: the last products are in registers
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
-          add_scaled(acc + 96, v1, s);
-        } else {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
-        }
-        if ((tb ^= 1u) == 0) tph ^= 1u;
+      for (int r = 0; r < 4; ++r) {
+        p[0][r] = nx[r] * nw0;
+        p[1][r] = nx[r] * nw1;
       }
-      const int c0 = t.f * kBN + half * (kBN / 2), rows = t.n - 32 * q;
-      if (!ok || rows <= 0 || c0 >= a.outer) continue;
-      // the piece is free once the TMA has read the tile before
-      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      if (++b == blocks) {
+        b = 0;
+        w += step;
+        if (w < tiles) begin(w, ++j);
+      }
+      if (w < tiles) load(b);
+      ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        sm.scale[tb][0][lane + 32 * r] = p[0][r];
+        sm.scale[tb][1][lane + 32 * r] = p[1][r];
+      }
       __syncwarp();
-      stage_piece(piece, acc);
-      send_piece(a, piece, t.row0 + 32 * q, rows, c0);
+      if (lane == 0) tc::mbar_arrive(&sm.tfull[tb]);
+      if ((tb ^= 1u) == 0) tph ^= 1u;
+    }
+  } else if (warp >= kWarpStore) {
+    // Stores: a warp has the pieces of sums' warps i and i + 4.
+    bool ok = true;
+    for (int j = 0; j < mine && ok; ++j) {
+#pragma unroll 1
+      for (int p = warp - kWarpStore; p < kSumWarps && ok; p += kStoreWarps) {
+        ok = wait_all(&sm.ofull[p], j & 1, sm, a.status);
+        if (!ok) break;
+        tc::fence_async_smem();  // the sums' writes before the TMA's reads
+        const Tile t = sm.tile[j % kTiles];
+        const int c0 = t.f * kBN + (p >> 2) * kHalf, row = 32 * (p & 3);
+        uint8_t* piece = pieces + p * kOutBytes;
+        send_piece(a, piece, t.row0 + row, t.n - row, c0);
+        send_piece(a, piece + kOutBytes / 2, t.row0 + row, t.n - row, c0 + 64);
+        asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+        // the piece is free once the TMA has read it: the one in front's, by now
+        if (p >= kStoreWarps) {
+          asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(&sm.ofree[p - kStoreWarps]);
+            tc::mbar_arrive(&sm.ofree[p]);
+          }
+        }
+      }
     }
     asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+  } else {
+    more_regs<kSumRegs>();
+    const int q = warp & 3, half = warp >> 2;   // this warp's lanes and columns
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * kHalf;
+    uint8_t* piece = pieces + warp * kOutBytes;
+    uint32_t n = 0;  // blocks in front
+    for (int j = 0; j < mine; ++j) {
+      float acc[kHalf];
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+      for (int b = 0; b < blocks; ++b, ++n) {
+        // (a wait that gave up is seen behind the loop, which then ends at once; lanes and
+        // columns without outputs add up what is there, and drop it)
+        const uint32_t tb = n & 1u;
+        tc::wait_bounded(&sm.tfull[tb], (n >> 1) & 1u, &sm.abort, a.status);
+        __syncwarp();
+        tc::fence_after_sync();
+        const uint32_t from = lanes + tb * kBN;
+        uint32_t v0[32], v1[32];
+        tc::tmem_ld_async(from, v0);
+        const float s = sm.scale[tb][half][32 * q + lane];
+        wait_ld_of(v0);
+        tc::tmem_ld_async(from + 32, v1);
+        add_scaled(acc, v0, s);
+        wait_ld_of(v1);
+        tc::tmem_ld_async(from + 64, v0);
+        add_scaled(acc + 32, v1, s);
+        wait_ld_of(v0);
+        tc::tmem_ld_async(from + 96, v1);
+        add_scaled(acc + 64, v0, s);
+        wait_ld_of(v1);
+        // the last products are in registers: the buffer goes back
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
+        add_scaled(acc + 96, v1, s);
+      }
+      // the warp's piece, once the tile before has left it
+      if (!wait_all(&sm.ofree[warp], (j & 1) ^ 1u, sm, a.status)) break;
+      stage_piece(piece, acc);
+      stage_piece(piece + kOutBytes / 2, acc + 64);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.ofull[warp]);
+    }
   }
   __syncthreads();
+  // a pair leaves together: MMAs read both CTAs' shared memory, and arrivals cross
+  if constexpr (kPair) cluster_sync();
   if (warp == kWarpMma) {
     __syncwarp();
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    if constexpr (kPair) pair_tmem_dealloc(tmem, 512);
+    else tc::tmem_dealloc(tmem, 512);
   }
+}
+
+template <bool kTrans, bool kPair>
+cudaError_t setup() {
+  return cudaFuncSetAttribute(k_linear<kTrans, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)smem_bytes<kPair>());
+}
+
+template <bool kTrans, bool kPair>
+cudaError_t launch(const LinArgs& a, int grid, bool pdl, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kPair>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_linear<kTrans, kPair>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t setup_linear() {
-  const cudaError_t e = cudaFuncSetAttribute(
-      k_linear<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_linear<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)kSmemBytes);
+  const cudaError_t e[4] = {setup<false, false>(), setup<false, true>(), setup<true, false>(),
+                            setup<true, true>()};
+  for (const cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
-cudaError_t launch_linear(const LinArgs& a, bool trans, int sm_count, bool pdl, cudaStream_t s) {
+bool linear_pairs(const LinArgs& a) {
+  static const char* env = getenv("MOE_PAIR");
+  return env ? atoi(env) != 0 : true;
+}
+
+cudaError_t launch_linear(const LinArgs& a, bool trans, bool pairs, int sm_count, bool pdl,
+                          cudaStream_t s) {
   const long long cols = (a.outer + kBN - 1) / kBN;
+  const int ctas = pairs ? 2 : 1, places = sm_count / ctas;
   // at most a part tile for each group that has rows
-  const long long tiles =
-      ((long long)a.rows / kBM + (a.groups < a.rows ? a.groups : a.rows)) * cols;
-  const int grid = (int)(tiles < sm_count ? tiles : sm_count);
-  return launch_pdl(trans ? k_linear<true> : k_linear<false>, dim3(grid), dim3(kThreads),
-                    kSmemBytes, s, pdl, a);
+  const long long tiles = ((long long)a.rows / (kBM * ctas) +
+                           (a.groups < a.rows ? a.groups : a.rows)) * cols;
+  const int grid = ctas * (int)(tiles < places ? tiles : places);
+  if (pairs)
+    return trans ? launch<true, true>(a, grid, pdl, s) : launch<false, true>(a, grid, pdl, s);
+  return trans ? launch<true, false>(a, grid, pdl, s) : launch<false, false>(a, grid, pdl, s);
 }
 
 }  // namespace moe

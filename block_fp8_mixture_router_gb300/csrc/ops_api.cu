@@ -4,6 +4,7 @@
 // sizes are checked against the cap before anything is allocated, and every refusal is a
 // status code.
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 #include <new>
@@ -129,14 +130,21 @@ int combine(moe_ops* c, const void* rows, int64_t rows_stride, const moe_order* 
 
 // Boxes of 128 bytes x box_rows rows under the 128-byte swizzle.
 bool encode(CUtensorMap* m, const void* p, bool in_bf16, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, cuuint32_t box_rows) {
+            const cuuint64_t* strides, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
   if (!fn) return false;
-  const cuuint32_t box[3] = {in_bf16 ? 64u : 128u, box_rows, 1}, unit[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {in_bf16 ? 64u : 128u, (cuuint32_t)box_rows, 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
   return fn(m, in_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
-            const_cast<void*>(p), dims, strides, box, unit,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a group that a CTA of the kernel for few rows takes, 0: the tensor-core kernel.
+int few_rows(int rows, int groups) {
+  static const char* env = getenv("MOE_FEW");
+  if (env) return atoi(env);
+  return rows <= 8 * groups ? 8 : rows <= 16 * groups ? 16 : 0;
 }
 
 int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int32_t* starts,
@@ -169,19 +177,27 @@ int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int3
   a.y = static_cast<bf16*>(y);
   a.y_stride = y_stride;
   a.status = c->status;
-  const cuuint64_t dx[2] = {(cuuint64_t)inner, (cuuint64_t)rows}, sx[1] = {(cuuint64_t)inner};
+  if (const int per = trans ? 0 : few_rows(rows, starts ? w->groups : 1))
+    return status_of(launch_linear_rows(a, static_cast<const bf16*>(x->values), x->stride,
+                                        x->codes, w->codes, per, s));
+  // (x as one group, so that one form of copy takes rows and weights)
+  const cuuint64_t dx[3] = {(cuuint64_t)inner, (cuuint64_t)rows, 1};
+  const cuuint64_t sx[2] = {(cuuint64_t)inner, (cuuint64_t)inner * rows};
   const cuuint64_t dw[3] = {(cuuint64_t)w->in, (cuuint64_t)w->out, (cuuint64_t)w->groups};
   const cuuint64_t sw[2] = {(cuuint64_t)w->in, (cuuint64_t)w->in * w->out};
   const cuuint64_t dy[2] = {(cuuint64_t)outer, (cuuint64_t)rows};
   const cuuint64_t sy[1] = {(cuuint64_t)(rows > 1 ? y_stride : outer) * 2};
-  if (!encode(&a.x, codes, false, 2, dx, sx, 128) || !encode(&a.xs, codes, false, 2, dx, sx, 32) ||
-      !encode(&a.w, w->codes, false, 3, dw, sw, 128) || !encode(&a.out, y, true, 2, dy, sy, 32))
+  const bool pairs = linear_pairs(a);
+  if (!encode(&a.x, codes, false, 3, dx, sx, 128) ||
+      !encode(&a.xs, codes, false, 3, dx, sx, 32) ||
+      !encode(&a.w, w->codes, false, 3, dw, sw, 128) ||
+      !encode(&a.out, y, true, 2, dy, sy, 32))
     return MOE_ERR_CUDA;
   if (x->values &&
       launch_quant_rows(static_cast<const bf16*>(x->values), x->stride, rows, inner, c->codes,
                         c->scales, s) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return status_of(launch_linear(a, trans, c->sm_count, x->values != nullptr, s));
+  return status_of(launch_linear(a, trans, pairs, c->sm_count, x->values != nullptr, s));
 }
 
 }  // namespace

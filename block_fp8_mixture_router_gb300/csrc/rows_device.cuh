@@ -63,30 +63,47 @@ __device__ __forceinline__ float div_by(float v, float s, float y) {
   return fmaf(fmaf(-q, s, v), y, q);
 }
 
+// Codes of kN x 16 values of a group whose largest magnitude is m: quant4's codes, without its
+// test of every value for a quotient that the product leaves open.  Quotients of bf16 values
+// often lie on e4m3's midpoints, where that test sends whole warps to the long division
+// (134 M values: 160 us that way, 77 this).  Returns the group's scale.
+template <int kN>
+__device__ __forceinline__ float quant_codes(const float (&v)[kN][16], float m, uint4 (&code)[kN]) {
+  m = m == 0.0f ? 448.0f : m;  // a group of zeros has the scale 1
+  if (m >= 0x1p-80f && m <= 0x1p100f) {
+    const float s = div_by(m, 448.0f, 0x1.24924ap-9f);  // RN(1 / 448)
+    const float y = __frcp_rn(s);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      float q[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = div_by(v[k][i], s, y);
+      code[k] = make_uint4(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]),
+                           e4m3x4(q[8], q[9], q[10], q[11]), e4m3x4(q[12], q[13], q[14], q[15]));
+    }
+    return s;
+  }
+  const float s = group_scale(m);
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+    code[k] = make_uint4(quant4(v[k][0], v[k][1], v[k][2], v[k][3], s),
+                         quant4(v[k][4], v[k][5], v[k][6], v[k][7], s),
+                         quant4(v[k][8], v[k][9], v[k][10], v[k][11], s),
+                         quant4(v[k][12], v[k][13], v[k][14], v[k][15], s));
+  return s;
+}
+
 // Codes and scale of a group of 128 values, 16 in each of eight neighbouring lanes (the
-// whole warp calls): quant4's codes, without its test of every value for a quotient that
-// the product leaves open.  Quotients of bf16 values often lie on e4m3's midpoints, where
-// that test sends whole warps to the long division (134 M values: 160 us that way, 77 this).
+// whole warp calls).
 __device__ __forceinline__ uint4 quant16(const float (&v)[16], float* scale) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m >= 0x1p-80f && m <= 0x1p100f) {
-    const float s = div_by(m, 448.0f, 0x1.24924ap-9f);
-    const float y = __frcp_rn(s);
-    float q[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = div_by(v[i], s, y);
-    *scale = s;
-    return make_uint4(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]),
-                      e4m3x4(q[8], q[9], q[10], q[11]), e4m3x4(q[12], q[13], q[14], q[15]));
-  }
-  const float s = group_scale(m);
-  *scale = s;
-  return make_uint4(quant4(v[0], v[1], v[2], v[3], s), quant4(v[4], v[5], v[6], v[7], s),
-                    quant4(v[8], v[9], v[10], v[11], s), quant4(v[12], v[13], v[14], v[15], s));
+  uint4 code[1];
+  *scale = quant_codes<1>(reinterpret_cast<const float(&)[1][16]>(v), m, code);
+  return code[0];
 }
 
 // Columns c .. c + 15 of row r of the output, whole groups of eight lanes at a time (the
