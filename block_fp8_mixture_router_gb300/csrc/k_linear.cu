@@ -12,21 +12,18 @@
 // (The weights along the lanes, as the layer's own products have them, want a scale from
 // shared memory for every column.)
 //
-// A CTA has 128 rows by 256 columns, a pair of CTAs 256 by 256: each loads its rows and half
-// of the columns' weights, and the first issues the MMAs of both.  The pair halves the
-// weights' way into shared memory, which binds a CTA alone (48 KB of a block at the 64 bytes a
-// clock that an SM takes from L2 are 768 cycles; the block's MMAs take 512).
-// A block's products go to TMEM by column halves, in turn through four buffers of 128
-// columns: the warps copy a buffer to registers, give it back, and multiply while the tensor
-// cores are three halves ahead.  (Two buffers of 256 columns, given back after the FMAs, left
-// either side waiting for the other: 16384 rows x 2048 x 4096 139 us.)
+// A tile is 128 rows by 256 columns.  Each block's MMAs (512 cycles) fill one of two TMEM
+// buffers while the warps empty the other: copy 32 columns to registers, multiply the 32 in
+// front of them, and give the buffer back before the last 32 are multiplied.  What binds it is
+// that exchange, about 860 cycles a block with its barriers' latencies on both sides
+// (16384 x 2048 x 4096 in 113 us, 2.4 PFLOP/s), not the 768 that 48 KB of a block take at the
+// 64 bytes a clock that an SM gets from L2: pairs of CTAs that share their columns' weights
+// (cta_group::2, 256 x 256) move a third less and take the same 113 us, and 126 instead of 96
+// for 1024 tokens' rows of 256 experts.  Four buffers of 128 columns: 163 us.
 //
-// Warps: 0-7 the sums and the store (warp w: lanes 32 (w % 4) and on, columns 64 (w / 4) and
-// on of each half), 8 the TMA loads, 9 and 10 the MMAs of the two halves, 11 the scales.
-// Persistent: a CTA, or pair, takes tiles first, first + step, ..; the tiles of a group's rows
-// lie next to each other.
-#include <stdlib.h>
-
+// Warps: 0-7 the sums (warp w: lanes 32 (w % 4) and on, columns 128 (w / 4) and on), 8 the TMA
+// loads, 9 and 10 the MMAs, 11 the scales, 12-15 the stores.  Persistent: a CTA takes tiles
+// blockIdx.x, + gridDim.x, ..; the tiles of a group's 128 rows lie next to each other.
 #include "attn_tc.cuh"
 #include "ops_internal.cuh"
 
@@ -43,34 +40,25 @@ constexpr int kThreads = 32 * (kWarpStore + kStoreWarps);
 // and 64 products on their way take what the others give.
 constexpr int kSumRegs = 216, kFeedRegs = 40, kStoreRegs = 40;
 static_assert(2 * kSumRegs + kFeedRegs + kStoreRegs <= 4 * 128, "no more registers than at launch");
-constexpr int kABytes = kBM * kKB;
+constexpr int kABytes = kBM * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 3;
 constexpr int kHalf = kBN / 2;                   // columns of a box of weights
 constexpr int kBufs = 512 / kBN;                 // TMEM buffers of a block's products: 2
-constexpr int kSmallBox = 32;                  // rows of a small box of x
-constexpr int kOutBytes = 32 * 128 * 2;        // a warp's piece of the output: 32 x 128
+constexpr int kSmallBox = 32;                    // rows of a small box of x
+constexpr int kOutBytes = 32 * 128 * 2;          // a warp's piece of the output: 32 x 128
 constexpr uint32_t kIdescBMajorN = 1u << 16;
-
-// A CTA alone, or a pair of CTAs that shares its columns.
-template <bool kPair>
-struct Cfg {
-  static constexpr int kCtas = kPair ? 2 : 1;
-  static constexpr int kBRows = kBN / kCtas;      // columns whose weights a CTA loads
-  static constexpr int kBBytes = kBRows * kKB, kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kPair ? 5 : 3;
-};
 
 struct Tile {
   int g, f, row0, n;  // group, column tile, first row, rows
 };
 
-constexpr int kMaxStages = 5;
-constexpr int kTiles = 8;  // the scales' warp is at most kBufs + 1 tiles ahead of the sums, and they two
-                             // ahead of the stores
+// The scales' warp is at most kBufs + 1 tiles ahead of the sums, and they two ahead of the
+// stores.
+constexpr int kTiles = 8;
 struct LinSmem {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kStages], empty[kStages];
   uint64_t tfull[kBufs], tempty[kBufs];
   uint64_t ofull[kSumWarps], ofree[kSumWarps];  // a warp's piece of the output
-  uint64_t peer_empty[kBufs];  // a pair's first CTA: the second's warps have read the buffer
   uint32_t tmem;
   int abort;
   Tile tile[kTiles];           // tiles j, j + 1, .. of this CTA, by j % kTiles
@@ -79,13 +67,9 @@ struct LinSmem {
 };
 // (The dynamic shared memory of a kernel without any static begins at a multiple of 1024
 // bytes, which the swizzled tiles need; the kernel checks it.)
-template <bool kPair>
-constexpr size_t smem_bytes() {
-  return (size_t)Cfg<kPair>::kStages * Cfg<kPair>::kStageBytes + kSumWarps * kOutBytes +
-         sizeof(LinSmem);
-}
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448,
-              "shared memory of a CTA");
+constexpr size_t kSmemBytes =
+    (size_t)kStages * kStageBytes + kSumWarps * kOutBytes + sizeof(LinSmem);
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
 // First row and rows of a group, clamped to the rows there are.
 __device__ __forceinline__ int2 group_rows(const LinArgs& a, int g, bool* bad = nullptr) {
@@ -96,24 +80,20 @@ __device__ __forceinline__ int2 group_rows(const LinArgs& a, int g, bool* bad = 
   return make_int2(r0, r1 - r0);
 }
 
-// Tile w; a pair's tile is its two CTAs' row tiles, this CTA's the one of its rank (n <= 0: it
-// has no rows).
-template <bool kPair>
-__device__ __forceinline__ Tile tile_of(const LinArgs& a, const LinSmem& sm, int cols, int w,
-                                        int rank) {
+__device__ __forceinline__ Tile tile_of(const LinArgs& a, const LinSmem& sm, int cols, int w) {
   const int t = w / cols;
   int lo = 0, hi = a.groups;  // the last group with pre <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (sm.pre[mid] <= t) lo = mid; else hi = mid;
   }
-  const int skip = kBM * ((t - sm.pre[lo]) * Cfg<kPair>::kCtas + rank);
+  const int skip = kBM * (t - sm.pre[lo]);
   const int2 r = group_rows(a, lo);
   return Tile{lo, w - t * cols, r.x + skip, min(kBM, r.y - skip)};
 }
 
-// The prefix of the groups' row tiles of `per` rows, by the block.
-__device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm, int per) {
+// The prefix of the groups' row tiles, by the block.
+__device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm) {
   if (threadIdx.x < 32) {
     constexpr int kPer = kMaxExperts / 32;
     const int lane = threadIdx.x;
@@ -124,7 +104,7 @@ __device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm, int p
       const int g = kPer * lane + i;
       loc[i] = 0;
       if (g < a.groups) {
-        loc[i] = (group_rows(a, g, &bad).y + per - 1) / per;
+        loc[i] = (group_rows(a, g, &bad).y + kBM - 1) / kBM;
         sum += loc[i];
       }
     }
@@ -147,73 +127,6 @@ __device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm, int p
     if (lane == 31) sm.pre[a.groups] = (unsigned short)(bad ? 0 : incl);
   }
   __syncthreads();
-}
-
-// ---- pairs of CTAs -----------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
-}
-
-// The address of a shared-memory object of this CTA in the CTA of the given rank.
-__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(tc::smem_u32(p)), "r"(rank));
-  return r;
-}
-
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar)
-               : "memory");
-}
-
-// A load of a pair's CTA, counted on the first CTA's barrier.
-__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, int x, int y,
-                                             int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-// The pair's MMA: 256 rows, the first 128 from this CTA's shared memory and into its TMEM.
-__device__ __forceinline__ void pair_mma(uint32_t d, tc::Desc a, tc::Desc b, uint32_t idesc,
-                                         uint32_t accumulate, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
-      " mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
-      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %5, p;\n}\n" ::"r"(d),
-      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
-
-// Arrives on the barrier in both CTAs once the MMAs issued so far are done.
-__device__ __forceinline__ void pair_commit(uint64_t* bar, uint32_t leader) {
-  asm volatile(
-      "{\n .reg .pred e;\n .reg .b16 m;\n setp.ne.b32 e, %1, 0;\n mov.b16 m, 3;\n"
-      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-      ".b64 [%0], m;\n}\n" ::"r"(tc::smem_u32(bar)),
-      "r"(leader)
-      : "memory");
-}
-
-__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t ncols) {
-  asm volatile(
-      "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n"
-      "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::"r"(tc::smem_u32(dst)),
-      "r"(ncols)
-      : "memory");
-}
-
-__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols)
-               : "memory");
 }
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, LinSmem& sm,
@@ -302,15 +215,12 @@ __device__ __forceinline__ void send_piece(const LinArgs& a, const uint8_t* piec
   }
 }
 
-template <bool kTrans, bool kPair>
+template <bool kTrans>
 __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ LinArgs a) {
-  using C = Cfg<kPair>;
-  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes;
   extern __shared__ __align__(1024) uint8_t stages[];
   uint8_t* pieces = stages + kStages * kStageBytes;
   LinSmem& sm = *reinterpret_cast<LinSmem*>(pieces + kSumWarps * kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kPair ? (int)cluster_rank() : 0;
   if (tc::smem_u32(stages) & 1023u) {  // the same for every CTA
     if (threadIdx.x == 0) atomicOr(a.status, kOpsTimeout);
     return;
@@ -323,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
     for (int i = 0; i < kBufs; ++i) {
       tc::mbar_init(&sm.tfull[i], 2);  // the MMAs' commit and the scale warp
       tc::mbar_init(&sm.tempty[i], kSumWarps);
-      tc::mbar_init(&sm.peer_empty[i], 1);
     }
     for (int i = 0; i < kSumWarps; ++i) {
       tc::mbar_init(&sm.ofull[i], 1);
@@ -338,22 +247,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
   }
   if (warp == kWarpMma) {
     __syncwarp();
-    if constexpr (kPair) {
-      pair_tmem_alloc(&sm.tmem, 512);
-    } else {
-      tc::tmem_alloc(&sm.tmem, 512);
-      tc::tmem_relinquish();
-    }
+    tc::tmem_alloc(&sm.tmem, 512);
+    tc::tmem_relinquish();
   }
   pdl_wait();
   tc::fence_before_sync();
-  group_tiles(a, sm, kBM * C::kCtas);
-  if constexpr (kPair) cluster_sync();  // the other CTA's barriers are there
+  group_tiles(a, sm);
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   const int cols = (a.outer + kBN - 1) / kBN, blocks = (a.inner + kKB - 1) / kKB;
   const int tiles = sm.pre[a.groups] * cols;
-  const int first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
+  const int first = blockIdx.x, step = gridDim.x;
   const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;  // this CTA's tiles
 
   if (warp >= kWarpStore) fewer_regs<kStoreRegs>();
@@ -362,36 +266,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
     uint32_t st = 0, ph = 0;
     int issued = 0;
     bool ok = true;
-    // a CTA's x rows of a block: more than half a tile of rows in one box (rows behind the
-    // group's do no harm: each row's products are its own), fewer in small boxes
-    const auto boxes = [](int n) { return (min(n, kBM / 2) + kSmallBox - 1) / kSmallBox; };
-    const auto x_bytes = [&](int n) {
-      return n <= 0 ? 0 : 2 * n > kBM ? kABytes : boxes(n) * kSmallBox * kKB;
-    };
-    // boxes of the weights' columns that there are for the CTA of this rank
-    const auto w_boxes = [&](int f, int r) {
-      const int left = a.outer - f * kBN - r * C::kBRows;
-      return left <= 0 ? 0 : kPair || left <= kHalf ? 1 : 2;
-    };
     for (int w = first; w < tiles && ok; w += step) {
-      const Tile t = tile_of<kPair>(a, sm, cols, w, rank);
-      const int n0 = t.f * kBN + rank * C::kBRows, n_boxes = w_boxes(t.f, rank);
-      uint32_t bytes = x_bytes(t.n) + n_boxes * (kHalf * kKB);
-      if constexpr (kPair)  // the second CTA's, too
-        bytes += x_bytes(tile_of<kPair>(a, sm, cols, w, 1).n) + w_boxes(t.f, 1) * (kHalf * kKB);
+      const Tile t = tile_of(a, sm, cols, w);
+      // rows: more than half a tile of them in one box (rows behind the group's do no harm:
+      // each row's products are its own), fewer in small boxes; columns: the halves there are
+      const int boxes = 2 * t.n > kBM ? 0 : (t.n + kSmallBox - 1) / kSmallBox;
+      const int halves = a.outer - t.f * kBN > kHalf ? 2 : 1;
+      const uint32_t bytes =
+          (boxes ? boxes * kSmallBox * kKB : kABytes) + halves * (kHalf * kKB);
       // this lane's copy: lanes 0-3 the rows, 4 and 5 the weights
       const CUtensorMap* map = nullptr;
       int place = 0, x0 = 0, y0 = 0, g = 0;
       bool along = true;  // the contraction runs along the box's rows of 128 bytes
       if (lane < 4) {
-        if (lane == 0 && 2 * t.n > kBM) map = &a.x;
-        else if (2 * t.n <= kBM && lane < boxes(t.n)) map = &a.xs;
+        if (boxes == 0 ? lane == 0 : lane < boxes) map = boxes == 0 ? &a.x : &a.xs;
         place = lane * kSmallBox * kKB;
         y0 = t.row0 + lane * kSmallBox;
-      } else if (lane < 4 + n_boxes) {
+      } else if (lane < 4 + halves) {
         map = &a.w;
         place = kABytes + (lane - 4) * (kHalf * kKB);
-        x0 = y0 = n0 + (lane - 4) * kHalf;
+        x0 = y0 = t.f * kBN + (lane - 4) * kHalf;
         g = t.g;
         along = !kTrans;
       }
@@ -402,15 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
         }
         // every lane with a copy issues it at once: one lane after the other's takes the warp
         // 150 cycles each
-        if (rank == 0 && lane == 0) tc::mbar_arrive_expect_tx(&sm.full[st], bytes);
+        if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[st], bytes);
         __syncwarp();
         if (map) {
           uint8_t* to = stages + st * kStageBytes + place;
           const int at = b * kKB;
-          if constexpr (kPair)
-            pair_load_3d(to, map, along ? at : x0, along ? y0 : at, g, in_cta(&sm.full[st], 0));
-          else
-            tc::tma_load_3d(to, map, along ? at : x0, along ? y0 : at, g, &sm.full[st]);
+          tc::tma_load_3d(to, map, along ? at : x0, along ? y0 : at, g, &sm.full[st]);
         }
         __syncwarp();
         ++issued;
@@ -423,47 +314,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
       if (++st == kStages) { st = 0; ph ^= 1u; }
     }
     if (!ok && lane == 0) {
-      // and after a wait that gave up, copies in flight have landed; a pair's second CTA,
-      // whose copies count on the first's barriers, allows them 10 ms
+      // and after a wait that gave up, copies in flight have landed
       const unsigned long long t0 = tc::global_ns();
       for (int i = 1; i <= kStages && i <= issued; ++i) {
         const int k = issued - i;
-        const unsigned long long limit = rank == 0 ? tc::kWaitLimitNs : 10000000ull;
-        while ((rank > 0 || !tc::mbar_try_wait(&sm.full[k % kStages],
-                                               (uint32_t)((k / kStages) & 1))) &&
-               tc::global_ns() - t0 < limit) {
+        while (!tc::mbar_try_wait(&sm.full[k % kStages], (uint32_t)((k / kStages) & 1)) &&
+               tc::global_ns() - t0 < tc::kWaitLimitNs) {
         }
       }
     }
   } else if (warp < kWarpScale && warp >= kWarpMma) {
     // Two warps take the blocks in turn, one for each buffer: an issuing warp waits for the
     // tensor cores to take its MMAs, then pays for two commits and two barrier waits, and
-    // the other's MMAs run meanwhile.  A pair's first CTA issues for both; the second's warps
-    // pass on that their buffer is empty.
+    // the other's MMAs run meanwhile.
     const uint32_t leader = lane == 0, tb = warp - kWarpMma;
     const tc::Desc da = tc::desc_of(tc::smem_u32(stages), true);
     const tc::Desc db = tc::desc_of(tc::smem_u32(stages + kABytes), true,
-                                    kTrans && !kPair ? kHalf * kKB : 16);
+                                    kTrans ? kHalf * kKB : 16);
     uint32_t st = tb, ph = 0, tph = 0, turn = 0;
     bool ok = true;
-    if (kPair && rank == 1) {
-      const uint32_t bar = in_cta(&sm.peer_empty[tb], 0);
-      for (int n = tb; n < mine * blocks && ok; n += 2, tph ^= 1u) {
-        ok = wait_all(&sm.tempty[tb], tph, sm, a.status);
-        tc::fence_after_sync();
-        tc::fence_before_sync();
-        if (lane == 0 && ok) arrive_at(bar);
-        __syncwarp();
-      }
-    }
-    for (int w = first; w < tiles && ok && rank == 0; w += step) {
+    for (int w = first; w < tiles && ok; w += step) {
       const int left = a.outer - (w % cols) * kBN;
-      const uint32_t idesc = tc::idesc_f8(kBM * C::kCtas, kPair || left > kHalf ? kBN : kHalf) |
+      const uint32_t idesc = tc::idesc_f8(kBM, left > kHalf ? kBN : kHalf) |
                              (kTrans ? kIdescBMajorN : 0u);
       for (int b = 0; b < blocks; ++b, turn ^= 1u) {
         if (turn != tb) continue;
         ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status) &&
-             (!kPair || wait_all(&sm.peer_empty[tb], tph ^ 1u, sm, a.status)) &&
              wait_all(&sm.full[st], ph, sm, a.status);
         if (!ok) break;
         tc::fence_after_sync();
@@ -472,18 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
         for (int k = 0; k < kKB / 32; ++k) {
           // 32 values along a row of 128 bytes; 32 rows of them where the rows run along N
           const tc::Desc ka = xa + 32 * k, kb = xb + (kTrans ? 32 * kKB : 32) * k;
-          if constexpr (kPair)
-            pair_mma(tmem + tb * kBN, ka, kb, idesc, k > 0, leader);
-          else
-            tc::mma_ss<true>(tmem + tb * kBN, ka, kb, idesc, k > 0, leader);
+          tc::mma_ss<true>(tmem + tb * kBN, ka, kb, idesc, k > 0, leader);
         }
-        if constexpr (kPair) {
-          pair_commit(&sm.tfull[tb], leader);
-          pair_commit(&sm.empty[st], leader);
-        } else {
-          tc::commit_by(&sm.tfull[tb], leader);
-          tc::commit_by(&sm.empty[st], leader);
-        }
+        tc::commit_by(&sm.tfull[tb], leader);
+        tc::commit_by(&sm.empty[st], leader);
         tph ^= 1u;
         st += 2;
         if (st >= kStages) { st -= kStages; ph ^= 1u; }
@@ -500,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
     unsigned sx[4], sw0 = 0, sw1 = 0;  // where the tile's scales begin
     float nx[4], nw0 = 0.0f, nw1 = 0.0f;
     const auto begin = [&](int w, int j) {
-      const Tile t = tile_of<kPair>(a, sm, cols, w, rank);
+      const Tile t = tile_of(a, sm, cols, w);
       if (lane == 0) sm.tile[j % kTiles] = t;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        sx[r] = (unsigned)min(t.row0 + max(min(lane + 32 * r, t.n - 1), 0), a.rows - 1) * blocks;
+        sx[r] = (unsigned)(t.row0 + min(lane + 32 * r, t.n - 1)) * blocks;
       const int cb = 2 * t.f, cb1 = min(cb + 1, nb_out - 1);
       const unsigned sw = (unsigned)t.g * nb_out * blocks;
       sw0 = sw + (kTrans ? cb : cb * blocks);
@@ -618,74 +486,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
     }
   }
   __syncthreads();
-  // a pair leaves together: MMAs read both CTAs' shared memory, and arrivals cross
-  if constexpr (kPair) cluster_sync();
   if (warp == kWarpMma) {
     __syncwarp();
     tc::fence_after_sync();
-    if constexpr (kPair) pair_tmem_dealloc(tmem, 512);
-    else tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(tmem, 512);
   }
-}
-
-template <bool kTrans, bool kPair>
-cudaError_t setup() {
-  return cudaFuncSetAttribute(k_linear<kTrans, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)smem_bytes<kPair>());
-}
-
-template <bool kTrans, bool kPair>
-cudaError_t launch(const LinArgs& a, int grid, bool pdl, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<kPair>();
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (kPair) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 2;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  if (pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_linear<kTrans, kPair>, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t setup_linear() {
-  const cudaError_t e[4] = {setup<false, false>(), setup<false, true>(), setup<true, false>(),
-                            setup<true, true>()};
-  for (const cudaError_t x : e)
-    if (x != cudaSuccess) return x;
-  return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      k_linear<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_linear<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)kSmemBytes);
 }
 
-bool linear_pairs(const LinArgs& a) {
-  static const char* env = getenv("MOE_PAIR");
-  return env ? atoi(env) != 0 : true;
-}
-
-cudaError_t launch_linear(const LinArgs& a, bool trans, bool pairs, int sm_count, bool pdl,
-                          cudaStream_t s) {
+cudaError_t launch_linear(const LinArgs& a, bool trans, int sm_count, bool pdl, cudaStream_t s) {
   const long long cols = (a.outer + kBN - 1) / kBN;
-  const int ctas = pairs ? 2 : 1, places = sm_count / ctas;
   // at most a part tile for each group that has rows
-  const long long tiles = ((long long)a.rows / (kBM * ctas) +
-                           (a.groups < a.rows ? a.groups : a.rows)) * cols;
-  const int grid = ctas * (int)(tiles < places ? tiles : places);
-  if (pairs)
-    return trans ? launch<true, true>(a, grid, pdl, s) : launch<false, true>(a, grid, pdl, s);
-  return trans ? launch<true, false>(a, grid, pdl, s) : launch<false, false>(a, grid, pdl, s);
+  const long long tiles =
+      ((long long)a.rows / kBM + (a.groups < a.rows ? a.groups : a.rows)) * cols;
+  const int grid = (int)(tiles < sm_count ? tiles : sm_count);
+  return launch_pdl(trans ? k_linear<true> : k_linear<false>, dim3(grid), dim3(kThreads),
+                    kSmemBytes, s, pdl, a);
 }
 
 }  // namespace moe

@@ -82,7 +82,7 @@ __device__ __forceinline__ void quant32(const bf16* row, int c, int width, bool 
   }
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  *scale = quant_codes<2>(v, m, b);
+  *scale = quant_codes<2, true>(v, m, b);
 }
 
 template <bool kCodes, int kNt>

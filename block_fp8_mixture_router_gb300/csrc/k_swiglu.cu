@@ -29,7 +29,7 @@ __device__ __forceinline__ Unit unit_of(unsigned u, int rows, int groups) {
 }
 
 template <bool kCodes>
-__global__ void __launch_bounds__(kThreads) k_swiglu(const bf16* gu, int64_t gu_stride, int rows,
+__global__ void __launch_bounds__(kThreads, 6) k_swiglu(const bf16* gu, int64_t gu_stride, int rows,
                                                      int width, RowsOut out) {
   const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(width));
   const bf16* row = gu + (int64_t)u.row * gu_stride;
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const bf16* gu, int64_t gu_
   unpack16(ru, v);
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] *= silu_f32(g[i]);
-  put16<kCodes>(out, u.row, u.c, width, u.on, v);
+  put16<kCodes, false>(out, u.row, u.c, width, u.on, v);
 }
 
 // Gradients of 16 gates and of 16 ups.
@@ -60,7 +60,7 @@ __device__ __forceinline__ void swiglu_back(const Vec16& rd, const Vec16& rg, co
 // One group of the width at a time, both halves of the output.  In codes the width is a
 // multiple of 128, so that groups of the output lie in one half.
 template <bool kCodes>
-__global__ void __launch_bounds__(kThreads) k_swiglu_grad(const bf16* dh, int64_t dh_stride,
+__global__ void __launch_bounds__(kThreads, 4) k_swiglu_grad(const bf16* dh, int64_t dh_stride,
                                                           const bf16* gu, int64_t gu_stride,
                                                           int rows, int width, RowsOut out) {
   const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(width));
@@ -70,19 +70,19 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_grad(const bf16* dh, int64_
   float dg[16], du[16];
   swiglu_back(rd, rg, ru, dg, du);
   if constexpr (kCodes) {
-    put16<true>(out, u.row, u.c, 2 * width, u.on, dg);
-    put16<true>(out, u.row, width + u.c, 2 * width, u.on, du);
+    put16<true, false>(out, u.row, u.c, 2 * width, u.on, dg);
+    put16<true, false>(out, u.row, width + u.c, 2 * width, u.on, du);
   } else {
     RowsOut half = out;
-    put16<false>(half, u.row, u.c, width, u.on, dg);
+    put16<false, false>(half, u.row, u.c, width, u.on, dg);
     half.v += width;
-    put16<false>(half, u.row, u.c, width, u.on, du);
+    put16<false, false>(half, u.row, u.c, width, u.on, du);
   }
 }
 
 // Codes at other widths (multiples of 16): one group of the output's 2 x width columns at a
 // time; the group on the border holds gradients of gates and of ups.
-__global__ void __launch_bounds__(kThreads) k_swiglu_grad_mixed(const bf16* dh, int64_t dh_stride,
+__global__ void __launch_bounds__(kThreads, 4) k_swiglu_grad_mixed(const bf16* dh, int64_t dh_stride,
                                                                 const bf16* gu, int64_t gu_stride,
                                                                 int rows, int width, RowsOut out) {
   const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(2 * width));
@@ -95,15 +95,15 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_grad_mixed(const bf16* dh, 
   swiglu_back(rd, rg, ru, dg, du);
 #pragma unroll
   for (int i = 0; i < 16; ++i) dg[i] = up ? du[i] : dg[i];
-  put16<true>(out, u.row, u.c, 2 * width, u.on, dg);
+  put16<true, false>(out, u.row, u.c, 2 * width, u.on, dg);
 }
 
-__global__ void __launch_bounds__(kThreads) k_quant_rows(const bf16* x, int64_t x_stride, int rows,
+__global__ void __launch_bounds__(kThreads, 6) k_quant_rows(const bf16* x, int64_t x_stride, int rows,
                                                          int width, RowsOut out) {
   const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(width));
   float v[16];
   unpack16(load16(x + (int64_t)u.row * x_stride, u.c, width, u.on), v);
-  put16<true>(out, u.row, u.c, width, u.on, v);
+  put16<true, true>(out, u.row, u.c, width, u.on, v);
   pdl_trigger();
 }
 

@@ -187,7 +187,6 @@ int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int3
   const cuuint64_t sw[2] = {(cuuint64_t)w->in, (cuuint64_t)w->in * w->out};
   const cuuint64_t dy[2] = {(cuuint64_t)outer, (cuuint64_t)rows};
   const cuuint64_t sy[1] = {(cuuint64_t)(rows > 1 ? y_stride : outer) * 2};
-  const bool pairs = linear_pairs(a);
   if (!encode(&a.x, codes, false, 3, dx, sx, 128) ||
       !encode(&a.xs, codes, false, 3, dx, sx, 32) ||
       !encode(&a.w, w->codes, false, 3, dw, sw, 128) ||
@@ -197,7 +196,7 @@ int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int3
       launch_quant_rows(static_cast<const bf16*>(x->values), x->stride, rows, inner, c->codes,
                         c->scales, s) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return status_of(launch_linear(a, trans, pairs, c->sm_count, x->values != nullptr, s));
+  return status_of(launch_linear(a, trans, c->sm_count, x->values != nullptr, s));
 }
 
 }  // namespace

@@ -70,10 +70,7 @@ struct LinArgs {
 cudaError_t launch_linear_rows(const LinArgs& a, const bf16* x, int64_t x_stride,
                                const uint8_t* codes, const uint8_t* w, int per, cudaStream_t s);
 cudaError_t setup_linear();
-// Whether the launch takes pairs of CTAs.
-bool linear_pairs(const LinArgs& a);
 // trans: y = x W instead of x W^T.
-cudaError_t launch_linear(const LinArgs& a, bool trans, bool pairs, int sm_count, bool pdl,
-                          cudaStream_t s);
+cudaError_t launch_linear(const LinArgs& a, bool trans, int sm_count, bool pdl, cudaStream_t s);
 
 }  // namespace moe
