@@ -876,6 +876,7 @@ class QuantRows:
         self.codes, self.scales = codes, scales
         self.shape = tuple(codes.shape)
         self._c = moe_rows(None, 0, codes.data_ptr(), scales.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, rows: int, width: int, device="cuda"):
@@ -947,6 +948,8 @@ class ExpertOps:
         _check(rc, "moe_ops_create")
         self.ctx = h
         self._lib = load_library()
+        self._bf16 = moe_rows(None, 0, None, None)
+        self._bf16_ref = ctypes.byref(self._bf16)
 
     def close(self):
         if getattr(self, "ctx", None):
@@ -967,28 +970,28 @@ class ExpertOps:
 
     def _rows2(self, t, what: str, rows=None, width=None) -> int:
         """Row stride of a bf16 tensor [rows, width] of this device."""
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or \
-                t.get_device() != self.device or t.dim() != 2 or \
-                (rows is not None and t.shape[0] != rows) or \
-                (width is not None and t.shape[1] != width):
-            raise ValueError(f"{what} must be a bf16 tensor "
-                             f"[{'rows' if rows is None else rows}, "
-                             f"{'width' if width is None else width}] of CUDA device "
-                             f"{self.device}")
-        if t.stride(1) != 1 and t.numel() and t.shape[1] > 1:
-            raise ValueError(f"{what}: the values of a row must lie side by side")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and \
+                t.get_device() == self.device and t.dim() == 2:
+            n, w = t.shape
+            if (rows is None or n == rows) and (width is None or w == width):
+                sr, sc = t.stride()
+                if sc != 1 and w > 1 and n:
+                    raise ValueError(f"{what}: the values of a row must lie side by side")
+                return sr if n > 1 else w
+        raise ValueError(f"{what} must be a bf16 tensor [{'rows' if rows is None else rows}, "
+                         f"{'width' if width is None else width}] of CUDA device {self.device}")
 
     def _form(self, t, what: str, rows=None, width=None):
-        """A moe_rows of either form, by reference."""
+        """A moe_rows of either form, by reference (one at a time: bf16 rows' is reused)."""
         if isinstance(t, QuantRows):
             if t.device != self.device or (rows is not None and t.shape[0] != rows) or \
                     (width is not None and t.shape[1] != width):
                 raise ValueError(f"{what} must be QuantRows [{rows}, {width}] of CUDA device "
                                  f"{self.device}")
-            return ctypes.byref(t._c)
-        stride = self._rows2(t, what, rows, width)
-        return ctypes.byref(moe_rows(t.data_ptr(), stride, None, None))
+            return t._ref
+        self._bf16.stride = self._rows2(t, what, rows, width)
+        self._bf16.values = t.data_ptr()
+        return self._bf16_ref
 
     def _new(self, rows: int, width: int, quantize: bool = False):
         dev = torch.device("cuda", self.device)

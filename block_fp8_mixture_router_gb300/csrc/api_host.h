@@ -13,13 +13,14 @@
 
 namespace moe {
 
-// The calling thread's device, set for a scope.
+// The calling thread's device, set for a scope (and left alone where it is the one already).
 struct Device {
   int prev = -1;
   bool ok = false;
   explicit Device(int dev) {
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = cudaSetDevice(dev) == cudaSuccess;
+    ok = prev == dev || cudaSetDevice(dev) == cudaSuccess;
+    if (prev == dev) prev = -1;
   }
   ~Device() {
     if (prev >= 0) cudaSetDevice(prev);

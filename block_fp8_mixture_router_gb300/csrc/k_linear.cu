@@ -131,6 +131,7 @@ __device__ __forceinline__ void group_tiles(const LinArgs& a, LinSmem& sm) {
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, LinSmem& sm,
                                          int* status) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
   const bool ok = tc::wait_bounded(bar, parity, &sm.abort, status);
   return !__any_sync(0xffffffffu, !ok);
 }
@@ -339,6 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
                              (kTrans ? kIdescBMajorN : 0u);
       for (int b = 0; b < blocks; ++b, turn ^= 1u) {
         if (turn != tb) continue;
+        // (in this order: a stage's phases go to the two warps in turn, and only the buffer's
+        // return says that the other's was over, without which its parity means nothing)
         ok = wait_all(&sm.tempty[tb], tph ^ 1u, sm, a.status) &&
              wait_all(&sm.full[st], ph, sm, a.status);
         if (!ok) break;

@@ -1,7 +1,7 @@
 // The block-FP8 product for few rows of a group, bounded by the weights' bytes and, for a
 // single row, by latency: one launch, rows quantised where they are used, no shared operand.
 //
-// A CTA takes 16 outputs of up to 8 kNt rows of a group.  Its eight warps share the blocks of
+// A CTA takes 16 outputs of up to eight rows of a group.  Its eight warps share the blocks of
 // 128 along the contraction: a warp loads a block's 16 x 128 weights straight into the
 // fragments of warp MMAs (m16n8k32, the order of K relabelled alike on both sides, see
 // mma_e4m3_k64), so that all of a CTA's weights are on their way at once and nothing waits
@@ -16,18 +16,15 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kBatch = 2;   // blocks whose weights a warp has on their way
+constexpr int kRows = 8;    // rows of a group to a CTA
 
 // The tile of rows with this number: its group, first row and rows (0: there is none).
 struct RowTile {
   int g, row0, n;
 };
 
-// kPer row tiles' rows; by the whole block.
-__device__ __forceinline__ RowTile row_tile(const LinArgs& a, int per, int item, RowTile* s) {
-  if (!a.starts) {
-    const int row0 = item * per;
-    return RowTile{0, row0, min(per, a.rows - row0)};
-  }
+__device__ __forceinline__ RowTile row_tile(const LinArgs& a, int item, RowTile* s) {
+  if (!a.starts) return RowTile{0, item * kRows, min(kRows, a.rows - item * kRows)};
   if (threadIdx.x < 32) {
     constexpr int kPer = kMaxExperts / 32;
     const int lane = threadIdx.x;
@@ -44,7 +41,7 @@ __device__ __forceinline__ RowTile row_tile(const LinArgs& a, int per, int item,
         count[i] = end - start[i];
         bad |= start[i] != s0 || end != s1;
       }
-      sum += (count[i] + per - 1) / per;
+      sum += (count[i] + kRows - 1) / kRows;
     }
     if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kOpsBadOrder);
     int incl = sum;
@@ -58,9 +55,9 @@ __device__ __forceinline__ RowTile row_tile(const LinArgs& a, int per, int item,
     if (at >= 0 && at < sum) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int tiles = (count[i] + per - 1) / per;
+        const int tiles = (count[i] + kRows - 1) / kRows;
         if (at >= 0 && at < tiles)
-          *s = RowTile{kPer * lane + i, start[i] + per * at, min(per, count[i] - per * at)};
+          *s = RowTile{kPer * lane + i, start[i] + kRows * at, min(kRows, count[i] - kRows * at)};
         at -= tiles;
       }
     }
@@ -85,24 +82,22 @@ __device__ __forceinline__ void quant32(const bf16* row, int c, int width, bool 
   *scale = quant_codes<2, true>(v, m, b);
 }
 
-template <bool kCodes, int kNt>
+template <bool kCodes>
 __global__ void __launch_bounds__(kThreads) k_linear_rows(const __grid_constant__ LinArgs a,
                                                           const bf16* x, int64_t x_stride,
                                                           const uint8_t* codes, const uint8_t* w) {
   __shared__ RowTile s_tile;
-  __shared__ float red[kWarps][kNt * 8][17];  // (17: rows apart by other banks)
-  const RowTile t = row_tile(a, 8 * kNt, blockIdx.y, &s_tile);
+  __shared__ float red[kWarps][kRows][17];  // (17: rows apart by other banks)
+  const RowTile t = row_tile(a, blockIdx.y, &s_tile);
   if (t.n <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q = lane & 3;
   const int n0 = 16 * blockIdx.x, blocks = groups_of(a.inner);
   const uint8_t* w0 = w + ((size_t)t.g * a.outer + n0 + r) * a.inner;
   const uint8_t* w8 = w0 + (size_t)8 * a.inner;
   const float* sw = a.sw + ((size_t)t.g * groups_of(a.outer) + n0 / kGroup) * blocks;
-  float acc[kNt][4];
-#pragma unroll
-  for (int i = 0; i < kNt; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool on = r < t.n;                      // lane's row, of the B fragments
+  const int64_t row = t.row0 + (on ? r : 0);
   for (int b0 = warp; b0 < blocks; b0 += kBatch * kWarps) {
     uint4 lo[kBatch][2], hi[kBatch][2];
     float ws[kBatch];
@@ -125,45 +120,36 @@ __global__ void __launch_bounds__(kThreads) k_linear_rows(const __grid_constant_
       const int b = b0 + k * kWarps;
       if (b >= blocks) break;
       const int c = b * kGroup + 16 * q;
-#pragma unroll
-      for (int i = 0; i < kNt; ++i) {
-        const int m = 8 * i + r;
-        const bool on = m < t.n;
-        const int64_t row = t.row0 + (on ? m : 0);
-        uint4 v[2];
-        float s;
-        if constexpr (kCodes) {
-          const uint8_t* p = codes + row * a.inner;
-          v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
-          if (on && c < a.inner) v[0] = __ldg(reinterpret_cast<const uint4*>(p + c));
-          if (on && c + 64 < a.inner) v[1] = __ldg(reinterpret_cast<const uint4*>(p + c + 64));
-          s = __ldg(a.sx + row * blocks + b);
-        } else {
-          quant32(x + row * x_stride, c, a.inner, on, v, &s);
-        }
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma_e4m3_k64(d, lo[k][0], hi[k][0], v[0]);
-        mma_e4m3_k64(d, lo[k][1], hi[k][1], v[1]);
-        // columns 2q and 2q + 1 of the products are the rows of lanes 8q and 8q + 4
-        const float s0 = ws[k] * __shfl_sync(0xffffffffu, s, 8 * q);
-        const float s1 = ws[k] * __shfl_sync(0xffffffffu, s, 8 * q + 4);
-        acc[i][0] = fmaf(d[0], s0, acc[i][0]);
-        acc[i][1] = fmaf(d[1], s1, acc[i][1]);
-        acc[i][2] = fmaf(d[2], s0, acc[i][2]);
-        acc[i][3] = fmaf(d[3], s1, acc[i][3]);
+      uint4 v[2];
+      float s;
+      if constexpr (kCodes) {
+        const uint8_t* p = codes + row * a.inner;
+        v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (on && c < a.inner) v[0] = __ldg(reinterpret_cast<const uint4*>(p + c));
+        if (on && c + 64 < a.inner) v[1] = __ldg(reinterpret_cast<const uint4*>(p + c + 64));
+        s = __ldg(a.sx + row * blocks + b);
+      } else {
+        quant32(x + row * x_stride, c, a.inner, on, v, &s);
       }
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma_e4m3_k64(d, lo[k][0], hi[k][0], v[0]);
+      mma_e4m3_k64(d, lo[k][1], hi[k][1], v[1]);
+      // columns 2q and 2q + 1 of the products are the rows of lanes 8q and 8q + 4
+      const float s0 = ws[k] * __shfl_sync(0xffffffffu, s, 8 * q);
+      const float s1 = ws[k] * __shfl_sync(0xffffffffu, s, 8 * q + 4);
+      acc[0] = fmaf(d[0], s0, acc[0]);
+      acc[1] = fmaf(d[1], s1, acc[1]);
+      acc[2] = fmaf(d[2], s0, acc[2]);
+      acc[3] = fmaf(d[3], s1, acc[3]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kNt; ++i) {
-    red[warp][8 * i + 2 * q][r] = acc[i][0];
-    red[warp][8 * i + 2 * q + 1][r] = acc[i][1];
-    red[warp][8 * i + 2 * q][r + 8] = acc[i][2];
-    red[warp][8 * i + 2 * q + 1][r + 8] = acc[i][3];
-  }
+  red[warp][2 * q][r] = acc[0];
+  red[warp][2 * q + 1][r] = acc[1];
+  red[warp][2 * q][r + 8] = acc[2];
+  red[warp][2 * q + 1][r + 8] = acc[3];
   __syncthreads();
   const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
-  if (m < t.n && m < 8 * kNt) {
+  if (m < t.n) {
     float y = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) y += red[i][m][n];
@@ -171,26 +157,19 @@ __global__ void __launch_bounds__(kThreads) k_linear_rows(const __grid_constant_
   }
 }
 
-template <bool kCodes, int kNt>
-cudaError_t launch(const LinArgs& a, const bf16* x, int64_t x_stride, const uint8_t* codes,
-                   const uint8_t* w, cudaStream_t s) {
-  const int full = a.rows / (8 * kNt);
-  const int tiles = a.starts ? full + (a.groups < a.rows ? a.groups : a.rows)
-                             : (a.rows + 8 * kNt - 1) / (8 * kNt);
-  k_linear_rows<kCodes, kNt><<<dim3(a.outer / 16, tiles), kThreads, 0, s>>>(a, x, x_stride, codes,
-                                                                            w);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_linear_rows(const LinArgs& a, const bf16* x, int64_t x_stride,
-                               const uint8_t* codes, const uint8_t* w, int per, cudaStream_t s) {
+                               const uint8_t* codes, const uint8_t* w, cudaStream_t s) {
+  // (the most there can be; a tile that is not there ends at once)
+  const int tiles = a.starts ? a.rows / kRows + (a.groups < a.rows ? a.groups : a.rows)
+                             : (a.rows + kRows - 1) / kRows;
+  const dim3 grid(a.outer / 16, tiles);
   if (codes)
-    return per <= 8 ? launch<true, 1>(a, nullptr, 0, codes, w, s)
-                    : launch<true, 2>(a, nullptr, 0, codes, w, s);
-  return per <= 8 ? launch<false, 1>(a, x, x_stride, nullptr, w, s)
-                  : launch<false, 2>(a, x, x_stride, nullptr, w, s);
+    k_linear_rows<true><<<grid, kThreads, 0, s>>>(a, x, x_stride, codes, w);
+  else
+    k_linear_rows<false><<<grid, kThreads, 0, s>>>(a, x, x_stride, codes, w);
+  return cudaGetLastError();
 }
 
 }  // namespace moe

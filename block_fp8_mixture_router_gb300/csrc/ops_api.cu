@@ -4,7 +4,6 @@
 // sizes are checked against the cap before anything is allocated, and every refusal is a
 // status code.
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <new>
@@ -140,11 +139,18 @@ bool encode(CUtensorMap* m, const void* p, bool in_bf16, int rank, const cuuint6
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a group that a CTA of the kernel for few rows takes, 0: the tensor-core kernel.
-int few_rows(int rows, int groups) {
-  static const char* env = getenv("MOE_FEW");
-  if (env) return atoi(env);
-  return rows <= 8 * groups ? 8 : rows <= 16 * groups ? 16 : 0;
+// Whether the kernel for few rows takes a product.  It costs the work of its row tiles (of
+// eight rows of a group), each on all of the group's weights, about 3.5 M weights a
+// microsecond; the tensor-core kernel's time is that of one tile's blocks, some 3 us and
+// 0.0035 for each value of the contraction, as long as it has an SM for every tile.
+// Measured, few / tensor-core kernel, in us, bf16 rows:
+//   2560 x 2048: 1 row 3.9 / 11.6, 16 6.1 / 12.0, 48 12.4 / 12.1, 96 21 / 11.5
+//   512 x 2048: 128 rows 8.0 / 11.8;  4096 x 4096: 8 7.0 / 17.6, 24 17.8 / 18.1, 48 31 / 18.0
+//   256 experts of 1024 x 2048, rows of 1, 2, 4 tokens, eight each: 5.9 / 12.0, 9.6 / 12.0,
+//   16.8 / 14.1; 64 experts, 4, 16, 32 tokens: 11.2 / 12.7, 26 / 27, 33 / 30.
+bool few_rows(int rows, int groups, int inner, int outer) {
+  const int64_t tiles = std::max((rows + 7) / 8, std::min(groups, rows));
+  return tiles * inner * outer <= 9000000 + (int64_t)12300 * inner;
 }
 
 int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int32_t* starts,
@@ -177,9 +183,9 @@ int linear(moe_ops* c, const moe_rows* x, const moe_block_weights* w, const int3
   a.y = static_cast<bf16*>(y);
   a.y_stride = y_stride;
   a.status = c->status;
-  if (const int per = trans ? 0 : few_rows(rows, starts ? w->groups : 1))
+  if (!trans && few_rows(rows, w->groups, inner, outer))
     return status_of(launch_linear_rows(a, static_cast<const bf16*>(x->values), x->stride,
-                                        x->codes, w->codes, per, s));
+                                        x->codes, w->codes, s));
   // (x as one group, so that one form of copy takes rows and weights)
   const cuuint64_t dx[3] = {(cuuint64_t)inner, (cuuint64_t)rows, 1};
   const cuuint64_t sx[2] = {(cuuint64_t)inner, (cuuint64_t)inner * rows};

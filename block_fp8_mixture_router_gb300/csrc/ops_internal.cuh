@@ -65,10 +65,9 @@ struct LinArgs {
   int64_t y_stride;
   int* status;
 };
-// Few rows to a group (k_linear_rows.cu): x bf16 or codes, the weights' codes; `per` rows of a
-// group to a CTA, 8 or 16.
+// Few rows (k_linear_rows.cu): x bf16, or codes; the weights' codes.
 cudaError_t launch_linear_rows(const LinArgs& a, const bf16* x, int64_t x_stride,
-                               const uint8_t* codes, const uint8_t* w, int per, cudaStream_t s);
+                               const uint8_t* codes, const uint8_t* w, cudaStream_t s);
 cudaError_t setup_linear();
 // trans: y = x W instead of x W^T.
 cudaError_t launch_linear(const LinArgs& a, bool trans, int sm_count, bool pdl, cudaStream_t s);

@@ -3,7 +3,6 @@ rational arithmetic: two steps give the IEEE quotient, one step gives its e4m3 c
 pair of bf16 value and bf16 largest value."""
 from __future__ import annotations
 
-import math
 import random
 from fractions import Fraction as F
 
@@ -20,7 +19,7 @@ def rounded(x: F, bits: int) -> F:
     n, r = divmod(a / u, 1)
     if r > F(1, 2) or (r == F(1, 2) and n % 2):
         n += 1
-    return math.copysign(1, x) * F(0) + (n * u if x > 0 else -n * u)
+    return n * u if x > 0 else -n * u
 
 
 def f32(x: F) -> F:
