@@ -4,6 +4,8 @@ GB300)."""
 from __future__ import annotations
 
 import ctypes
+import os
+import sys
 
 import pytest
 import torch
@@ -15,6 +17,10 @@ pytestmark = pytest.mark.gpu
 
 m = pytest.importorskip("block_fp8_mixture_router_gb300")
 
+sys.path.insert(0, os.path.join(os.path.dirname(__file__), os.pardir, "examples"))
+
+import expert_parts as P  # noqa: E402
+
 
 @pytest.fixture(scope="module")
 def dev():
@@ -24,35 +30,6 @@ def dev():
     return torch.device("cuda", 0)
 
 
-class Experts:
-    """The routed half of a layer from its parts, forward and backward."""
-
-    def __init__(self, shape, layer, tokens, quantize=True):
-        self.shape, self.q = shape, quantize
-        self.w13 = m.BlockWeights(layer["w13"], layer["s13"])
-        self.w2 = m.BlockWeights(layer["w2"], layer["s2"])
-        self.ops = m.ExpertOps(shape.n_experts, shape.top_k, tokens,
-                               max(shape.hidden, 2 * shape.inter))
-
-    def forward(self, x, idx, w):
-        o = self.ops
-        self.x, self.w = x, w
-        self.order, rows = o.dispatch(x, idx, quantize=self.q)
-        starts = self.order.starts
-        self.gate_up = o.linear(rows, self.w13, starts=starts)
-        self.h = o.swiglu(self.gate_up, quantize=self.q)
-        self.out = o.linear(self.h, self.w2, starts=starts)
-        return o.combine(self.out, self.order, w)
-
-    def backward(self, dy):
-        o, starts = self.ops, self.order.starts
-        self.dout, dw = o.combine_grad(dy, self.out, self.order, self.w, quantize=self.q)
-        self.dh = o.linear_grad(self.dout, self.w2, starts=starts)
-        self.dgate_up = o.swiglu_grad(self.dh, self.gate_up, quantize=self.q)
-        self.drows = o.linear_grad(self.dgate_up, self.w13, starts=starts)
-        return o.dispatch_grad(self.drows, self.order), dw
-
-
 def make(dev, shape, tokens, seed=0, quantize=True, kind="normal"):
     layer = W.make_layer(shape, seed, kind, device=dev)
     for n in ("ws13", "ws2"):
@@ -60,7 +37,7 @@ def make(dev, shape, tokens, seed=0, quantize=True, kind="normal"):
     net = m.MoELayer(m.LayerShape(shape.hidden, shape.n_experts, shape.top_k, shape.inter,
                                   shape.shared_inter), tokens)
     net.load(layer)
-    return net, Experts(shape, layer, tokens, quantize)
+    return net, P.Experts(shape, layer, tokens, quantize)
 
 
 @pytest.mark.parametrize("quantize", [True, False])
@@ -206,6 +183,11 @@ def test_takes_the_add_norms_codes(dev):
     _, xn, codes, scales = net.add_rmsnorm_quantize(r, x, g, W.NORM_EPS)
     wt = m.BlockWeights(p.w13.codes[0], p.w13.scales[0])
     assert torch.equal(p.ops.linear(m.QuantRows(codes, scales), wt), p.ops.linear(xn, wt))
+
+
+def test_example_runs(dev, capsys):
+    P.main(tokens=200, steps=2, shape=W.TINY)
+    assert "us a step" in capsys.readouterr().out
 
 
 # ---- refusals ---------------------------------------------------------------

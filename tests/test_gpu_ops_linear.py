@@ -88,6 +88,8 @@ def test_one_group(dev, size, trans):
 def test_groups(dev, counts, trans):
     check(dev, counts, 400, 272, trans, True)
     check(dev, counts, 512, 640, trans, False, rows=sum(counts) + 13)
+    # few rows of weights this large are few rows to the one kernel, many to the other
+    check(dev, counts, 1552, 1808, trans, len(counts) % 2 == 0)
 
 
 def test_many_tiles(dev):
@@ -133,43 +135,64 @@ def test_strides(dev, rows):
     assert bool((dx[:, :8] == 4).all()) and bool((dx[:, 264:] == 4).all())
 
 
+@pytest.mark.parametrize("call", ["linear", "linear_grad"])
 @pytest.mark.parametrize("rows", [6, 150])
-def test_bad_values_stay_in_their_rows(dev, rows):
-    w = weights(dev, 1, 272, 256)
+def test_bad_values_stay_in_their_rows(dev, rows, call):
+    w = weights(dev, 1, 256, 256)
     ops = m.ExpertOps(1, 1, rows, 256)
+    call = getattr(ops, call)
     x = torch.randn((rows, 256), generator=gen(dev, 1), device=dev).bfloat16()
-    clean = ops.linear(x, w)
+    clean = call(x, w)
     x[1, 3], x[4, 255] = float("inf"), float("nan")
-    y = ops.linear(x, w)
+    y = call(x, w)
     assert bool(y[1].isnan().all()) and bool(y[4].isnan().all())
     keep = [r for r in range(rows) if r not in (1, 4)]
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("call", ["linear", "linear_grad"])
 @pytest.mark.parametrize("rows", [3, 40, 500])
-def test_repeats_bit_for_bit(dev, rows):
-    w = weights(dev, 3, 400, 1040)
+def test_repeats_bit_for_bit(dev, rows, call):
+    w = weights(dev, 3, 1040, 1040)
     ops = m.ExpertOps(3, 1, rows, 1040)
+    call = getattr(ops, call)
     x = torch.randn((rows, 1040), generator=gen(dev, 1), device=dev).bfloat16()
     starts = starts_of([rows // 3, 1, rows - rows // 3 - 1], dev)
-    first = ops.linear(x, w, starts=starts)
+    first = call(x, w, starts=starts)
     for _ in range(5):
-        assert torch.equal(first, ops.linear(x, w, starts=starts))
+        assert torch.equal(first, call(x, w, starts=starts))
 
 
 @pytest.mark.parametrize("bad", [[0, 50, 20, 60], [-5, 10, 20, 60], [0, 10, 20, 1 << 30],
                                  [70, 80, 90, 100], [60, 40, 20, 0]])
-def test_bad_starts_are_reported(dev, bad):
+@pytest.mark.parametrize("call", ["linear", "linear_grad"])
+def test_bad_starts_are_reported(dev, bad, call):
     w = weights(dev, 3, 128, 128)
     ops = m.ExpertOps(3, 1, 60, 128)
     x = torch.randn((60, 128), generator=gen(dev, 1), device=dev).bfloat16()
     buf = torch.full((62, 128), 3.0, dtype=torch.bfloat16, device=dev)
-    ops.linear(x, w, starts=torch.tensor(bad, dtype=torch.int32, device=dev), out=buf[1:61])
+    getattr(ops, call)(x, w, starts=torch.tensor(bad, dtype=torch.int32, device=dev),
+                       out=buf[1:61])
     assert ops.device_status() == m.MOE_ERR_INVALID_ARG
     assert ops.device_status() == m.MOE_OK
     assert bool((buf[0] == 3).all()) and bool((buf[61] == 3).all())
     y = ops.linear(x, w, starts=torch.tensor([0, 20, 40, 60], dtype=torch.int32, device=dev))
     assert bool(torch.isfinite(y).all()) and ops.device_status() == m.MOE_OK
+
+
+def test_starts_that_overlap_again_and_again(dev):
+    """256 groups, every second of all rows: bounds that any sum of tiles would pass."""
+    rows = 65536
+    w = weights(dev, 256, 16, 16)
+    ops = m.ExpertOps(256, 1, rows, 16)
+    starts = torch.zeros(257, dtype=torch.int32, device=dev)
+    starts[1::2] = rows
+    x = torch.randn((rows, 16), generator=gen(dev, 1), device=dev).bfloat16()
+    for call in (ops.linear, ops.linear_grad):
+        buf = torch.full((rows + 2, 16), 3.0, dtype=torch.bfloat16, device=dev)
+        call(x, w, starts=starts, out=buf[1:-1])
+        assert ops.device_status() == m.MOE_ERR_INVALID_ARG
+        assert bool((buf[0] == 3).all()) and bool((buf[-1] == 3).all())
 
 
 def test_long_offsets(dev):
