@@ -38,8 +38,8 @@ constexpr int kWarpStore = kSumWarps + 4, kStoreWarps = 4;
 constexpr int kThreads = 32 * (kWarpStore + kStoreWarps);
 // Registers of a thread: sixteen warps start with 128; the two warpgroups that hold 128 sums
 // and 64 products on their way take what the others give.
-constexpr int kSumRegs = 216, kFeedRegs = 40, kStoreRegs = 40;
-static_assert(2 * kSumRegs + kFeedRegs + kStoreRegs <= 4 * 128, "no more registers than at launch");
+constexpr int kSumRegs = 216, kOtherRegs = 40;
+static_assert(2 * kSumRegs + 2 * kOtherRegs <= 4 * 128, "no more registers than at launch");
 constexpr int kABytes = kBM * kKB, kBBytes = kBN * kKB, kStageBytes = kABytes + kBBytes;
 constexpr int kStages = 3;
 constexpr int kHalf = kBN / 2;                   // columns of a box of weights
@@ -261,8 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
   const int first = blockIdx.x, step = gridDim.x;
   const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;  // this CTA's tiles
 
-  if (warp >= kWarpStore) fewer_regs<kStoreRegs>();
-  else if (warp >= kSumWarps) fewer_regs<kFeedRegs>();
+  if (warp >= kSumWarps) fewer_regs<kOtherRegs>();
   if (warp == kWarpTma) {
     uint32_t st = 0, ph = 0;
     int issued = 0;
