@@ -9,6 +9,10 @@
 //
 // The rows' bytes bound all of it (a row moves once each way); the sort is a few
 // microseconds in front.  No atomics order anything: a pair's slot follows from counts.
+//   16384 tokens of 2048, eight experts of 256 each:  99 us, 92 % of the copy's rate (the
+//     gather 89; the order alone 7 us)
+//   11 tokens to codes 3.4 us, one launch;  weighted back: 16384 tokens 91 us (100 %), one 2.6
+//   the gather's gradient, 5003 tokens of 2560, four of six pairs each: 24 us (79 %)
 #include "rows_device.cuh"
 
 namespace moe {
@@ -84,8 +88,11 @@ __device__ __forceinline__ void gather_rows(const bf16* x, int64_t x_stride, int
 // ---- few pairs: one launch --------------------------------------------------------
 // Every block counts all pairs itself (in front of its own tokens and in all), so that no
 // block waits for another; then it places its tokens' pairs and gathers their rows.
+// Up to 1536 tokens of eight pairs, near where both ways take as long (order, and rows of
+// 2048, this way and the other: 64 tokens 3.1 and 5.8 us, 1024 8.9 and 11.4, 1500 11.9 and
+// 13.2, 2048 17.4 and 16.2, 4096 38.8 and 31.0).
 constexpr int kSmallThreads = 512;
-constexpr int kSmallPairs = 16384;
+constexpr int kSmallPairs = 12288;
 
 template <bool kCodes>
 __global__ void __launch_bounds__(kSmallThreads) k_dispatch_small(OrderArgs o, const int* idx,
@@ -157,6 +164,18 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(OrderArgs o, const 
   pdl_trigger();
 }
 
+// The lanes whose expert this lane's is, bit by bit (__match_any_sync takes a turn for each
+// expert among the lanes: 1.2 us more).
+__device__ __forceinline__ unsigned same_expert(int e, bool in) {
+  unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+  for (int b = 1; b < kMaxExperts; b <<= 1) {
+    const unsigned set = __ballot_sync(0xffffffffu, e & b);
+    same &= e & b ? set : ~set;
+  }
+  return same;
+}
+
 // Warp w takes the block's pairs 64 w .. 64 w + 63.  A pair's place among its expert's is
 // the count of the blocks in front, of the warps in front, and of the lanes in front.
 __global__ void __launch_bounds__(kSortThreads) k_sort_place(OrderArgs o, const int* idx,
@@ -176,7 +195,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(OrderArgs o, const 
     const int p = blockIdx.x * kSortPairs + 64 * warp + 32 * i + lane;
     e[i] = p < P ? __ldg(idx + p) : -1;
     const bool in = there(e[i], o.E);
-    const unsigned same = __match_any_sync(0xffffffffu, in ? e[i] : -1);
+    const unsigned same = same_expert(e[i], in);
     const unsigned lower = same & ((1u << lane) - 1);
     rank[i] = __popc(lower) + (in ? of_warp[warp][e[i]] : 0);
     __syncwarp();
@@ -288,7 +307,11 @@ __global__ void __launch_bounds__(kBackThreads, 6) k_combine(OrderArgs o, const 
   *reinterpret_cast<uint4*>(y + (int64_t)t * y_stride + c) = pack8(acc);
 }
 
-// A warp takes a pair: the dot product of dy with its row, and the row's gradient.
+// A warp takes a pair: the dot product of dy with its row, and the row's gradient.  4099 tokens
+// of eight rows of 2048 to codes: 45 us, 73 % of the copy's rate; the quotients keep the
+// schedulers busy in two thirds of the cycles.  (Five blocks to an SM; 60 us without a bound on
+// registers; a block to a token, with dy and its groups' magnitudes kept for all of its pairs,
+// 52.)
 template <bool kCodes>
 __global__ void __launch_bounds__(kBackThreads, 5) k_combine_grad(OrderArgs o, const bf16* dy,
                                                                int64_t dy_stride, const bf16* rows,

@@ -8,6 +8,11 @@
 // for a barrier before the sums of the warps are added, in warp order, at the end.  The lanes
 // of a row's fragment hold 32 of its 128 values each, so a group's largest is two shuffles
 // away and a bf16 row needs no launch in front that quantises it.
+//
+// One bf16 row x 2048 x 2560 takes 3.9 us (5.2 MB of weights: 0.8 us at HBM's rate; launch, one
+// round of loads, the sums' exchange), 4.8 where the weights come from HBM; eight rows 4.3;
+// eight rows of eight experts of 1024 x 2048 5.9.  With 16 rows to a CTA (two products of each
+// fragment) the same sizes took 6.3, 6.7 and 8.8 us: twice the quantisation in each warp.
 #include "rows_device.cuh"
 
 namespace moe {

@@ -3,9 +3,13 @@
 //
 //   h = silu(g) u,  dg = dh u s (1 + g (1 - s)),  du = dh silu(g),  s = 1 / (1 + e^-g)
 //
-// Every value is read and written once, so HBM bounds them.  Eight lanes take a group of
-// 128 columns, 16 values each: the group's largest is then three shuffles away and a lane's
-// loads and stores are 16-byte vectors.
+// Every value is read and written once, so HBM bounds them, and the quotients behind codes
+// nearly do: 131072 rows of 512 to codes 58 us (87 % of the copy's rate; the schedulers issue
+// in 78 % of cycles), the gradient of 10493 rows of 1408 in bf16 23 us (96 %), 131072 rows of
+// 1024 quantised 68 us (88 %).  Eight lanes take a group of 128 columns, 16 values each: the
+// group's largest is then three shuffles away and a lane's loads and stores are 16-byte
+// vectors.  Blocks to an SM as measured: six for what has few values in flight (62 us with
+// four for the first), four for the gradient (27 us with six).
 #include "rows_device.cuh"
 
 namespace moe {

@@ -53,7 +53,8 @@ def sentinel(rows, width, dev, quantize, ops):
 CASES = [  # tokens, top_k, experts, width, kind
     (1, 8, 256, 2048, "distinct"), (1, 1, 1, 16, "any"), (11, 8, 256, 2048, "distinct"),
     (3, 16, 4, 128, "any"), (153, 8, 256, 272, "dropped"), (700, 6, 60, 1040, "any"),
-    (200, 5, 7, 2560, "one"), (64, 2, 3, 144, "none"), (2048, 8, 256, 48, "any"),
+    (200, 5, 7, 2560, "one"), (64, 2, 3, 144, "none"), (1536, 8, 256, 48, "any"),
+    (1537, 8, 256, 80, "dropped"), (2048, 8, 256, 48, "any"),
     (2049, 8, 256, 64, "dropped"), (5000, 7, 100, 128, "any"), (20000, 1, 5, 16, "dropped"),
     (9001, 16, 256, 32, "one"), (65536, 16, 256, 16, "any")]
 
