@@ -937,7 +937,8 @@ class ExpertOrder:
 class ExpertOps:
     """The layer's parts as operators, with their gradients, on one GPU: owns a context and
     its workspace (moe_ops_config in include/moe.h).  Rows are bf16 tensors [rows, width], or
-    QuantRows; `out` may be given in either form, `quantize` asks for new QuantRows."""
+    QuantRows; `out` may be given in either form, `quantize` asks for new QuantRows.  The
+    gradients are calls of their own: nothing here is recorded by torch.autograd."""
 
     def __init__(self, n_experts: int = 256, top_k: int = 8, max_rows: int = 1024,
                  max_width: int = 2048, device: int = 0, workspace_cap_bytes: int = 0):

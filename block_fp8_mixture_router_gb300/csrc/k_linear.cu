@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
     };
     const auto load = [&](int b) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) nx[r] = __ldg(a.sx + (sx[r] + b));
+      for (int r = 0; r < 4; ++r) nx[r] = a.sx[sx[r] + b];  // (of the launch in front: no ldg)
       nw0 = __ldg(a.sw + (sw0 + b * sw_step));
       nw1 = __ldg(a.sw + (sw1 + b * sw_step));
     };

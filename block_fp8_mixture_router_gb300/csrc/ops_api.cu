@@ -82,9 +82,16 @@ bool overlaps(const void* v, int64_t stride, int width, int rows, const moe_rows
   if (rows < 1 || r_rows < 1) return false;
   const size_t bytes = 2 * ((size_t)(rows - 1) * stride + width);
   if (r->values) {
-    if (rows == r_rows)
-      return overlap_rows(v, stride, width, r->values, r->stride, r_width, rows);
-    return bytes_overlap(v, bytes, r->values, 2 * ((size_t)(r_rows - 1) * r->stride + r_width));
+    // runs of as many rows of the longer array as the shorter one has
+    const int run = std::min(rows, r_rows), all = std::max(rows, r_rows);
+    for (int i = 0; i < all; i += run) {
+      const bf16* a = static_cast<const bf16*>(v) + (rows > r_rows ? (int64_t)i * stride : 0);
+      const bf16* b = static_cast<const bf16*>(r->values) +
+                      (r_rows > rows ? (int64_t)i * r->stride : 0);
+      if (overlap_rows(a, stride, width, b, r->stride, r_width, std::min(run, all - i)))
+        return true;
+    }
+    return false;
   }
   return bytes_overlap(v, bytes, r->codes, (size_t)r_rows * r_width) ||
          bytes_overlap(v, bytes, r->scales, (size_t)r_rows * groups_of(r_width) * 4);
@@ -136,7 +143,8 @@ bool encode(CUtensorMap* m, const void* p, bool in_bf16, int rank, const cuuint6
   const cuuint32_t unit[3] = {1, 1, 1};
   return fn(m, in_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
             const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Whether the kernel for few rows takes a product.  It costs the work of its row tiles (of

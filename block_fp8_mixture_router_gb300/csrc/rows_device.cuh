@@ -66,8 +66,8 @@ __device__ __forceinline__ Vec16 pack16(const float (&v)[16]) { return {pack8(v)
 template <bool kShort = false>
 __device__ __forceinline__ float div_by(float v, float s, float y) {
   float q = v * y;
-  q = fmaf(fmaf(-q, s, v), y, q);
-  return kShort ? q : fmaf(fmaf(-q, s, v), y, q);
+  q = fmaf(-fmaf(q, s, -v), y, q);  // (the remainder negated: a zero keeps its sign so)
+  return kShort ? q : fmaf(-fmaf(q, s, -v), y, q);
 }
 
 // Codes of kN x 16 values of a group whose largest magnitude is m: quant4's codes, without its

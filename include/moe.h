@@ -634,7 +634,7 @@ typedef struct {
   size_t workspace_cap_bytes; /* 0 = no cap */
 } moe_ops_config;
 
-/* Rows in one of the two forms, device memory of the caller: `values` (codes and scales
+/* Rows in one of the two forms, device memory of the caller, at most 131072 wide: `values` (codes and scales
  * NULL), bf16, 16-byte aligned, row stride in values a multiple of 8 and at least the width,
  * the width a multiple of 8; or `codes` [rows][width], 16-byte aligned, and `scales`
  * [rows][ceil(width / 128)] (values NULL), the width a multiple of 16. */

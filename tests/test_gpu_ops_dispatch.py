@@ -226,6 +226,47 @@ def test_infinities_and_nans_stay_in_their_rows(dev):
             assert bool(v[row, 200].isnan())
 
 
+def test_codes_at_the_ends_of_the_range(dev):
+    """Groups from bf16's smallest subnormal to its largest value, zeros among them, and rows
+    whose product with a weight is tiny or huge: codes and scales bit for bit."""
+    g = gen(dev, 8)
+    e = torch.tensor([-133, -130, -126, -110, -90, -81, -80, -79, -40, 0, 60, 99, 100, 101, 120,
+                      127], device=dev)
+    tokens, width = len(e) * 3, 400
+    x = torch.randn((tokens, width), generator=g, device=dev).clamp(-1.9, 1.9)
+    x = (x.double() * torch.exp2(e.double()).repeat(3)[:, None]).bfloat16()
+    x[::5, 128:256] = 0.0
+    x[1::7, ::3] = 0.0
+    x[2::7, 5] = -0.0
+    idx = torch.arange(tokens, device=dev, dtype=torch.int32)[:, None] % 7
+    ops = m.ExpertOps(7, 1, tokens, 0)
+    order, got = ops.dispatch(x, idx.contiguous(), quantize=True)
+    codes, scales = R.quantise(x)
+    at = order.pair_of_slot.long()
+    assert torch.equal(got.codes, codes[at]) and torch.equal(got.scales, scales[at])
+    for weight in (1.0, 2.0 ** -30 / 3, 0.0, -2.0 ** 20 / 3):
+        w = torch.full((tokens, 1), weight, device=dev)
+        out, _ = ops.combine_grad(x, x[at].contiguous(), order, w, quantize=True)
+        codes, scales = R.quantise((w * x.float())[at])
+        assert torch.equal(out.scales, scales) and torch.equal(out.codes, codes)
+
+
+def test_columns_of_one_buffer(dev):
+    """Token rows and their pairs' rows as columns of one buffer; sharing a byte is refused."""
+    tokens, k = 6, 3
+    ops = m.ExpertOps(4, k, tokens, 0)
+    idx = experts(dev, tokens, k, 4, "any")
+    buf = torch.zeros((tokens * k, 64), dtype=torch.bfloat16, device=dev)
+    buf[:tokens, :16] = torch.randn((tokens, 16), generator=gen(dev, 9), device=dev).bfloat16()
+    order, rows = ops.dispatch(buf[:tokens, :16], idx, out=buf[:, 16:32])
+    assert torch.equal(rows, buf[:tokens, :16][order.pair_of_slot.long() // k])
+    ops.combine(rows, order, torch.ones((tokens, k), device=dev), out=buf[:tokens, 32:48])
+    for out in (buf[:, 8:24], buf[:, :16]):
+        with pytest.raises(m.MoEError) as e:
+            ops.dispatch(buf[tokens:2 * tokens, :16], idx, out=out)
+        assert e.value.status == m.MOE_ERR_INVALID_ARG
+
+
 def test_long_offsets(dev):
     """Rows whose offsets pass 2^31 values."""
     tokens, k, width = 65536, 9, 4096
