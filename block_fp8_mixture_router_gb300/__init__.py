@@ -949,8 +949,6 @@ class ExpertOps:
         _check(rc, "moe_ops_create")
         self.ctx = h
         self._lib = load_library()
-        self._bf16 = moe_rows(None, 0, None, None)
-        self._bf16_ref = ctypes.byref(self._bf16)
 
     def close(self):
         if getattr(self, "ctx", None):
@@ -971,7 +969,7 @@ class ExpertOps:
 
     def _rows2(self, t, what: str, rows=None, width=None) -> int:
         """Row stride of a bf16 tensor [rows, width] of this device."""
-        if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and \
+        if getattr(t, "dtype", None) is torch.bfloat16 and \
                 t.get_device() == self.device and t.dim() == 2:
             n, w = t.shape
             if (rows is None or n == rows) and (width is None or w == width):
@@ -983,16 +981,16 @@ class ExpertOps:
                          f"{'width' if width is None else width}] of CUDA device {self.device}")
 
     def _form(self, t, what: str, rows=None, width=None):
-        """A moe_rows of either form, by reference (one at a time: bf16 rows' is reused)."""
+        """A moe_rows of either form, by reference (bf16 rows' is new: a second host thread
+        may be between its own and its call)."""
         if isinstance(t, QuantRows):
             if t.device != self.device or (rows is not None and t.shape[0] != rows) or \
                     (width is not None and t.shape[1] != width):
                 raise ValueError(f"{what} must be QuantRows [{rows}, {width}] of CUDA device "
                                  f"{self.device}")
             return t._ref
-        self._bf16.stride = self._rows2(t, what, rows, width)
-        self._bf16.values = t.data_ptr()
-        return self._bf16_ref
+        stride = self._rows2(t, what, rows, width)
+        return ctypes.byref(moe_rows(t.data_ptr(), stride, None, None))
 
     def _new(self, rows: int, width: int, quantize: bool = False):
         dev = torch.device("cuda", self.device)
