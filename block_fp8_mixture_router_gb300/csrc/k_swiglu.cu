@@ -32,6 +32,25 @@ __device__ __forceinline__ Unit unit_of(unsigned u, int rows, int groups) {
   return r;
 }
 
+// The sigmoid of z and that of -z, in fp32 at any z: 1 / (1 + e) with e = e^-|z|, which does
+// not overflow, and e times it, which follows e^-|z| down to fp32's last subnormal and is 0
+// behind it.  (An exponent held back instead leaves z s growing with z at far negative z, and
+// 1 - s, times a far positive z, wants a quotient that is 1 to the last bit.)  e is the square
+// of e^(-|z| / 2), a normal number for all z that matter: neither approximation meets a
+// subnormal, and takes no steps for one.
+struct Sigmoid {
+  float s, other;
+};
+
+__device__ __forceinline__ Sigmoid sigmoid_any(float z) {
+  float root, big;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(root) : "f"(fabsf(z) * -0.721347520444f));
+  const float e = root * root;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(big) : "f"(1.0f + e));
+  const float small = e * big;
+  return z >= 0.0f ? Sigmoid{big, small} : Sigmoid{small, big};
+}
+
 template <bool kCodes>
 __global__ void __launch_bounds__(kThreads, 6) k_swiglu(const bf16* gu, int64_t gu_stride, int rows,
                                                      int width, RowsOut out) {
@@ -42,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 6) k_swiglu(const bf16* gu, int64_t 
   unpack16(rg, g);
   unpack16(ru, v);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] *= silu_f32(g[i]);
+  for (int i = 0; i < 16; ++i) v[i] *= g[i] * sigmoid_any(g[i]).s;
   put16<kCodes, false>(out, u.row, u.c, width, u.on, v);
 }
 
@@ -55,8 +74,9 @@ __device__ __forceinline__ void swiglu_back(const Vec16& rd, const Vec16& rg, co
   unpack16(ru, u);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float s = sigmoid_f32(g[i]), z = g[i] * s;
-    dg[i] = d[i] * u[i] * (s + z * (1.0f - s));
+    const Sigmoid p = sigmoid_any(g[i]);
+    const float z = g[i] * p.s;
+    dg[i] = d[i] * u[i] * (p.s + z * p.other);
     du[i] = d[i] * z;
   }
 }

@@ -744,9 +744,10 @@ int moe_linear(moe_ops* ctx, const moe_rows* x, const moe_block_weights* w, cons
 int moe_linear_grad(moe_ops* ctx, const moe_rows* dy, const moe_block_weights* w,
                     const int32_t* starts, int rows, void* dx, int64_t dx_stride, void* stream);
 
-/* h = silu(gate) x up in fp32: gate_up bf16 [rows][2 width], the gates in front of the ups
- * as a product with moe_weights' w13 leaves them; h [rows][width], rounded to bf16 or
- * quantised once.  rows <= max_rows x top_k, width <= 65536.  Asynchronous.
+/* h = gate s up in fp32, s = 1 / (1 + e^-gate): gate_up bf16 [rows][2 width], the gates in
+ * front of the ups as a product with moe_weights' w13 leaves them; h [rows][width], rounded
+ * to bf16 or quantised once.  s is held in fp32 at any gate: below about -104 it is 0, and h
+ * with it.  A gate of -infinity makes h NaN.  rows <= max_rows x top_k, width <= 65536.  Asynchronous.
  * Defined by: commit "one SwiGLU launch for the routed and shared experts" (routed rows are
  * stored as their FP8 quantization). */
 int moe_swiglu(moe_ops* ctx, const void* gate_up, int64_t gate_up_stride, int rows, int width,
@@ -754,7 +755,8 @@ int moe_swiglu(moe_ops* ctx, const void* gate_up, int64_t gate_up_stride, int ro
 
 /* Its gradient: with s = 1 / (1 + e^-gate), dgate = dh up s (1 + gate (1 - s)) and
  * dup = dh gate s, side by side as [rows][2 width] in either form (128 columns of the 2 width
- * share a scale); dh bf16 [rows][width].  Asynchronous.
+ * share a scale); dh bf16 [rows][width].  An infinite gate makes dgate NaN, one of -infinity
+ * dup too.  Asynchronous.
  * Defined by: the operation of moe_swiglu (commit "one SwiGLU launch for the routed and
  * shared experts"); gradients are this library's. */
 int moe_swiglu_grad(moe_ops* ctx, const void* dh, int64_t dh_stride, const void* gate_up,
