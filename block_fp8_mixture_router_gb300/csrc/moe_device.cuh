@@ -204,13 +204,15 @@ __device__ __forceinline__ uint32_t quant4(float v0, float v1, float v2, float v
   return undecided ? quant4_exact(v0, v1, v2, v3, s) : c;
 }
 
-// silu(z) = z / (1 + e^-z) with the fast exponential and divide; the
-// exponent is clamped so the divisor stays finite (silu(z) is then ~0).
+// silu(z) = z / (1 + e^-z) with the fast exponential and divide, which gives 0 for a finite
+// z and a divisor above 2^126 (z below -87.3, where silu(z) is above -2^-119).  Holding the
+// exponent back instead would leave a quotient that grows with z.
 __device__ __forceinline__ float silu_f32(float z) {
-  return __fdividef(z, 1.0f + __expf(fminf(-z, 80.0f)));
+  return __fdividef(z, 1.0f + __expf(-z));
 }
 
-// Logistic sigmoid with the fast exponential and divide.
+// Logistic sigmoid with the fast exponential and divide; the exponent is held at 80, so it
+// is within 2^-115 of its value below -80.
 __device__ __forceinline__ float sigmoid_f32(float v) {
   return __fdividef(1.0f, 1.0f + __expf(fminf(-v, 80.0f)));
 }
