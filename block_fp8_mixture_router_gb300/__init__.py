@@ -443,6 +443,27 @@ def moe_status_string(status: int) -> str:
 
 # ---- convenience wrapper ---------------------------------------------------
 
+def _made_on(device: int, stream, make):
+    """The tensor make() makes, for a call on `stream` (a torch.cuda.Stream or a handle; None:
+    PyTorch's current stream).  It is made under that stream, so that its memory is the
+    stream's and no other stream's work is still using it, and recorded for the current one,
+    where the caller will go on with it."""
+    if stream is None:
+        return make()
+    handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(device):
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (handles 0 and 1 name the default stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else \
+            torch.cuda.default_stream(device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)
+    return t
+
+
 @dataclass
 class LayerShape:
     hidden: int = 2048
@@ -883,6 +904,10 @@ class QuantRows:
         return cls(torch.empty((rows, width), dtype=torch.uint8, device=device),
                    torch.empty((rows, _groups(width)), dtype=torch.float32, device=device))
 
+    def record_stream(self, stream):
+        self.codes.record_stream(stream)
+        self.scales.record_stream(stream)
+
 
 class BlockWeights:
     """W [groups, out, in] (or [out, in]) as a block-FP8 checkpoint stores it: e4m3 codes
@@ -933,12 +958,19 @@ class ExpertOrder:
             return torch.empty(shape, dtype=torch.int32, device=device)
         return cls(ints(n_experts + 1), ints(tokens * top_k), ints(tokens, top_k))
 
+    def record_stream(self, stream):
+        for t in (self.starts, self.pair_of_slot, self.slot_of_pair):
+            t.record_stream(stream)
+
 
 class ExpertOps:
     """The layer's parts as operators, with their gradients, on one GPU: owns a context and
     its workspace (moe_ops_config in include/moe.h).  Rows are bf16 tensors [rows, width], or
     QuantRows; `out` may be given in either form, `quantize` asks for new QuantRows.  The
-    gradients are calls of their own: nothing here is recorded by torch.autograd."""
+    gradients are calls of their own: nothing here is recorded by torch.autograd.  A call runs on
+    `stream` (a torch.cuda.Stream or a handle), and what it returns is made there; None:
+    PyTorch's current stream.  The caller orders the streams, and holds the inputs until the
+    call has run."""
 
     def __init__(self, n_experts: int = 256, top_k: int = 8, max_rows: int = 1024,
                  max_width: int = 2048, device: int = 0, workspace_cap_bytes: int = 0):
@@ -992,11 +1024,13 @@ class ExpertOps:
         stride = self._rows2(t, what, rows, width)
         return ctypes.byref(moe_rows(t.data_ptr(), stride, None, None))
 
-    def _new(self, rows: int, width: int, quantize: bool = False):
+    def _new(self, rows: int, width: int, quantize: bool, stream):
+        """New rows for a call on `stream`."""
         dev = torch.device("cuda", self.device)
         if quantize:
-            return QuantRows.empty(rows, width, dev)
-        return torch.empty((rows, width), dtype=torch.bfloat16, device=dev)
+            return _made_on(self.device, stream, lambda: QuantRows.empty(rows, width, dev))
+        return _made_on(self.device, stream, lambda: torch.empty(
+            (rows, width), dtype=torch.bfloat16, device=dev))
 
     def _order(self, order: ExpertOrder):
         if not isinstance(order, ExpertOrder) or order.device != self.device or \
@@ -1029,16 +1063,19 @@ class ExpertOps:
                              f"CUDA device {self.device}")
         tokens = idx.shape[0]
         if order is None:
-            order = ExpertOrder.empty(self.n_experts, tokens, self.top_k, idx.device)
-            if tokens == 0:
-                order.starts.zero_()
+            def make():
+                o = ExpertOrder.empty(self.n_experts, tokens, self.top_k, idx.device)
+                if tokens == 0:
+                    o.starts.zero_()
+                return o
+            order = _made_on(self.device, stream, make)
         ref = self._order(order)
         if order.tokens != tokens:
             raise ValueError("the order is of another number of tokens")
         ptr, stride, width, form = None, 0, 0, None
         if x is not None:
             stride, width = self._rows2(x, "x", tokens), x.shape[1]
-            out = self._new(tokens * self.top_k, width, quantize) if out is None else out
+            out = self._new(tokens * self.top_k, width, quantize, stream) if out is None else out
             ptr, form = x.data_ptr(), self._form(out, "out", tokens * self.top_k, width)
         rc = self._lib.moe_dispatch(self.ctx, idx.data_ptr(), ptr, stride, width, ref, form,
                                     self._at(stream))
@@ -1051,7 +1088,7 @@ class ExpertOps:
         """The gradient of dispatch's x: each token's rows added up."""
         ref, width = self._order(order), drows.shape[-1]
         stride = self._rows2(drows, "drows", order.tokens * self.top_k)
-        out = self._new(order.tokens, width) if out is None else out
+        out = self._new(order.tokens, width, False, stream) if out is None else out
         rc = self._lib.moe_dispatch_grad(self.ctx, drows.data_ptr(), stride, ref, width,
                                          out.data_ptr(),
                                          self._rows2(out, "out", order.tokens, width),
@@ -1065,7 +1102,7 @@ class ExpertOps:
         """The experts' rows [tokens x top_k, width] back to tokens, by weights [tokens, top_k]."""
         ref, width = self._order(order), rows.shape[-1]
         stride = self._rows2(rows, "rows", order.tokens * self.top_k)
-        out = self._new(order.tokens, width) if out is None else out
+        out = self._new(order.tokens, width, False, stream) if out is None else out
         rc = self._lib.moe_combine(self.ctx, rows.data_ptr(), stride, ref,
                                    self._floats(weights, "weights", order.tokens), width,
                                    out.data_ptr(), self._rows2(out, "out", order.tokens, width),
@@ -1080,9 +1117,9 @@ class ExpertOps:
         """The gradients of combine: (drows, dweights)."""
         ref, width, pairs = self._order(order), rows.shape[-1], order.tokens * self.top_k
         stride = self._rows2(rows, "rows", pairs)
-        out = self._new(pairs, width, quantize) if out is None else out
+        out = self._new(pairs, width, quantize, stream) if out is None else out
         if dweights is None:
-            dweights = torch.empty_like(weights)
+            dweights = _made_on(self.device, stream, lambda: torch.empty_like(weights))
         rc = self._lib.moe_combine_grad(
             self.ctx, dy.data_ptr(), self._rows2(dy, "dy", order.tokens, width), rows.data_ptr(),
             stride, ref, self._floats(weights, "weights", order.tokens), width,
@@ -1103,7 +1140,7 @@ class ExpertOps:
                              f"device {self.device}")
         rows = x.shape[0]
         form = self._form(x, "the rows", rows, inner)
-        out = self._new(rows, outer) if out is None else out
+        out = self._new(rows, outer, False, stream) if out is None else out
         rc = call(self.ctx, form, w._ref, None if starts is None else starts.data_ptr(), rows,
                   out.data_ptr(), self._rows2(out, "out", rows, outer), self._at(stream))
         if rc:
@@ -1128,7 +1165,7 @@ class ExpertOps:
         rows, width = gate_up.shape[0], gate_up.shape[1] // 2
         if gate_up.shape[1] % 2:
             raise ValueError("gate_up holds as many gates as ups")
-        out = self._new(rows, width, quantize) if out is None else out
+        out = self._new(rows, width, quantize, stream) if out is None else out
         rc = self._lib.moe_swiglu(self.ctx, gate_up.data_ptr(), stride, rows, width,
                                   self._form(out, "out", rows, width), self._at(stream))
         if rc:
@@ -1140,7 +1177,7 @@ class ExpertOps:
         """The gradient of swiglu's gate_up."""
         stride = self._rows2(dh, "dh")
         rows, width = dh.shape
-        out = self._new(rows, 2 * width, quantize) if out is None else out
+        out = self._new(rows, 2 * width, quantize, stream) if out is None else out
         rc = self._lib.moe_swiglu_grad(self.ctx, dh.data_ptr(), stride, gate_up.data_ptr(),
                                        self._rows2(gate_up, "gate_up", rows, 2 * width), rows,
                                        width, self._form(out, "out", rows, 2 * width),
