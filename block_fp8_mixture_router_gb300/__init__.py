@@ -464,6 +464,13 @@ def _made_on(device: int, stream, make):
     return t
 
 
+def _contiguous_on(device: int, stream, t: torch.Tensor) -> torch.Tensor:
+    """t itself, or its contiguous copy for a call on `stream`, made there."""
+    if t.is_contiguous() or not t.is_cuda:
+        return t.contiguous()
+    return _made_on(device, stream, t.contiguous)
+
+
 @dataclass
 class LayerShape:
     hidden: int = 2048
@@ -507,7 +514,7 @@ class MoELayer:
     def load(self, layer: dict, stream=None):
         """Weights as torch tensors (see include/moe.h for names, dtypes, layouts)."""
         names = ("w13", "s13", "w2", "s2", "router", "ws13", "ws2", "shared_gate")
-        ts = [layer[n].contiguous() for n in names]
+        ts = [_contiguous_on(self.device, stream, layer[n]) for n in names]
         on_dev = {t.is_cuda for t in ts}
         if len(on_dev) != 1:
             raise ValueError("weights must be all on the device or all on the host")
@@ -516,15 +523,22 @@ class MoELayer:
                "moe_load_weights")
         self._keep = ts  # alive until the synchronous copy returned
 
+    def _like(self, x: torch.Tensor, stream) -> torch.Tensor:
+        return _made_on(self.device, stream, lambda: torch.empty_like(x))
+
+    def _new(self, shape, dtype, device, stream) -> torch.Tensor:
+        return _made_on(self.device, stream, lambda: torch.empty(shape, dtype=dtype,
+                                                                 device=device))
+
     def set_option(self, option: int, value: int):
         _check(moe_set_option(self.ctx, option, value), "moe_set_option")
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2:
             raise ValueError("x must be a 2-D bf16 CUDA tensor")
-        x = x.contiguous()
+        x = _contiguous_on(self.device, stream, x)
         if y is None:
-            y = torch.empty_like(x)
+            y = self._like(x, stream)
         _check(moe_forward(self.ctx, x, y, x.shape[0], stream), "moe_forward")
         return y
 
@@ -535,9 +549,9 @@ class MoELayer:
             if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("residual, x and gamma must be contiguous bf16 CUDA tensors")
         T, H = x.shape
-        h = torch.empty_like(x)
-        xn = torch.empty_like(x) if keep_xn else None
-        y = torch.empty_like(x)
+        h = self._like(x, stream)
+        xn = self._like(x, stream) if keep_xn else None
+        y = self._like(x, stream)
         _check(moe_forward_addnorm(self.ctx, residual, x, gamma, eps, T, h, xn, y, stream),
                "moe_forward_addnorm")
         return h, xn, y
@@ -555,16 +569,18 @@ class MoELayer:
 
     def route(self, x: torch.Tensor, stream=None):
         T = x.shape[0]
-        idx = torch.empty((T, self.shape.top_k), dtype=torch.int32, device=x.device)
-        w = torch.empty((T, self.shape.top_k), dtype=torch.float32, device=x.device)
-        _check(moe_route(self.ctx, x.contiguous(), T, idx, w, stream), "moe_route")
+        idx = self._new((T, self.shape.top_k), torch.int32, x.device, stream)
+        w = self._new((T, self.shape.top_k), torch.float32, x.device, stream)
+        x = _contiguous_on(self.device, stream, x)
+        _check(moe_route(self.ctx, x, T, idx, w, stream), "moe_route")
         return idx, w
 
     def quantize(self, x: torch.Tensor, stream=None):
         T, H = x.shape
-        codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
-        _check(moe_quantize(self.ctx, x.contiguous(), T, codes, scales, stream), "moe_quantize")
+        codes = self._new((T, H), torch.uint8, x.device, stream)
+        scales = self._new((T, H // 128), torch.float32, x.device, stream)
+        x = _contiguous_on(self.device, stream, x)
+        _check(moe_quantize(self.ctx, x, T, codes, scales, stream), "moe_quantize")
         return codes, scales
 
     def add_rmsnorm_quantize(self, residual: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor,
@@ -578,10 +594,10 @@ class MoELayer:
         T, H = x.shape
         if residual.shape != x.shape or gamma.shape != (H,):
             raise ValueError("residual and x must be [rows, H] and gamma [H]")
-        h_out = torch.empty_like(x) if h_out is None else h_out
-        xn_out = torch.empty_like(x) if xn_out is None else xn_out
-        codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
+        h_out = self._like(x, stream) if h_out is None else h_out
+        xn_out = self._like(x, stream) if xn_out is None else xn_out
+        codes = self._new((T, H), torch.uint8, x.device, stream)
+        scales = self._new((T, H // 128), torch.float32, x.device, stream)
         _check(moe_add_rmsnorm_quantize(self.ctx, residual, x, gamma, eps, T, h_out, xn_out,
                                         codes, scales, stream), "moe_add_rmsnorm_quantize")
         return h_out, xn_out, codes, scales
@@ -589,8 +605,8 @@ class MoELayer:
     def expert_activations(self, rows: int, stream=None):
         k, I = self.shape.top_k, self.shape.inter
         dev = torch.device("cuda", self.device)
-        hq = torch.empty((rows, k, I), dtype=torch.uint8, device=dev)
-        sh = torch.empty((rows, k, I // 128), dtype=torch.float32, device=dev)
+        hq = self._new((rows, k, I), torch.uint8, dev, stream)
+        sh = self._new((rows, k, I // 128), torch.float32, dev, stream)
         _check(moe_expert_activations(self.ctx, rows, hq, sh, stream), "moe_expert_activations")
         return hq, sh
 
@@ -599,8 +615,8 @@ class MoELayer:
         recent forward read: ([rows, k, H] uint8, [rows, k, H/128] fp32)."""
         k, H = self.shape.top_k, self.shape.hidden
         dev = torch.device("cuda", self.device)
-        codes = torch.empty((rows, k, H), dtype=torch.uint8, device=dev)
-        scales = torch.empty((rows, k, H // 128), dtype=torch.float32, device=dev)
+        codes = self._new((rows, k, H), torch.uint8, dev, stream)
+        scales = self._new((rows, k, H // 128), torch.float32, dev, stream)
         _check(moe_forward_codes(self.ctx, rows, codes, scales, stream), "moe_forward_codes")
         return codes, scales
 
@@ -638,10 +654,11 @@ class MoEChain:
         """x [rows, H] bf16 -> every layer's output [n_layers, rows, H]."""
         if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2:
             raise ValueError("x must be a 2-D bf16 CUDA tensor")
-        x = x.contiguous()
+        device = x.get_device()
+        x = _contiguous_on(device, stream, x)
         if y_all is None:
-            y_all = torch.empty((len(self.layers),) + tuple(x.shape), dtype=x.dtype,
-                                device=x.device)
+            y_all = _made_on(device, stream, lambda: torch.empty(
+                (len(self.layers),) + tuple(x.shape), dtype=x.dtype, device=x.device))
         _check(moe_chain_forward(self.chain, x, y_all, x.shape[0], stream), "moe_chain_forward")
         return y_all
 
@@ -798,9 +815,9 @@ class Attention:
                              f"{self.device}")
         return g.data_ptr()
 
-    def _out(self, like, rows):
-        return torch.empty((rows, self.shape.q_heads, self.shape.head_dim), dtype=torch.bfloat16,
-                           device=like.device)
+    def _out(self, like, rows, heads, stream):
+        return _made_on(self.device, stream, lambda: torch.empty(
+            (rows, heads, self.shape.head_dim), dtype=torch.bfloat16, device=like.device))
 
     def rope(self, x: torch.Tensor, positions: torch.Tensor, gamma: torch.Tensor | None = None,
              eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -815,7 +832,7 @@ class Attention:
             raise ValueError(f"positions must be a contiguous int32 tensor [rows] of CUDA device "
                              f"{self.device}")
         if out is None:
-            out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=x.device)
+            out = self._out(x, rows, heads, stream)
         rc = self._lib.moe_rope(self.ctx, x.data_ptr(), xs, heads, positions.data_ptr(),
                                 self._gamma(gamma), eps, rows, out.data_ptr(),
                                 _rows3(out, rows, heads, dim, "out", self.device), self._at(stream))
@@ -842,7 +859,7 @@ class Attention:
         s, n = self.shape, batch.rows
         qs = _rows3(q, n, s.q_heads, s.head_dim, "q", self.device)
         if out is None:
-            out = self._out(q, n)
+            out = self._out(q, n, s.q_heads, stream)
         self._cache_ok(cache, batch)
         rc = self._lib.moe_attn_forward(self.ctx, cache._ref, q.data_ptr(), qs, batch._ref,
                                         out.data_ptr(),
@@ -860,7 +877,7 @@ class Attention:
         s, n = self.shape, batch.rows
         xs = _rows3(qkv, n, s.q_heads + 2 * s.kv_heads, s.head_dim, "qkv", self.device)
         if out is None:
-            out = self._out(qkv, n)
+            out = self._out(qkv, n, s.q_heads, stream)
         self._cache_ok(cache, batch)
         rc = self._lib.moe_attn_step(self.ctx, cache._ref, qkv.data_ptr(), xs,
                                      self._gamma(q_gamma), self._gamma(k_gamma), eps, batch._ref,
