@@ -104,21 +104,32 @@ __global__ void __launch_bounds__(kThreads, 4) k_swiglu_grad(const bf16* dh, int
   }
 }
 
-// Codes at other widths (multiples of 16): one group of the output's 2 x width columns at a
-// time; the group on the border holds gradients of gates and of ups.
+// Columns a .. a + 7 and b .. b + 7 of a row.
+__device__ __forceinline__ Vec16 load8_8(const bf16* row, int a, int b, bool on) {
+  Vec16 v = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (on) {
+    v.a = *reinterpret_cast<const uint4*>(row + a);
+    v.b = *reinterpret_cast<const uint4*>(row + b);
+  }
+  return v;
+}
+
+// Codes at other widths (multiples of 8): one group of the output's 2 x width columns at a
+// time; the group on the border holds gradients of gates and of ups, and so may a lane's two
+// vectors of 8.
 __global__ void __launch_bounds__(kThreads, 4) k_swiglu_grad_mixed(const bf16* dh, int64_t dh_stride,
                                                                 const bf16* gu, int64_t gu_stride,
                                                                 int rows, int width, RowsOut out) {
   const Unit u = unit_of(blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3), rows, groups_of(2 * width));
-  const bool up = u.c >= width, on = u.on && u.c < 2 * width;
-  const int c = up ? u.c - width : u.c;
+  const bool on = u.on && u.c < 2 * width, up0 = u.c >= width, up1 = u.c + 8 >= width;
+  const int a = up0 ? u.c - width : u.c, b = up1 ? u.c + 8 - width : u.c + 8;
   const bf16* row = gu + (int64_t)u.row * gu_stride;
-  const Vec16 rd = load16(dh + (int64_t)u.row * dh_stride, c, width, on);
-  const Vec16 rg = load16(row, c, width, on), ru = load16(row + width, c, width, on);
+  const Vec16 rd = load8_8(dh + (int64_t)u.row * dh_stride, a, b, on);
+  const Vec16 rg = load8_8(row, a, b, on), ru = load8_8(row + width, a, b, on);
   float dg[16], du[16];
   swiglu_back(rd, rg, ru, dg, du);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dg[i] = up ? du[i] : dg[i];
+  for (int i = 0; i < 16; ++i) dg[i] = (i < 8 ? up0 : up1) ? du[i] : dg[i];
   put16<true, false>(out, u.row, u.c, 2 * width, u.on, dg);
 }
 

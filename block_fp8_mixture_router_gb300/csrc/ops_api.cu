@@ -389,8 +389,9 @@ int moe_swiglu_grad(moe_ops* ctx, const void* dh, int64_t dh_stride, const void*
   if (!ctx || rows < 0) return MOE_ERR_INVALID_ARG;
   if (rows > ctx->cfg.max_rows * ctx->cfg.top_k) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
+  // (2 width is a multiple of 16, as codes want it, where width is one of 8)
   if (width < 1 || width > kMaxWidth || !form_ok(dgate_up, 2 * width) ||
-      !width_ok(width, dgate_up->codes != nullptr) || !rows_ok(dh, dh_stride, width) ||
+      !width_ok(width, false) || !rows_ok(dh, dh_stride, width) ||
       !rows_ok(gate_up, gate_up_stride, 2 * (int64_t)width) ||
       overlaps(gate_up, gate_up_stride, 2 * width, rows, dgate_up, 2 * width, rows) ||
       overlaps(dh, dh_stride, width, rows, dgate_up, 2 * width, rows))
