@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
       for (int i = 0; i < kHalf; ++i) acc[i] = 0.0f;
 #pragma unroll 1
       for (int b = 0; b < blocks; ++b, ++n) {
-        // (a wait that gave up is seen behind the loop, which then ends at once; lanes and
+        // (a wait that gave up has set the abort flag, which is seen behind the loop; lanes and
         // columns without outputs add up what is there, and drop it)
         const uint32_t tb = n & 1u;
         tc::wait_bounded(&sm.tfull[tb], (n >> 1) & 1u, &sm.abort, a.status);
@@ -485,6 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
         if (lane == 0) tc::mbar_arrive(&sm.tempty[tb]);
         add_scaled(acc + 96, v1, s);
       }
+      // sums of a tile with a wait that gave up, any warp's, are not handed on
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sm.abort))) break;
       // the warp's piece, once the tile before has left it
       if (!wait_all(&sm.ofree[warp], (j & 1) ^ 1u, sm, a.status)) break;
       stage_piece(piece, acc);
