@@ -700,7 +700,18 @@ class AttnShape:
             max_seqs, workspace_cap_bytes)
 
 
-class KVCache:
+class _Described:
+    """Tensors with the C struct that describes them, made together: the struct holds their
+    addresses and sizes, so that another tensor put into an attribute would not be seen."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{name}: a {type(self).__name__} keeps what it was made of; "
+                                 "make another one")
+        object.__setattr__(self, name, value)
+
+
+class KVCache(_Described):
     """One layer's paged cache: e4m3 codes [pages][kv_heads][page_tokens][head_dim]
     (uint8) and fp32 scales [pages][kv_heads], for keys and for values."""
 
@@ -734,7 +745,7 @@ class KVCache:
         return cls(codes(), codes(), scales(), scales())
 
 
-class AttnBatch:
+class AttnBatch(_Described):
     """The rows of one call (moe_attn_batch): int32 CUDA tensors row_start
     [n_seqs + 1], kv_len [n_seqs] (with this call's rows) and pages [n_seqs][most pages].
     Their contents may change from call to call (a captured graph replays with new
@@ -898,7 +909,7 @@ def _groups(width: int) -> int:
     return -(-width // 128)
 
 
-class QuantRows:
+class QuantRows(_Described):
     """Rows in 8 bits: e4m3 codes [rows, width] (uint8) and a fp32 scale for each 128 values
     of a row [rows, ceil(width / 128)], as MoELayer.quantize and add_rmsnorm_quantize return
     them."""
@@ -926,7 +937,7 @@ class QuantRows:
         self.scales.record_stream(stream)
 
 
-class BlockWeights:
+class BlockWeights(_Described):
     """W [groups, out, in] (or [out, in]) as a block-FP8 checkpoint stores it: e4m3 codes
     (uint8) and a fp32 scale per 128 x 128 block."""
 
@@ -948,7 +959,7 @@ class BlockWeights:
         self._ref = ctypes.byref(self._c)
 
 
-class ExpertOrder:
+class ExpertOrder(_Described):
     """Rows sorted by expert (moe_order in include/moe.h): int32 starts [n_experts + 1],
     pair_of_slot [tokens x top_k] and slot_of_pair [tokens, top_k]."""
 
