@@ -623,8 +623,10 @@ void moe_attn_destroy(moe_attn* ctx);
  * infinity or NaN makes every result that takes it NaN.  In a gradient, quantising counts as
  * the identity.
  *
- * A call reads and writes the rows it names and no others.  Arrays of one call share no
- * byte (MOE_ERR_INVALID_ARG where the library sees it: rows read and rows written). */
+ * A call writes the rows it names and no others, and no result depends on others: rows
+ * behind an order's last, or of no group, may hold anything (moe_linear may read them, within
+ * its `rows`).  Arrays of one call share no byte (MOE_ERR_INVALID_ARG where the library sees
+ * it: rows read and rows written). */
 typedef struct {
   int n_experts;  /* 1..256 */
   int top_k;      /* 1..16: pairs of a token; need not be distinct experts */
@@ -634,10 +636,10 @@ typedef struct {
   size_t workspace_cap_bytes; /* 0 = no cap */
 } moe_ops_config;
 
-/* Rows in one of the two forms, device memory of the caller, at most 131072 wide: `values` (codes and scales
- * NULL), bf16, 16-byte aligned, row stride in values a multiple of 8 and at least the width,
- * the width a multiple of 8; or `codes` [rows][width], 16-byte aligned, and `scales`
- * [rows][ceil(width / 128)] (values NULL), the width a multiple of 16. */
+/* Rows in one of the two forms, device memory of the caller, at most 131072 wide: `values`
+ * (codes and scales NULL), bf16, 16-byte aligned, row stride in values a multiple of 8 and at
+ * least the width, the width a multiple of 8; or `codes` [rows][width], 16-byte aligned, and
+ * `scales` [rows][ceil(width / 128)] (values NULL), the width a multiple of 16. */
 typedef struct {
   void* values;
   int64_t stride;
