@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear(const __grid_constant__ 
   LinSmem& sm = *reinterpret_cast<LinSmem*>(pieces + kSumWarps * kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (tc::smem_u32(stages) & 1023u) {  // the same for every CTA
-    if (threadIdx.x == 0) atomicOr(a.status, kOpsTimeout);
+    if (threadIdx.x == 0) atomicOr(a.status, kOpsBadBase);
     return;
   }
   if (threadIdx.x == 0) {

@@ -292,6 +292,7 @@ int moe_ops_last_device_status(moe_ops* ctx) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
+  if (v & kOpsBadBase) return MOE_ERR_CUDA;
   if (v & kOpsTimeout) return MOE_ERR_DEVICE_TIMEOUT;
   return v & kOpsBadOrder ? MOE_ERR_INVALID_ARG : MOE_OK;
 }

@@ -9,6 +9,7 @@ namespace moe {
 // Device status word bits.
 constexpr int kOpsTimeout = 1;
 constexpr int kOpsBadOrder = 2;
+constexpr int kOpsBadBase = 4;  // shared memory that does not begin where the tiles need it
 
 // Rows a kernel writes: bf16, or e4m3 codes with a scale for each 128 values.
 struct RowsOut {
