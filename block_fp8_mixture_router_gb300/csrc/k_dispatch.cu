@@ -9,8 +9,8 @@
 //
 // The rows' bytes bound all of it (a row moves once each way); the sort is a few
 // microseconds in front.  No atomics order anything: a pair's slot follows from counts.
-//   16384 tokens of 2048, eight experts of 256 each:  99 us, 92 % of the copy's rate (the
-//     gather 89; the order alone 7 us)
+//   16384 tokens of 2048, eight experts of 256 each:  98 us, 93 % of the copy's rate (the
+//   gather 89; the order alone 7 us);  to codes 61 us (85 %)
 //   11 tokens to codes 3.4 us, one launch;  weighted back: 16384 tokens 91 us (100 %), one 2.6
 //   the gather's gradient, 5003 tokens of 2560, four of six pairs each: 24 us (79 %)
 #include "rows_device.cuh"
@@ -271,7 +271,7 @@ __device__ __forceinline__ int slot_of(const OrderArgs& o, int p, int* status) {
 
 // A block takes up to 256 vectors of 8 columns of a token, a thread one of them: its rows'
 // loads go out together, four rows at a time, and the products are added in rank order.
-// (16384 tokens of eight rows of 2048: 92 us, the bytes' floor 90; with eight rows at a time
+// (16384 tokens of eight rows of 2048: 91 us, the bytes' floor 90; with eight rows at a time
 // and four blocks to an SM 98, without a bound on registers 125.)
 __global__ void __launch_bounds__(kBackThreads, 6) k_combine(OrderArgs o, const bf16* rows,
                                                              int64_t rows_stride, const float* w,
@@ -308,8 +308,9 @@ __global__ void __launch_bounds__(kBackThreads, 6) k_combine(OrderArgs o, const 
 }
 
 // A warp takes a pair: the dot product of dy with its row, and the row's gradient.  4099 tokens
-// of eight rows of 2048 to codes: 45 us, 73 % of the copy's rate; the quotients keep the
-// schedulers busy in two thirds of the cycles.  (Five blocks to an SM; 60 us without a bound on
+// of eight rows of 2048 in bf16: 44 us, 96 % of the copy's rate; to codes 45 us, 73 %: the
+// quotients keep the schedulers busy in two thirds of the cycles, and the next columns are
+// asked for behind them.  (Five blocks to an SM; 60 us without a bound on
 // registers; a block to a token, with dy and its groups' magnitudes kept for all of its pairs,
 // 52.)
 template <bool kCodes>

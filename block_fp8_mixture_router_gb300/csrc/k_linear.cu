@@ -16,16 +16,16 @@
 // buffers while the warps empty the other: copy 32 columns to registers, multiply the 32 in
 // front of them, and give the buffer back before the last 32 are multiplied.
 //
-// 16384 rows x 2048 x 4096 take 110 us, 2.5 PFLOP/s, and the gradient of 131072 rows of 256
-// experts of 1024 x 2048 305 us (1.8 PFLOP/s, 3.8 TB/s).  About 900 cycles a block: the
+// 16384 rows x 2048 x 4096 take 109 us, 2.5 PFLOP/s, and the gradient of 131072 rows of 256
+// experts of 1024 x 2048 308 us (1.8 PFLOP/s, 3.8 TB/s).  About 900 cycles a block: the
 // buffers' exchange (a block's MMAs with their issue and commit take 800 to be seen done,
 // its products 400 to be read and 70 to be given back) and the 768 that 48 KB of a block take
 // at the 64 bytes a clock that an SM gets from L2 bind it together.  Without the FMAs it is no
 // faster, with two thirds of the bytes 3 %, with a quarter of the MMAs 10 %, without all
 // three 16 %.  Measured and not kept: pairs of CTAs that share their columns' weights
-// (cta_group::2, 256 x 256): 113 us, and 126 instead of 96 for 1024 tokens' rows of 256
-// experts; four buffers of 128 columns: 163 us; clusters that share a tile's contraction where
-// tiles are few: 100 rows x 2048 x 2560 13.4 us and more against 12.4.
+// (cta_group::2, 256 x 256): no faster (113 us both ways then), and 126 instead of 96 for 1024
+// tokens' rows of 256 experts; four buffers of 128 columns: 163 us; clusters that share a
+// tile's contraction where tiles are few: 100 rows x 2048 x 2560 13.4 us and more against 12.4.
 //
 // Warps: 0-7 the sums (warp w: lanes 32 (w % 4) and on, columns 128 (w / 4) and on), 8 the TMA
 // loads, 9 and 10 the MMAs, 11 the scales, 12-15 the stores.  Persistent: a CTA takes tiles

@@ -5,8 +5,9 @@
 //
 // Every value is read and written once, so HBM bounds them, and the quotients behind codes
 // nearly do: 131072 rows of 512 to codes 58 us (87 % of the copy's rate; the schedulers issue
-// in 78 % of cycles), the gradient of 10493 rows of 1408 in bf16 23 us (96 %), 131072 rows of
-// 1024 quantised 68 us (88 %).  Eight lanes take a group of 128 columns, 16 values each: the
+// in 75 % of cycles), the gradient of 10493 rows of 1408 in bf16 23 us (96 %), of 131072 rows
+// of 512 to codes 98 us (83 %; of 528, where groups straddle gates and ups and every operand
+// is read twice, 158: 53 %), 131072 rows of 1024 quantised 68 us (88 %).  Eight lanes take a group of 128 columns, 16 values each: the
 // group's largest is then three shuffles away and a lane's loads and stores are 16-byte
 // vectors.  Blocks to an SM as measured: six for what has few values in flight (62 us with
 // four for the first), four for the gradient (27 us with six).

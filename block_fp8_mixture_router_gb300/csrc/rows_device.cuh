@@ -73,7 +73,7 @@ __device__ __forceinline__ float div_by(float v, float s, float y) {
 // Codes of kN x 16 values of a group whose largest magnitude is m: quant4's codes, without its
 // test of every value for a quotient that the product leaves open.  Quotients of bf16 values
 // often lie on e4m3's midpoints, where that test sends whole warps to the long division
-// (134 M values: 160 us that way, 77 this).  kBf16: the values and m are bf16's.  Returns the
+// (134 M values: 160 us that way, 68 this).  kBf16: the values and m are bf16's.  Returns the
 // group's scale.
 template <int kN, bool kBf16>
 __device__ __forceinline__ float quant_codes(const float (&v)[kN][16], float m, uint4 (&code)[kN]) {
