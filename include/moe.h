@@ -767,7 +767,10 @@ int moe_swiglu_grad(moe_ops* ctx, const void* dh, int64_t dh_stride, const void*
 
 /* Device-side status of the context: MOE_OK; MOE_ERR_INVALID_ARG if a call's starts were not
  * ascending within its rows or a slot lay outside them; MOE_ERR_DEVICE_TIMEOUT if a bounded
- * wait gave up (rows of that call's output may then be left as they were).  Synchronises the context's last stream and clears the flag.
+ * wait gave up (rows of that call's output may then be left as they were); MOE_ERR_CUDA if a
+ * kernel could not run as it was launched.  Synchronises the stream of the context's last call,
+ * which must still exist, and clears the flag; the replay of a graph on another stream is the
+ * caller's to wait for.
  * Defined by: PR #939 "drama3: Fish Audio Drama 3 text to speech on one CUDA
  * GPU", conversation, the follow-up fixes (a bad value is refused by name with
  * an error, not trapped on). */

@@ -94,3 +94,27 @@ def test_the_parts_on_a_stream_given_by_hand(dev, side):
     torch.cuda.current_stream().wait_stream(s)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert ops.device_status() == m.MOE_OK
+
+
+def test_a_branch_of_a_captured_graph(dev, side):
+    """A stream given by hand that the capture has forked to: replayed with other rows."""
+    s, given = side
+    ops = m.ExpertOps(1, 1, 512, 0)
+    gu = torch.randn((512, 2048), device=dev).bfloat16()
+    dh = torch.randn((512, 1024), device=dev).bfloat16()
+    ops.swiglu(gu, stream=given)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        y = ops.swiglu(gu, stream=given)
+        d = ops.swiglu_grad(dh, gu, quantize=True, stream=given)
+        torch.cuda.current_stream().wait_stream(s)
+        z = y + 1
+    for seed in range(3):
+        torch.manual_seed(seed)
+        gu.copy_(torch.randn(gu.shape, device=dev))
+        graph.replay()
+        want, dwant = ops.swiglu(gu), ops.swiglu_grad(dh, gu, quantize=True)
+        assert torch.equal(y, want) and torch.equal(z, want + 1)
+        assert torch.equal(d.codes, dwant.codes) and torch.equal(d.scales, dwant.scales)
