@@ -749,7 +749,8 @@ int moe_linear_grad(moe_ops* ctx, const moe_rows* dy, const moe_block_weights* w
 /* h = gate s up in fp32, s = 1 / (1 + e^-gate): gate_up bf16 [rows][2 width], the gates in
  * front of the ups as a product with moe_weights' w13 leaves them; h [rows][width], rounded
  * to bf16 or quantised once.  s is held in fp32 at any gate: below about -104 it is 0, and h
- * with it.  A gate of -infinity makes h NaN.  rows <= max_rows x top_k, width <= 65536.  Asynchronous.
+ * with it.  A gate of -infinity makes h NaN.  rows <= max_rows x top_k, width <= 65536.
+ * Asynchronous.
  * Defined by: commit "one SwiGLU launch for the routed and shared experts" (routed rows are
  * stored as their FP8 quantization). */
 int moe_swiglu(moe_ops* ctx, const void* gate_up, int64_t gate_up_stride, int rows, int width,
